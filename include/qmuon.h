@@ -1,7 +1,8 @@
 /*
  * qmuon.h -- C ABI of libqmuon.so: one Muon optimizer step on an AMD MI355X
  * (gfx950), as a blockwise-int8 momentum update followed by quintic
- * Newton-Schulz orthogonalisation.
+ * Newton-Schulz orthogonalisation; next to it the AdamW step of the
+ * parameters Muon does not fit and the global gradient norm.
  *
  * Conventions shared by every entry point
  *   - Pointers are device pointers unless a parameter says "host".
@@ -466,6 +467,140 @@ QM_API qm_status grasp_step(const qm_grasp_state *state, int64_t rows,
                             float c, float eps, int32_t ns_precision,
                             float *weight, float lr, float weight_decay,
                             void *ws, size_t ws_bytes, qm_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Global gradient norm and clipping
+ *
+ * Over the grads of a whole model (those Muon steps and those AdamW steps):
+ *   S = sum of g*g over every element (fp64);  norm = sqrt(S);
+ *   coef = min(1, max_norm / (norm + eps)),  NaN if S is not finite.
+ * coef stays on the device: adamw_step multiplies it into the gradients it
+ * reads, grad_scale into gradients in place (those of the Muon step).
+ * ---------------------------------------------------------------------- */
+typedef struct {
+    void *grad;         /* dtype, aligned to its element                     */
+    int64_t numel;      /* >= 0                                              */
+    int64_t cols, ld;   /* cols = 0: contiguous; else rows of cols elements
+                           (a divisor of numel) at pitch ld >= cols; numel
+                           < 2^32 then                                       */
+    int32_t dtype;      /* qm_dtype                                          */
+    int32_t reserved;   /* must be 0                                         */
+} qm_grad_tensor;
+
+/* Build a grad-list blob (host only; touches no GPU), used like a norm plan:
+ * the caller copies it verbatim to the device once (64-byte aligned) and
+ * passes both copies.  host_blob == NULL asks for the size, as in
+ * qm_plan_encode.  Errors: QM_E_ARG (null, counts, overlapping buffers),
+ * QM_E_ALIGN, QM_E_DTYPE, QM_E_SHAPE, QM_E_UNSUPPORTED. */
+QM_API qm_status qm_grad_plan_encode(const qm_grad_tensor *grads, int32_t n_grads,
+                                     void *host_blob, size_t *inout_blob_bytes);
+
+/* Workspace bytes of grad_norm for this blob (0 if it is not a grad list). */
+QM_API size_t grad_norm_workspace_bytes(const void *host_plan);
+
+/* norm_out[0], coef_out[0]: device fp32 out, as defined above (max_norm > 0,
+ * infinity allowed: coef is then 1; eps >= 0).  Fixed summation order, no
+ * atomics.  ws: >= grad_norm_workspace_bytes, 8-byte aligned.
+ * Errors: QM_E_ARG, QM_E_PLAN, QM_E_ALIGN, QM_E_WORKSPACE, QM_E_HIP. */
+QM_API qm_status grad_norm(const void *host_plan, const void *dev_plan,
+                           double max_norm, double eps, float *norm_out,
+                           float *coef_out, void *ws, size_t ws_bytes,
+                           qm_stream_t stream);
+
+/* Every grad of the list times coef[0] (device fp32), rounded to nearest
+ * even into its dtype; a NaN coef leaves the grads as they are.
+ * Errors: QM_E_ARG, QM_E_PLAN, QM_E_ALIGN, QM_E_HIP. */
+QM_API qm_status grad_scale(const void *host_plan, const void *dev_plan,
+                            const float *coef, qm_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * AdamW over many tensors ("Decoupled Weight Decay Regularization",
+ * Loshchilov and Hutter, ICLR 2019), for the parameters a Muon step does not
+ * fit: embeddings, heads, norm gains, biases.  Per element, with t the step,
+ * g the gradient (times *grad_scale if given), lr_t = lr * lr_scale:
+ *   m <- beta1 m + (1 - beta1) g;   v <- beta2 v + (1 - beta2) g g;
+ *   w <- w - lr_t weight_decay w
+ *          - lr_t (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ * in fp32, the new w rounded to nearest even into its dtype, and into `copy`
+ * if given (the low-precision weight a model computes with next to its fp32
+ * weight).  Grads are only read.
+ *
+ * States in 32 bits: m and v are fp32.  States in 8 bits, per 256-element
+ * block (the last block of a tensor covers the remainder):
+ *   m = m_code * (m_absmax / 127),         m_code int8 in [-127, 127];
+ *   v = v_code^2 * (v_absmax / 65025),     v_code uint8 (65025 = 255^2).
+ * v_code is proportional to sqrt(v), the number the update divides by: a
+ * block spans a factor of 255 in it, and decoding needs no root.  The weight
+ * sees the new m and v before they are coded.  Coding, in binary32 with one
+ * rounding per operation: step_m = beta1 (m_absmax / 127), step_v = beta2
+ * (v_absmax / 65025), m = m_code step_m + (1 - beta1) g, v = (v_code v_code)
+ * step_v + (1 - beta2) (g g); m_absmax' = max|m|, v_absmax' = max v over the
+ * block (0 if below 2^-100: the block then holds zeros);
+ *   x = m (127 / m_absmax'),   m_code' = x rounded to nearest even;
+ *   y = v (65025 / v_absmax'), k = floor(sqrt(y)), v_code' = k + 1 if
+ *   y - k^2 > k + 1/2, else k (the code whose square is nearest), and at
+ *   least 1 where v > 0, so that no update is divided by eps alone.
+ * A block whose maximum is not finite gets codes 0 and that maximum (a NaN
+ * counts as the largest), and decodes to NaN from then on.
+ *
+ * Nearest rounding holds an 8-bit v still once its change per step is less
+ * than half a code's, which with beta2 near 1 is soon the case; stochastic
+ * rounding keeps the mean: with r the element's random word (the counter and
+ * key of qm_rounding, the tensor's index in this list), m_code' =
+ * floor(x) + 1 if (r >> 16) 2^-16 < x - floor(x), else floor(x); v_code' =
+ * k + 1 if y - k^2 > (r mod 2^15) 2^-15 (2k + 1), else k: the mean of the
+ * code's square is y.  Clamped to the codes' ranges.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+    void *weight;        /* weight_dtype [numel], in/out                     */
+    const void *grad;    /* grad_dtype                                       */
+    void *m, *v;         /* [numel] fp32 (state_bits 32), or int8 and uint8
+                            codes (state_bits 8), in/out                     */
+    float *m_absmax;     /* state_bits 8: [ceil(numel/256)], in/out; else
+                            null                                             */
+    float *v_absmax;     /* the same                                         */
+    void *copy;          /* nullable: copy_dtype [numel], out                */
+    int64_t numel;       /* >= 0                                             */
+    int64_t grad_cols, grad_ld;  /* as cols, ld of qm_grad_tensor            */
+    int32_t weight_dtype, grad_dtype;   /* qm_dtype                          */
+    int32_t copy_dtype;  /* QM_BF16 or QM_F16; ignored without copy          */
+    int32_t state_bits;  /* 32 or 8                                          */
+    float lr_scale;      /* finite                                           */
+    float weight_decay;  /* finite                                           */
+} qm_adamw_tensor;
+
+typedef struct {
+    double lr, beta1, beta2, eps;  /* 0 <= beta < 1, eps > 0                 */
+    int64_t step;        /* t, 1-based                                       */
+    int32_t rounding;    /* qm_rounding of 8-bit states                      */
+    uint32_t offset;     /* counter word 2 of stochastic rounding            */
+    uint64_t seed;       /* its key                                          */
+} qm_adamw_hparams;
+
+/* Build an AdamW list blob (host only); use as qm_grad_plan_encode's.  All
+ * buffers aligned to their elements, none overlapping another. */
+QM_API qm_status qm_adamw_plan_encode(const qm_adamw_tensor *tensors, int32_t n_tensors,
+                                      void *host_blob, size_t *inout_blob_bytes);
+
+/* Blocks of all tensors of a grad or AdamW list, in list order (tensor t's
+ * first block is the sum of ceil(numel / 256) over the tensors before it);
+ * -1 if the blob is neither. */
+QM_API int64_t qm_list_blocks(const void *host_plan);
+
+/* One AdamW step over every tensor of the list.  grad_scale: nullable device
+ * fp32 [1]; if it is NaN (a gradient norm that is not finite) nothing is
+ * written.  Errors: QM_E_ARG, QM_E_ALIGN, QM_E_PLAN, QM_E_HIP. */
+QM_API qm_status adamw_step(const void *host_plan, const void *dev_plan,
+                            const qm_adamw_hparams *hp, const float *grad_scale,
+                            qm_stream_t stream);
+
+/* The values the states stand for, e.g. for a checkpoint that does not
+ * depend on the state's form: element e of tensor t goes to m_out and v_out
+ * [256 * (t's first block) + e] (fp32 [256 * qm_list_blocks], 16-byte
+ * aligned); what lies between two tensors is set to 0.
+ * Errors: QM_E_ARG, QM_E_ALIGN, QM_E_PLAN, QM_E_HIP. */
+QM_API qm_status adamw_read_state(const void *host_plan, const void *dev_plan,
+                                  float *m_out, float *v_out, qm_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Launch timing (measurement aid, off by default).

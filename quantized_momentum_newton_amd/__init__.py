@@ -20,6 +20,9 @@ Entry points (same names as the C ABI in include/qmuon.h):
   muon_step                        update + NS + weight apply, block-periodic
   muon_apply                       the NS + weight-apply half of muon_step
   GraspState, grasp_step           the GRASP 4-bit momentum variant
+  GradPlan, grad_norm, grad_scale  global gradient norm, clip factor, clipping in place
+  AdamWState, AdamWPlan, adamw_step, adamw_read_state
+                                   AdamW over many tensors, states in 32 or 8 bits
   timing_enable, timing_read       per-kernel-class launch timing (HIP events)
 """
 import ctypes
@@ -447,3 +450,194 @@ def grasp_step(state, grad, warm, mu=0.95, ns_steps=5, coeffs=QUINTIC, eps=1e-7,
                            _dtype(grad), _ptr(warm), mu, ns_steps, a, b, c, eps, PRECISION[ns_precision],
                            _ptr(weight), lr,
                            weight_decay, _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def _encode_list(encode, arr, n):
+    """A list blob built by `encode`: (host bytes, their size)."""
+    size = ctypes.c_size_t(0)
+    _check(encode(arr, n, None, ctypes.byref(size)))
+    host = torch.empty(size.value, dtype=torch.uint8)
+    _check(encode(arr, n, ctypes.c_void_p(host.data_ptr()), ctypes.byref(size)))
+    return host
+
+
+def _grad_view(t, name):
+    """(cols, ld) of a gradient: (0, 0) if contiguous, else those of a 2-D view."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.is_contiguous():
+        return 0, 0
+    if t.dim() != 2 or t.stride(1) != 1 or t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}: a non-contiguous grad must be 2-D with unit column stride and rows that do not overlap")
+    return t.shape[1], t.stride(0)
+
+
+class _ListPlan:
+    """A tensor list encoded once and copied to the device once."""
+
+    def _finish(self, host, device, numels):
+        self.host, self.device = host, device
+        self.dev = host.to(device)
+        self.hptr, self.dptr = ctypes.c_void_p(host.data_ptr()), ctypes.c_void_p(self.dev.data_ptr())
+        self.numels = numels
+        self.n_blocks = _LIB.qm_list_blocks(self.hptr)
+        # index of each tensor's first 256-element block (list order)
+        self.block_offsets, at = [], 0
+        for n in numels:
+            self.block_offsets.append(at)
+            at += -(-n // BLOCK)
+
+
+class GradPlan(_ListPlan):
+    """The gradients of a model, for their global norm.
+
+    grads: list of fp32 / bf16 / f16 device tensors, each contiguous or a 2-D
+           view with unit column stride; none overlaps another."""
+
+    def __init__(self, grads, device=None):
+        if not grads:
+            raise ValueError("no grads")
+        dev = device if device is not None else grads[0].device
+        arr = (L.GradTensor * len(grads))()
+        for i, g in enumerate(grads):
+            cols, ld = _grad_view(g, f"grad {i}")
+            if g.device != grads[0].device:
+                raise ValueError(f"grad {i} is on {g.device}, expected {grads[0].device}")
+            arr[i] = L.GradTensor(g.data_ptr(), g.numel(), cols, ld, _dtype(g), 0)
+        self._keep = list(grads)
+        self._finish(_encode_list(_LIB.qm_grad_plan_encode, arr, len(grads)), dev, [g.numel() for g in grads])
+
+    def workspace_bytes(self):
+        return _LIB.grad_norm_workspace_bytes(self.hptr)
+
+    def workspace(self):
+        return torch.empty(self.workspace_bytes(), dtype=torch.uint8, device=self.device)
+
+
+def _scalar(t, name, device):
+    if t is None:
+        return torch.empty(1, dtype=torch.float32, device=device)
+    _require(t, name, torch.float32, device, numel=1)
+    return t
+
+
+def grad_norm(plan, max_norm=float("inf"), eps=1e-6, norm=None, coef=None, ws=None, stream=None):
+    """Norm of all gradients of the plan and min(1, max_norm / (norm + eps)),
+    NaN where the norm is not finite, as device fp32 [1] tensors (given or
+    new): (norm, coef)."""
+    norm, coef = _scalar(norm, "norm", plan.device), _scalar(coef, "coef", plan.device)
+    if ws is None:
+        ws = plan.workspace()
+    _check(_LIB.grad_norm(plan.hptr, plan.dptr, max_norm, eps, _ptr(norm), _ptr(coef), _ptr(ws), ws.numel(),
+                          _stream(stream)))
+    return norm, coef
+
+
+def grad_scale(plan, coef, stream=None):
+    """Every gradient of the plan times coef (device fp32 [1]) in place; a NaN
+    coef leaves them as they are."""
+    _require(coef, "coef", torch.float32, plan.device, numel=1)
+    _check(_LIB.grad_scale(plan.hptr, plan.dptr, _ptr(coef), _stream(stream)))
+
+
+class AdamWState:
+    """AdamW state of one tensor of `numel` elements, zero at the start.
+
+    bits = 32: m, v fp32 [numel].  bits = 8: m int8 and v uint8 codes [numel],
+    m_absmax and v_absmax fp32, one per 256 elements.  Buffers that are given
+    are used as they are."""
+
+    def __init__(self, numel, bits=32, device="cuda", m=None, v=None, m_absmax=None, v_absmax=None):
+        if bits not in (8, 32):
+            raise ValueError(f"states have 32 or 8 bits, not {bits}")
+        if bits == 32 and (m_absmax is not None or v_absmax is not None):
+            raise ValueError("32-bit states have no absmax")
+        given = [t for t in (m, v, m_absmax, v_absmax) if t is not None]
+        dev = given[0].device if given else torch.device(device)
+
+        def take(t, name, count, dt):
+            if t is None:
+                return torch.zeros(count, dtype=dt, device=dev)
+            _require(t, name, dt, dev, numel=count)
+            return t
+
+        self.numel, self.bits = numel, bits
+        self.m = take(m, "m", numel, torch.float32 if bits == 32 else torch.int8)
+        self.v = take(v, "v", numel, torch.float32 if bits == 32 else torch.uint8)
+        self.m_absmax = self.v_absmax = None
+        if bits == 8:
+            self.m_absmax = take(m_absmax, "m_absmax", -(-numel // BLOCK), torch.float32)
+            self.v_absmax = take(v_absmax, "v_absmax", -(-numel // BLOCK), torch.float32)
+
+    def tensors(self):
+        return [t for t in (self.m, self.v, self.m_absmax, self.v_absmax) if t is not None]
+
+
+class AdamWPlan(_ListPlan):
+    """The parameters an AdamW step covers.
+
+    tensors: list of (weight, grad, state, copy, lr_scale, weight_decay):
+             weight fp32 / bf16 / f16, contiguous; grad of any of these types,
+             contiguous or a 2-D view with unit column stride; state an
+             AdamWState; copy None, or a bf16 / f16 tensor that receives the
+             new weight too; lr_scale a factor on the step's lr."""
+
+    def __init__(self, tensors, device=None):
+        if not tensors:
+            raise ValueError("no tensors")
+        home = tensors[0][0].device
+        arr = (L.AdamWTensor * len(tensors))()
+        keep, numels = [], []
+        for i, (weight, grad, state, copy, lr_scale, weight_decay) in enumerate(tensors):
+            n = state.numel
+            _require(weight, f"weight {i}", weight.dtype, home, numel=n)
+            cols, ld = _grad_view(grad, f"grad {i}")
+            if grad.numel() != n:
+                raise ValueError(f"grad {i} has {grad.numel()} elements, expected {n}")
+            if grad.device != home or state.m.device != home:
+                raise ValueError(f"tensor {i}: grad and state must be on {home}")
+            if copy is not None:
+                _require(copy, f"copy {i}", copy.dtype, home, numel=n)
+            p = [t.data_ptr() if t is not None else None
+                 for t in (weight, grad, state.m, state.v, state.m_absmax, state.v_absmax, copy)]
+            arr[i] = L.AdamWTensor(*p, n, cols, ld, _dtype(weight), _dtype(grad),
+                                   _dtype(copy) if copy is not None else 0, state.bits, lr_scale, weight_decay)
+            keep += [weight, grad, copy, state]
+            numels.append(n)
+        self._keep = keep
+        self._finish(_encode_list(_LIB.qm_adamw_plan_encode, arr, len(tensors)),
+                     device if device is not None else home, numels)
+
+    def view(self, flat, i):
+        """Tensor i's elements of a [256 * n_blocks] buffer (adamw_read_state)."""
+        e0 = self.block_offsets[i] * BLOCK
+        return flat[e0:e0 + self.numels[i]]
+
+
+def adamw_step(plan, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, grad_scale=None, rounding="nearest", seed=0,
+               offset=None, stream=None):
+    """One AdamW step (1-based `step`) over every tensor of the plan, in place.
+    grad_scale: optional device fp32 [1] factor on the gradients (the coef of
+    grad_norm); where it is NaN nothing is written.  rounding of 8-bit states:
+    "nearest" or "stochastic" (random stream chosen by seed and offset, the
+    step number if not given)."""
+    if grad_scale is not None:
+        _require(grad_scale, "grad_scale", torch.float32, plan.device, numel=1)
+    hp = L.AdamWHparams(lr, betas[0], betas[1], eps, step, ROUNDING[rounding],
+                        (step if offset is None else offset) & 0xFFFFFFFF, seed)
+    _check(_LIB.adamw_step(plan.hptr, plan.dptr, ctypes.byref(hp), _ptr(grad_scale), _stream(stream)))
+
+
+def adamw_read_state(plan, m=None, v=None, stream=None):
+    """The values the states stand for: fp32 [256 * plan.n_blocks] tensors
+    (given or new); plan.view(m, i) is tensor i's part.  Returns (m, v)."""
+    n = plan.n_blocks * BLOCK
+    out = []
+    for t, name in ((m, "m"), (v, "v")):
+        if t is None:
+            t = torch.empty(n, dtype=torch.float32, device=plan.device)
+        else:
+            _require(t, name, torch.float32, plan.device, numel=n)
+        out.append(t)
+    _check(_LIB.adamw_read_state(plan.hptr, plan.dptr, _ptr(out[0]), _ptr(out[1]), _stream(stream)))
+    return tuple(out)

@@ -21,6 +21,7 @@ c_void_p = ctypes.c_void_p
 c_i32 = ctypes.c_int32
 c_i64 = ctypes.c_int64
 c_f32 = ctypes.c_float
+c_f64 = ctypes.c_double
 c_size = ctypes.c_size_t
 
 
@@ -56,6 +57,24 @@ class GraspStateC(ctypes.Structure):
     _fields_ = [("res_codes", c_void_p), ("res_rmax", c_void_p), ("res_cmax", c_void_p),
                 ("p_codes", c_void_p), ("p_rmax", c_void_p), ("p_cmax", c_void_p),
                 ("r_codes", c_void_p), ("r_rmax", c_void_p), ("r_cmax", c_void_p)]
+
+
+class GradTensor(ctypes.Structure):
+    _fields_ = [("grad", c_void_p), ("numel", c_i64), ("cols", c_i64), ("ld", c_i64),
+                ("dtype", c_i32), ("reserved", c_i32)]
+
+
+class AdamWTensor(ctypes.Structure):
+    _fields_ = [("weight", c_void_p), ("grad", c_void_p), ("m", c_void_p), ("v", c_void_p),
+                ("m_absmax", c_void_p), ("v_absmax", c_void_p), ("copy", c_void_p),
+                ("numel", c_i64), ("grad_cols", c_i64), ("grad_ld", c_i64),
+                ("weight_dtype", c_i32), ("grad_dtype", c_i32), ("copy_dtype", c_i32),
+                ("state_bits", c_i32), ("lr_scale", c_f32), ("weight_decay", c_f32)]
+
+
+class AdamWHparams(ctypes.Structure):
+    _fields_ = [("lr", c_f64), ("beta1", c_f64), ("beta2", c_f64), ("eps", c_f64), ("step", c_i64),
+                ("rounding", c_i32), ("offset", ctypes.c_uint32), ("seed", ctypes.c_uint64)]
 
 
 # name -> (restype, argtypes); every symbol include/qmuon.h declares.
@@ -100,6 +119,14 @@ SIGNATURES = {
     "grasp_step": (c_i32, [ctypes.POINTER(GraspStateC), c_i64, c_i64, c_i32, c_i32, c_void_p, c_i32,
                            c_void_p, c_f32, c_i32, c_f32, c_f32, c_f32, c_f32, c_i32, c_void_p, c_f32, c_f32,
                            c_void_p, c_size, c_void_p]),
+    "qm_grad_plan_encode": (c_i32, [ctypes.POINTER(GradTensor), c_i32, c_void_p, ctypes.POINTER(c_size)]),
+    "grad_norm_workspace_bytes": (c_size, [c_void_p]),
+    "grad_norm": (c_i32, [c_void_p, c_void_p, c_f64, c_f64, c_void_p, c_void_p, c_void_p, c_size, c_void_p]),
+    "grad_scale": (c_i32, [c_void_p, c_void_p, c_void_p, c_void_p]),
+    "qm_adamw_plan_encode": (c_i32, [ctypes.POINTER(AdamWTensor), c_i32, c_void_p, ctypes.POINTER(c_size)]),
+    "qm_list_blocks": (c_i64, [c_void_p]),
+    "adamw_step": (c_i32, [c_void_p, c_void_p, ctypes.POINTER(AdamWHparams), c_void_p, c_void_p]),
+    "adamw_read_state": (c_i32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
     "qm_timing_enable": (c_i32, [c_i32]),
     "qm_timing_read": (c_i32, [c_i32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(c_i64)]),
     "qm_hbm_stream_copy": (c_i32, [c_void_p, c_void_p, c_size, c_void_p]),

@@ -2,8 +2,9 @@
 
 Every HIP translation unit is compiled with packed-fp32 instructions turned
 off (-Xclang -target-feature -Xclang -packed-fp32-ops) and for gfx950 only.
-The q8 update unit also gets -ffp-contract=off: its binary32 arithmetic must
-keep one rounding per operation to stay bit-identical to the CPU definition.
+The q8 update and AdamW units also get -ffp-contract=off: the binary32
+arithmetic of their 8-bit states must keep one rounding per operation to stay
+bit-identical to the CPU definition.
 """
 import concurrent.futures as cf
 import os
@@ -28,7 +29,10 @@ UNITS = [
     ("ns.hip", []),
     ("grasp.hip", ["-ffp-contract=off"]),
     ("hbm_stream.hip", []),
+    ("adamw.hip", ["-ffp-contract=off"]),
+    ("grad_norm.hip", []),
     ("plan.cpp", []),
+    ("list_plan.cpp", []),
     ("timing.cpp", ["-D__HIP_PLATFORM_AMD__", "-I", "/opt/rocm/include"]),
 ]
 

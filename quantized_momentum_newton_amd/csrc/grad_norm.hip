@@ -1,0 +1,190 @@
+// Global gradient norm and clip factor over a list of gradients, and the
+// scaling of the list in place, for gfx950 (wave64).
+//
+// norm = sqrt(sum g*g), summed in fp64: squares of fp32 gradients leave its
+// range long before the norm does, and sums of 10^9 of them lose digits in
+// fp32.  Two launches: every workgroup adds its tasks in order into one
+// partial sum, one workgroup adds the partials in order, so the result does
+// not depend on timing.  Bound by HBM: one read of the gradients.
+#include <hip/hip_runtime.h>
+
+#include <math.h>
+#include <stdint.h>
+
+#include "internal.h"
+#include "list_device.h"
+#include "list_layout.h"
+#include "qmuon.h"
+
+namespace qm {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWavesPerWG = kThreads / 64;
+constexpr int kMaxParts = 2048;   // workgroups of the first pass: 8 per CU, a read-only stream's best
+
+// Sum over the workgroup, valid in thread 0.
+__device__ __forceinline__ double wg_sum(double s) {
+    __shared__ double lds[kWavesPerWG];
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) s += xor_lanes(s, k);
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = s;
+    __syncthreads();
+    double t = 0.0;
+    if (threadIdx.x == 0)
+        for (int k = 0; k < kWavesPerWG; k++) t += lds[k];
+    return t;
+}
+
+template <int DT> __device__ __forceinline__ double task_sum(const ListTensor &T, int64_t e_task, int nvalid, int lane) {
+    double s = 0.0;
+    for (int p = 0; p < kListTask / 256; p++) {
+        const int e0 = p * 256 + lane * 4;
+        const int n = min(4, nvalid - e0);
+        if (n <= 0) continue;
+        const Raw4<DT> r = load_grad<DT>(T, e_task + e0, n);
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const double x = (double)elem<DT>(r, j);
+            s += x * x;
+        }
+    }
+    return s;
+}
+
+__global__ __launch_bounds__(kThreads) void grad_sumsq_kernel(const ListTensor *tensors, const int32_t *owner, int n_tasks,
+                                                             double *parts) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * kWavesPerWG + (threadIdx.x >> 6)));
+    double s = 0.0;
+    for (int task = wave; task < n_tasks; task += (int)gridDim.x * kWavesPerWG) {
+        const int32_t ti = __builtin_amdgcn_readfirstlane(gmem<const int32_t>(owner)[task]);
+        const ListTensor &T = gmem<const ListTensor>(tensors)[ti];
+        const int64_t e_task = (task - T.task_offset) * kListTask, rem = T.numel - e_task;
+        const int nvalid = rem < kListTask ? (int)rem : kListTask;
+        if (T.grad_dtype == QM_F32) s += task_sum<QM_F32>(T, e_task, nvalid, lane);
+        else if (T.grad_dtype == QM_BF16) s += task_sum<QM_BF16>(T, e_task, nvalid, lane);
+        else s += task_sum<QM_F16>(T, e_task, nvalid, lane);
+    }
+    s = wg_sum(s);
+    if (threadIdx.x == 0) parts[blockIdx.x] = s;
+}
+
+__global__ __launch_bounds__(kThreads) void grad_norm_finish_kernel(const double *parts, int n_parts, double max_norm, double eps,
+                                                                   float *norm_out, float *coef_out) {
+    double s = 0.0;
+    for (int k = threadIdx.x; k < n_parts; k += kThreads) s += parts[k];
+    s = wg_sum(s);
+    if (threadIdx.x != 0) return;
+    const double norm = sqrt(s);
+    *norm_out = (float)norm;
+    const double c = max_norm / (norm + eps);
+    *coef_out = !(s < (double)INFINITY) ? NAN : c < 1.0 ? (float)c : 1.0f;
+}
+
+template <int DT> __device__ __forceinline__ void task_scale(const ListTensor &T, int64_t e_task, int nvalid, int lane, float c) {
+    for (int p = 0; p < kListTask / 256; p++) {
+        const int e0 = p * 256 + lane * 4;
+        const int n = min(4, nvalid - e0);
+        if (n <= 0) continue;
+        const Raw4<DT> r = load_grad<DT>(T, e_task + e0, n);
+        float x[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) x[j] = elem<DT>(r, j) * c;
+        store_grad<DT>(T, e_task + e0, n, x);
+    }
+}
+
+__global__ __launch_bounds__(kThreads) void grad_scale_kernel(const ListTensor *tensors, const int32_t *owner, int n_tasks,
+                                                             const float *coef) {
+    const int lane = threadIdx.x & 63;
+    const int task = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * kWavesPerWG + (threadIdx.x >> 6)));
+    if (task >= n_tasks) return;
+    const float c = *gmem<const float>(coef);
+    if (c != c) return;
+    const int32_t ti = __builtin_amdgcn_readfirstlane(gmem<const int32_t>(owner)[task]);
+    const ListTensor &T = gmem<const ListTensor>(tensors)[ti];
+    const int64_t e_task = (task - T.task_offset) * kListTask, rem = T.numel - e_task;
+    const int nvalid = rem < kListTask ? (int)rem : kListTask;
+    if (T.grad_dtype == QM_F32) task_scale<QM_F32>(T, e_task, nvalid, lane, c);
+    else if (T.grad_dtype == QM_BF16) task_scale<QM_BF16>(T, e_task, nvalid, lane, c);
+    else task_scale<QM_F16>(T, e_task, nvalid, lane, c);
+}
+
+qm_status launched(const char *what) {
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? QM_OK : fail(QM_E_HIP, "%s launch: %s", what, hipGetErrorString(e));
+}
+
+unsigned parts_of(const ListHeader *h) {
+    const int64_t wgs = (h->n_tasks + kWavesPerWG - 1) / kWavesPerWG;
+    return (unsigned)(wgs < kMaxParts ? wgs : kMaxParts);
+}
+
+const ListHeader *list_args(const void *host_plan, const void *dev_plan, qm_status *st) {
+    const ListHeader *h = list_header(host_plan, kListGrads, st);
+    if (!h) return nullptr;
+    if (!dev_plan) {
+        *st = fail(QM_E_ARG, "device copy of the list is null");
+        return nullptr;
+    }
+    if (!aligned(dev_plan, 64)) {
+        *st = fail(QM_E_ALIGN, "device copy of the list must be 64-byte aligned");
+        return nullptr;
+    }
+    return h;
+}
+
+}  // namespace
+}  // namespace qm
+
+using namespace qm;
+
+extern "C" size_t grad_norm_workspace_bytes(const void *host_plan) {
+    qm_status st;
+    const ListHeader *h = list_header(host_plan, kListGrads, &st);
+    return h ? (size_t)(parts_of(h) + 1) * sizeof(double) : 0;
+}
+
+extern "C" qm_status grad_norm(const void *host_plan, const void *dev_plan, double max_norm, double eps, float *norm_out,
+                               float *coef_out, void *ws, size_t ws_bytes, qm_stream_t stream) {
+    clear_error();
+    qm_status st;
+    const ListHeader *h = list_args(host_plan, dev_plan, &st);
+    if (!h) return st;
+    if (!(max_norm > 0.0)) return fail(QM_E_ARG, "max_norm must be positive");
+    if (!(eps >= 0.0 && eps < (double)INFINITY)) return fail(QM_E_ARG, "eps must be finite and not negative");
+    if (!norm_out || !coef_out) return fail(QM_E_ARG, "norm_out and coef_out must not be null");
+    if (!aligned(norm_out, 4) || !aligned(coef_out, 4)) return fail(QM_E_ALIGN, "norm_out and coef_out need 4-byte alignment");
+    const unsigned parts = parts_of(h);
+    if (!ws || ws_bytes < (parts + 1) * sizeof(double))
+        return fail(QM_E_WORKSPACE, "workspace: need %zu bytes", (size_t)(parts + 1) * sizeof(double));
+    if (!aligned(ws, 8)) return fail(QM_E_ALIGN, "workspace needs 8-byte alignment");
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const char *dev = static_cast<const char *>(dev_plan);
+    double *part = static_cast<double *>(ws);
+    if (parts > 0) {
+        grad_sumsq_kernel<<<parts, kThreads, 0, s>>>(reinterpret_cast<const ListTensor *>(dev + h->off_tensors),
+                                                     reinterpret_cast<const int32_t *>(dev + h->off_task_tensor),
+                                                     (int)h->n_tasks, part);
+        if (qm_status e = launched("gradient norm")) return e;
+    }
+    grad_norm_finish_kernel<<<1, kThreads, 0, s>>>(part, (int)parts, max_norm, eps, norm_out, coef_out);
+    return launched("gradient norm");
+}
+
+extern "C" qm_status grad_scale(const void *host_plan, const void *dev_plan, const float *coef, qm_stream_t stream) {
+    clear_error();
+    qm_status st;
+    const ListHeader *h = list_args(host_plan, dev_plan, &st);
+    if (!h) return st;
+    if (!coef) return fail(QM_E_ARG, "coef must not be null");
+    if (!aligned(coef, 4)) return fail(QM_E_ALIGN, "coef needs 4-byte alignment");
+    if (h->n_tasks == 0) return QM_OK;
+    const char *dev = static_cast<const char *>(dev_plan);
+    const unsigned grid = (unsigned)((h->n_tasks + kWavesPerWG - 1) / kWavesPerWG);
+    grad_scale_kernel<<<grid, kThreads, 0, static_cast<hipStream_t>(stream)>>>(
+        reinterpret_cast<const ListTensor *>(dev + h->off_tensors),
+        reinterpret_cast<const int32_t *>(dev + h->off_task_tensor), (int)h->n_tasks, coef);
+    return launched("gradient scale");
+}

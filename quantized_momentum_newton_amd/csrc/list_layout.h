@@ -1,0 +1,51 @@
+// Byte layout of a tensor-list blob: what the AdamW step and the gradient
+// norm read on the device.  The host encoder (list_plan.cpp) writes it, the
+// caller copies it verbatim.
+//
+// The work is cut into tasks of up to 1024 consecutive elements (four
+// 256-element blocks) of one tensor, one wave64 each.  Tasks of tensors with
+// 32-bit states come first, then those with 8-bit states, each in list
+// order, so that one launch covers one kind.  A table names every task's
+// tensor (4 bytes per 1024 elements, one scalar load instead of a search).
+#pragma once
+#include <stdint.h>
+
+#include "qmuon.h"
+
+namespace qm {
+
+constexpr uint32_t kListMagic = 0x54534c51u;  // "QLST"
+constexpr uint32_t kListVersion = 1;
+constexpr int kListTask = 1024;
+enum { kListGrads = 1, kListAdamW = 2 };
+
+struct ListHeader {
+    uint32_t magic, version;
+    int32_t kind, n_tensors;
+    int64_t n_blocks, total_numel;
+    int64_t n_tasks;          // of all tensors
+    int64_t n_tasks32;        // tasks [0, n_tasks32): 32-bit states (grad lists: all)
+    int64_t off_tensors;      // ListTensor[n_tensors], list order
+    int64_t off_task_tensor;  // int32[n_tasks]
+    int64_t total_bytes;
+};
+
+struct ListTensor {
+    uint64_t weight, grad, m, v, m_absmax, v_absmax, copy;  // device addresses
+    int64_t numel;
+    int64_t grad_cols, grad_ld;   // 0: contiguous
+    int64_t task_offset;          // its first task
+    int64_t block_offset;         // its first block, list order
+    int32_t grad_dtype, weight_dtype, copy_dtype, state_bits;
+    float lr_scale, weight_decay;
+    int32_t pad[2];
+};
+
+static_assert(sizeof(ListHeader) == 72, "list header layout");
+static_assert(sizeof(ListTensor) == 128, "list tensor layout");
+
+// Reads and checks a host list blob of this kind (0: either); nullptr on
+// error (message recorded).
+const ListHeader *list_header(const void *host_blob, int kind, qm_status *st);
+
+}  // namespace qm

@@ -1,0 +1,367 @@
+"""AdamW over many tensors on the GPU against the oracle.
+
+8-bit states: codes and block maxima bit for bit.  Weights, copies and 32-bit
+states against fp64, within bounds counted from the roundings (u = 2^-24, half
+an fp32 step):
+  m: beta1 and 1 - beta1 as fp32, c g, two products, one sum: 5 u (|b1 m0| + |a1 g|);
+  v: the same and g g: 7 u (b2 v0 + a2 g^2);
+  update step m / (sqrt(v) root + eps): M = |b1 m0| + |a1 g| bounds |m|.  m: 5 u
+  (7 u with the block scale of 8-bit states), v / 2 and the root within an ulp
+  (2 u): 6.5 u, root and eps as fp32, product, sum: 4 u, the reciprocal within an ulp, the
+  product with m, step and lr_scale: 6 u -- 24 u step M / denom;
+  weight: decay as fp32 with three products: 5 u decay |w|, two sums: u (|w| + |w'|),
+  then its own type's rounding, eps / 2 relative or half the smallest subnormal.
+"""
+import numpy as np
+import pytest
+import torch
+
+import quantized_momentum_newton_amd as q
+from gpu_util import say
+from harness import inputs as H
+from oracle import adamw as A
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+U = 2.0 ** -24
+HP = dict(lr=2e-3, betas=(0.9, 0.99), eps=1e-8)
+DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+SUBNORMAL = {torch.float32: 2.0 ** -150, torch.bfloat16: 2.0 ** -134, torch.float16: 2.0 ** -25}
+
+
+def npf(t):
+    return t.detach().float().cpu().numpy().reshape(-1).copy()
+
+
+class Param:
+    """One tensor: device buffers (each inside a larger one with a canary on
+    both sides, `shift` elements off its start) and host copies."""
+
+    def __init__(self, n, bits, wdt, gdt, seed, copy=None, shift=0, cols=0, ld=0, lr_scale=1.0, decay=0.1, zero=False):
+        self.n, self.bits, self.lr_scale, self.decay = n, bits, lr_scale, decay
+        self.guards = []
+        nb = -(-n // 256)
+        if cols:
+            self.wide = torch.full((n // cols, ld), 7.0, dtype=gdt, device=DEV)
+            self.grad = self.wide[:, :cols]
+            self.grad.copy_(H.grad((n // cols, cols), gdt, DEV, seed, 1, std=1e-2))
+        else:
+            self.grad = self.place(H.grad((n,), gdt, DEV, seed, 1, std=1e-2), shift)
+        self.weight = self.place(H.weights((n,), DEV, seed, 2).to(wdt), shift)
+        self.copy = self.place(torch.zeros(n, dtype=copy, device=DEV), shift) if copy else None
+        g = H.gen(DEV, seed, 3)
+        if bits == 32:
+            m = torch.randn(n, generator=g, device=DEV) * 3e-3
+            v = torch.rand(n, generator=g, device=DEV) * 1e-4
+            if zero:
+                m, v = m * 0, v * 0
+            self.state = q.AdamWState(n, 32, DEV, m=self.place(m, shift), v=self.place(v, shift))
+        else:
+            m = torch.randint(-127, 128, (n,), generator=g, device=DEV, dtype=torch.int16).to(torch.int8)
+            v = torch.randint(0, 256, (n,), generator=g, device=DEV, dtype=torch.int16).to(torch.uint8)
+            ma, va = torch.rand(nb, generator=g, device=DEV) * 1e-2, torch.rand(nb, generator=g, device=DEV) * 1e-4
+            if zero:
+                m, v, ma, va = m * 0, v * 0, ma * 0, va * 0
+            self.state = q.AdamWState(n, 8, DEV, m=self.place(m, shift), v=self.place(v, shift),
+                                      m_absmax=self.place(ma, shift), v_absmax=self.place(va, shift))
+        self.snapshot()
+
+    def place(self, t, shift):
+        room = torch.empty(t.numel() + 64, dtype=t.dtype, device=DEV)
+        room.copy_(torch.arange(room.numel(), device=DEV) % 97)
+        at = 16 + shift
+        self.guards.append((room, at, t.numel(), room.clone()))
+        room[at:at + t.numel()] = t.reshape(-1)
+        return room[at:at + t.numel()]
+
+    def snapshot(self):
+        self.h = {"w": npf(self.weight), "g": npf(self.grad)}
+        for k in ("m", "v", "m_absmax", "v_absmax"):
+            t = getattr(self.state, k)
+            self.h[k] = t.cpu().numpy().copy() if t is not None else None
+
+    def tuple(self):
+        return (self.weight, self.grad, self.state, self.copy, self.lr_scale, self.decay)
+
+    def check(self, index, step, c=None, rounding="nearest", seed=0, offset=None, hp=HP):
+        (b1, b2), lr, eps = hp["betas"], hp["lr"] * self.lr_scale, hp["eps"]
+        h = self.h
+        g64 = h["g"].astype(np.float64) * (1.0 if c is None else float(c))
+        if self.bits == 32:
+            m0, v0 = h["m"].astype(np.float64), h["v"].astype(np.float64)
+        else:
+            word = None
+            if rounding == "stochastic":
+                word = A.words(self.n, seed, step if offset is None else offset, index)
+            g32 = h["g"] if c is None else h["g"] * np.float32(c)
+            want = A.coded_states(h["m"], h["v"], h["m_absmax"], h["v_absmax"], g32, b1, b2, word)
+            for k, x in zip(("m", "v", "m_absmax", "v_absmax"), want):
+                got = getattr(self.state, k).cpu().numpy()
+                assert np.array_equal(got, x, equal_nan=got.dtype.kind == "f"), (k, index, self.n)
+            blk = np.arange(self.n) // 256
+            m0 = h["m"].astype(np.float64) * (h["m_absmax"].astype(np.float64) / 127)[blk]
+            v0 = h["v"].astype(np.float64) ** 2 * (h["v_absmax"].astype(np.float64) / 65025)[blk]
+        m, v = A.moments(m0, v0, g64, b1, b2)
+        big = np.abs(b1 * m0) + np.abs((1 - b1) * g64)
+        if self.bits == 32:
+            em = np.abs(self.state.m.double().cpu().numpy() - m)
+            ev = np.abs(self.state.v.double().cpu().numpy() - v)
+            assert np.all(em <= 5 * U * big + 2.0 ** -148), (index, self.n)
+            assert np.all(ev <= 7 * U * v + 2.0 ** -147), (index, self.n)
+        w = A.weight(h["w"], m, v, step, lr, b1, b2, eps, self.decay)
+        denom = np.sqrt(v / (1 - b2 ** step)) + eps
+        tol = 24 * U * abs(lr) / (1 - b1 ** step) * big / denom
+        tol += 5 * U * abs(lr * self.decay) * np.abs(h["w"]) + U * (np.abs(h["w"]) + np.abs(w))
+        for t in (self.weight, self.copy):
+            if t is None:
+                continue
+            own = torch.finfo(t.dtype).eps / 2 if t.dtype != torch.float32 else 0.0
+            e = np.abs(t.double().cpu().numpy() - w)
+            lim = tol + own * (np.abs(w) + tol) + SUBNORMAL[t.dtype]
+            assert np.all(e <= lim), (index, self.n, t.dtype, float(np.max(e - lim)))
+        for room, at, n, before in self.guards:
+            assert torch.equal(room[:at], before[:at]) and torch.equal(room[at + n:], before[at + n:]), "canary"
+        assert np.array_equal(npf(self.grad), h["g"]), "the gradient is only read"
+
+
+SIZES = [1, 0, 2, 3, 5, 63, 255, 256, 257, 1000, 1023, 1024, 1025, 17 * 129, 4096 + 7, 70001]
+
+
+@pytest.mark.parametrize("gdt", list(DTYPES))
+@pytest.mark.parametrize("wdt", list(DTYPES))
+@pytest.mark.parametrize("bits", [32, 8])
+def test_sizes_and_types(bits, wdt, gdt):
+    """Every pair of types over ragged sizes: one plan, three steps from the
+    same buffers, the second with a clip factor, the third stochastic."""
+    seed = 100 + bits + 7 * list(DTYPES).index(gdt) + list(DTYPES).index(wdt)
+    ps = [Param(n, bits, DTYPES[wdt], DTYPES[gdt], seed * 50 + i, shift=i % 4, lr_scale=[1.0, 0.25][i % 2],
+                decay=[0.1, 0.0][i % 2], zero=i % 5 == 4,
+                copy=[None, torch.bfloat16, torch.float16][i % 3] if wdt == "f32" else None)
+          for i, n in enumerate(SIZES)]
+    plan = q.AdamWPlan([p.tuple() for p in ps])
+    c = torch.tensor([0.37], dtype=torch.float32, device=DEV)
+    for step, kw in ((1, {}), (2, dict(grad_scale=c)), (900, dict(rounding="stochastic", seed=(5 << 32) + 11))):
+        say("adamw", bits, wdt, gdt, "step", step)
+        q.adamw_step(plan, step, **HP, **kw)
+        torch.cuda.synchronize()
+        for i, p in enumerate(ps):
+            p.check(i, step, c=c.item() if "grad_scale" in kw else None, rounding=kw.get("rounding", "nearest"),
+                    seed=kw.get("seed", 0))
+            p.snapshot()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("cols,ld", [(256, 256), (256, 300), (12, 13), (7, 9), (1, 3), (1000, 1001), (2048, 2304)])
+def test_gradient_views(bits, cols, ld):
+    """Column slices of a wider buffer, aligned or not, rows that end inside
+    a lane's four elements."""
+    ps = [Param(rows * cols, bits, torch.float32, gdt, 900 + cols + 13 * k, cols=cols, ld=ld)
+          for k, (rows, gdt) in enumerate([(37, torch.bfloat16), (5, torch.float32), (1, torch.float16)])]
+    plan = q.AdamWPlan([p.tuple() for p in ps])
+    say("adamw views", bits, cols, ld)
+    q.adamw_step(plan, 3, **HP)
+    torch.cuda.synchronize()
+    for i, p in enumerate(ps):
+        p.check(i, 3)
+
+
+def test_mixed_list_and_state_values():
+    """32- and 8-bit states and all types in one list; the values read out
+    are the decoded ones, zero between tensors."""
+    spec = [(300, 8, "bf16", "f32"), (5000, 32, "f32", "bf16"), (1, 8, "f32", "f16"), (0, 32, "f32", "f32"),
+            (2048, 32, "bf16", "bf16"), (4097, 8, "f32", "bf16"), (77, 32, "f16", "f32")]
+    ps = [Param(n, b, DTYPES[w], DTYPES[g], 4000 + i, copy=torch.bfloat16 if w == "f32" else None)
+          for i, (n, b, w, g) in enumerate(spec)]
+    plan = q.AdamWPlan([p.tuple() for p in ps])
+    say("adamw mixed list")
+    q.adamw_step(plan, 7, **HP, rounding="stochastic", seed=3, offset=99)
+    m, v = q.adamw_read_state(plan)
+    torch.cuda.synchronize()
+    inside = torch.zeros_like(m, dtype=torch.bool)
+    for i, p in enumerate(ps):
+        p.check(i, 7, rounding="stochastic", seed=3, offset=99)
+        st = p.state
+        if p.bits == 32:
+            wm, wv = st.m.cpu().numpy(), st.v.cpu().numpy()
+        else:
+            wm, wv = A.decode(*(t.cpu().numpy() for t in (st.m, st.v, st.m_absmax, st.v_absmax)))
+        assert np.array_equal(plan.view(m, i).cpu().numpy(), wm) and np.array_equal(plan.view(v, i).cpu().numpy(), wv)
+        plan.view(inside, i).fill_(True)
+    assert torch.all(m[~inside] == 0) and torch.all(v[~inside] == 0)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_nan_factor_writes_nothing(bits):
+    p = Param(5000, bits, torch.bfloat16, torch.float32, 77)
+    plan = q.AdamWPlan([p.tuple()])
+    before = [t.clone() for t in [p.weight] + p.state.tensors()]
+    q.adamw_step(plan, 2, **HP, grad_scale=torch.full((1,), float("nan"), device=DEV))
+    torch.cuda.synchronize()
+    for a, b in zip(before, [p.weight] + p.state.tensors()):
+        assert torch.equal(a, b)
+
+
+def test_edge_values_of_8_bit_states():
+    """Blocks that are zero, tiny, hold an infinity or a NaN, or span the
+    whole range; other blocks of the tensor are untouched by them."""
+    n = 256 * 9 + 40
+    p = Param(n, 8, torch.float32, torch.float32, 5, zero=True)
+    g = torch.zeros(n)
+    g[256] = 1e-31
+    g[512], g[513] = float("inf"), 1.0
+    g[768], g[769] = float("nan"), float("inf")
+    g[1024], g[1025], g[1026] = 1.0, 1e-18, 1e-30
+    g[1280:1536] = torch.logspace(-20, 18, 256)
+    g[1536:1792] = 3.0e38
+    g[1792:2048] = torch.linspace(-255, 255, 256)
+    g[-1] = float("nan")
+    p.grad.copy_(g)
+    p.snapshot()
+    plan = q.AdamWPlan([p.tuple()])
+    with np.errstate(all="ignore"):
+        for step in (1, 2):
+            q.adamw_step(plan, step, **HP)
+            torch.cuda.synchronize()
+            want = A.coded_states(p.h["m"], p.h["v"], p.h["m_absmax"], p.h["v_absmax"], p.h["g"], *HP["betas"])
+            for k, x in zip(("m", "v", "m_absmax", "v_absmax"), want):
+                assert np.array_equal(getattr(p.state, k).cpu().numpy(), x, equal_nan=x.dtype.kind == "f"), (k, step)
+            p.snapshot()
+    w = p.weight.cpu().numpy()
+    fine = np.isfinite(p.h["g"])
+    fine[512:1024] = False              # decoded from a poisoned block in the second step
+    fine[256 * 9:] = False
+    fine[1280:1792] = False             # squares past fp32's range
+    assert np.all(np.isfinite(w[fine]))
+
+
+def test_edge_values_of_32_bit_states():
+    """A NaN or an infinity stays with its element."""
+    p = Param(3000, 32, torch.float32, torch.float32, 6)
+    p.grad[5], p.grad[1500] = float("nan"), float("inf")
+    plan = q.AdamWPlan([p.tuple()])
+    q.adamw_step(plan, 4, **HP)
+    torch.cuda.synchronize()
+    bad = torch.zeros(3000, dtype=torch.bool, device=DEV)
+    bad[5] = bad[1500] = True
+    assert torch.all(torch.isfinite(p.weight[~bad])) and torch.all(torch.isfinite(p.state.m[~bad]))
+    assert torch.isnan(p.weight[5]) and torch.isnan(p.state.v[5]) and torch.isinf(p.state.v[1500])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_repeats_bit_for_bit(bits):
+    outs = []
+    for _ in range(2):
+        p = Param(300007, bits, torch.bfloat16, torch.bfloat16, 31)
+        plan = q.AdamWPlan([p.tuple()])
+        for step in range(1, 5):
+            q.adamw_step(plan, step, **HP, rounding="stochastic", seed=8)
+        torch.cuda.synchronize()
+        outs.append([p.weight.clone()] + [t.clone() for t in p.state.tensors()])
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+
+
+def test_training_tracks_32_bit_states():
+    """30 steps on noisy gradients: weights by stochastic 8-bit states stay
+    within 5 % (Frobenius) of the way that 32-bit states take, block edges
+    and all.  m's rounding is at most one step of 1/127 of its block's
+    maximum (about 3 rms) and v's at most 2 / (2 k + 1) at root k, of
+    independent signs: an update's rms error is about 3 / 127 / sqrt(6) +
+    1 / 100 of its size, 2 %; the bound leaves the factor that errors of
+    consecutive steps share through m's memory."""
+    n = 256 * 200 + 13
+    a, b = (Param(n, bits, torch.float32, torch.float32, 71, zero=True) for bits in (32, 8))
+    start = a.weight.clone()
+    b.weight.copy_(start)
+    plans = [q.AdamWPlan([p.tuple()]) for p in (a, b)]
+    for step in range(1, 31):
+        g = H.grad((n,), torch.float32, DEV, 72, step, std=1e-2) + 5e-3
+        for p, plan in zip((a, b), plans):
+            p.grad.copy_(g)
+            q.adamw_step(plan, step, **HP, rounding="stochastic", seed=1)
+    torch.cuda.synchronize()
+    way, off = (a.weight - start).double(), (a.weight - b.weight).double()
+    say("8-bit against 32-bit states after 30 steps:", float(off.norm() / way.norm()))
+    assert off.norm() < 0.05 * way.norm()
+
+
+def test_side_stream_and_graph():
+    """On a stream of its own, then captured and replayed three times with
+    eager work between, each replay against the eager step."""
+    ps = [Param(n, b, torch.float32, torch.bfloat16, 51 + n, copy=torch.bfloat16) for n, b in ((5000, 8), (777, 32))]
+    plan = q.AdamWPlan([p.tuple() for p in ps])
+    grads = q.GradPlan([p.grad for p in ps])
+    ws = grads.workspace()
+    norm, coef = torch.zeros(1, device=DEV), torch.zeros(1, device=DEV)
+    live = [t for p in ps for t in [p.weight, p.copy] + p.state.tensors()]
+    before = [t.clone() for t in live]
+
+    def work():
+        q.grad_norm(grads, 0.5, norm=norm, coef=coef, ws=ws)
+        q.adamw_step(plan, 5, **HP, grad_scale=coef)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        work()
+    torch.cuda.synchronize()
+    c = coef.item()
+    for i, p in enumerate(ps):
+        p.check(i, 5, c=c)
+    want = [t.clone() for t in live]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        work()
+    for k in range(3):
+        for t, b in zip(live, before):
+            t.copy_(b)
+        torch.randn(1000, device=DEV).sum().item()
+        graph.replay()
+        torch.cuda.synchronize()
+        for t, w in zip(live, want):
+            assert torch.equal(t, w), k
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_elements_past_32_bit_offsets(bits):
+    """A tensor of 2^32 + 300 elements: the elements beyond 2^32 (and some
+    before) against the oracle; the norm of its gradient."""
+    n = (1 << 32) + 300
+    say("adamw past 2^32 elements, states of", bits, "bits")
+    w = torch.zeros(n, dtype=torch.bfloat16, device=DEV)
+    g = torch.zeros(n, dtype=torch.bfloat16, device=DEV)
+    st = q.AdamWState(n, bits, DEV)
+    spots = [slice(0, 300), slice((1 << 31) - 256, (1 << 31) + 256), slice((1 << 32) - 256, n)]
+    for k, s in enumerate(spots):
+        g[s] = H.grad((s.stop - s.start,), torch.bfloat16, DEV, 600, k, std=1e-2)
+        w[s] = H.weights((s.stop - s.start,), DEV, 601, k).to(torch.bfloat16)
+    plan = q.AdamWPlan([(w, g, st, None, 1.0, 0.1)])
+    w0 = [npf(w[s]) for s in spots]
+    norm, coef = q.grad_norm(q.GradPlan([g]), 1e9)
+    q.adamw_step(plan, 1, **HP, rounding="stochastic", seed=2)
+    torch.cuda.synchronize()
+    total = 0.0
+    for k, s in enumerate(spots):
+        gh = npf(g[s])
+        total += float(np.sum(gh.astype(np.float64) ** 2))
+        m, v = A.moments(np.zeros(gh.size), np.zeros(gh.size), gh, *HP["betas"])
+        want = A.weight(w0[k], m, v, 1, HP["lr"], *HP["betas"], HP["eps"], 0.1)
+        assert np.all(np.abs(npf(w[s]) - want) <= np.abs(want) * 2.0 ** -8 + HP["lr"] * 40 * U), k
+        if bits == 32:
+            assert np.all(np.abs(npf(st.m[s]) - m) <= 5 * U * np.abs(m) + 2.0 ** -148)
+        else:
+            zero = np.zeros(gh.size)
+            nb = -(-gh.size // 256)
+            word = A.words(300, 2, 1, 0) if k == 0 else None
+            if word is not None:
+                full = A.coded_states(zero.astype(np.int8), zero.astype(np.uint8), np.zeros(nb, np.float32),
+                                      np.zeros(nb, np.float32), gh, *HP["betas"], word)
+                assert np.array_equal(st.m[:256].cpu().numpy(), full[0][:256])
+            blocks = slice(s.start // 256, s.start // 256 + nb)
+            top = np.array([np.max(np.abs(x)) for x in np.split(np.float32(1.0 - HP["betas"][0]) * gh, range(256, gh.size, 256))])
+            got = st.m_absmax[blocks].cpu().numpy()
+            assert np.array_equal(got, top)
+    # nothing anywhere else
+    assert int((w != 0).sum()) == sum(int((w[s] != 0).sum()) for s in spots)
+    assert int((st.m != 0).sum()) == sum(int((st.m[s] != 0).sum()) for s in spots)
+    assert abs(norm.item() - total ** 0.5) <= 2 * U * total ** 0.5 and coef.item() == 1.0
