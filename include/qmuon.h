@@ -570,7 +570,7 @@ typedef struct {
 } qm_adamw_tensor;
 
 typedef struct {
-    double lr, beta1, beta2, eps;  /* 0 <= beta < 1, eps > 0                 */
+    double lr, beta1, beta2, eps;  /* 0 <= beta < 1, eps >= 2^-126           */
     int64_t step;        /* t, 1-based                                       */
     int32_t rounding;    /* qm_rounding of 8-bit states                      */
     uint32_t offset;     /* counter word 2 of stochastic rounding            */

@@ -44,8 +44,8 @@ struct AdamArgs {
 // New weight from the new moments.  The root and the quotient are the
 // hardware's to within an ulp or two: the update is a small part of w.
 __device__ __forceinline__ float new_weight(float w, float m, float v, float step, float decay, const AdamArgs &A) {
-    const float denom = sqrtf(v) * A.root + A.eps;
-    return (w - w * decay) - step * (m / denom);
+    const float denom = __builtin_amdgcn_sqrtf(v) * A.root + A.eps;
+    return (w - w * decay) - step * (m * __builtin_amdgcn_rcpf(denom));
 }
 
 template <int DT> __device__ __forceinline__ void store_weight(const ListTensor &T, int64_t e, int n, const float *w) {
@@ -83,6 +83,47 @@ __device__ __forceinline__ void task32(const ListTensor &T, int64_t e_task, int 
         store_upto4<QM_F32>(T.m, e, n, m);
         store_upto4<QM_F32>(T.v, e, n, v);
         store_weight<WDT>(T, e, n, w);
+    }
+}
+
+// A whole task with every load issued before the arithmetic: 4 elements per
+// lane in each of 4 parts, one contiguous 1 KiB (fp32) or 512 B span per
+// instruction.
+template <int GDT, int WDT>
+__device__ __forceinline__ void task32_full(const ListTensor &T, int64_t e_task, int lane, float c, const AdamArgs &A) {
+    constexpr int P = kListTask / 256;
+    PackedOf<GDT, 4> rg[P];
+    PackedOf<WDT, 4> rw[P];
+    Packed<16> rm[P], rv[P];
+    const uint64_t bw = T.weight + (uint64_t)e_task * kSizeOf<WDT>, bm = T.m + (uint64_t)e_task * 4, bv = T.v + (uint64_t)e_task * 4;
+    load_grad_task<GDT, 4, P>(T, e_task, lane, rg);
+#pragma unroll
+    for (int p = 0; p < P; p++) {
+        const uint32_t i = p * 256 + lane * 4;
+        rw[p] = load_bytes<4 * kSizeOf<WDT>>(bw, i * kSizeOf<WDT>);
+        rm[p] = load_bytes<16>(bm, i * 4);
+        rv[p] = load_bytes<16>(bv, i * 4);
+    }
+    const float step = A.step * T.lr_scale, decay = A.lr * T.lr_scale * T.weight_decay;
+#pragma unroll
+    for (int p = 0; p < P; p++) {
+        const uint32_t i = p * 256 + lane * 4;
+        float m[4], v[4], w[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const float g = unpack<GDT>(rg[p], j) * c;
+            m[j] = A.b1 * unpack<QM_F32>(rm[p], j) + A.omb1 * g;
+            v[j] = A.b2 * unpack<QM_F32>(rv[p], j) + A.omb2 * (g * g);
+            w[j] = new_weight(unpack<WDT>(rw[p], j), m[j], v[j], step, decay, A);
+        }
+        store_bytes(bm, i * 4, pack<QM_F32, 4>(m));
+        store_bytes(bv, i * 4, pack<QM_F32, 4>(v));
+        store_bytes(bw, i * kSizeOf<WDT>, pack<WDT, 4>(w));
+        if (T.copy) {
+            const uint64_t bc = T.copy + (uint64_t)e_task * 2;
+            if (T.copy_dtype == QM_BF16) store_bytes(bc, i * 2, pack<QM_BF16, 4>(w));
+            else store_bytes(bc, i * 2, pack<QM_F16, 4>(w));
+        }
     }
 }
 
@@ -200,17 +241,172 @@ __device__ __forceinline__ void task8(const ListTensor &T, int32_t tensor, int64
     }
 }
 
+// ---- a whole task: 8 elements per lane in each of 2 halves.  A lane's
+// accesses are 16 bytes of a 16-bit type or 8 of codes, and a block is 32
+// lanes of one half.
+
+// x / D for D = 127 or 65025, correctly rounded: quotient by the rounded
+// reciprocal, one step of its residual.  Equal to the division for every
+// significand (checked exhaustively) and every x that a block maximum can be
+// (0, or 2^-100 and above).
+template <int D> __device__ __forceinline__ float div_const(float x) {
+    constexpr float d = (float)D, r = 1.0f / d;
+    const float q = x * r;
+    return __builtin_fmaf(__builtin_fmaf(-q, d, x), r, q);
+}
+
+// Rows are the 16-lane quarters of a wave.  Row r holds the scalars of block
+// (r & 1) * 2 + (r >> 1) of the task: after permlane16_swap the pairs (half
+// 0, half 1) of a lane's blocks come from two registers, and back.
+__device__ __forceinline__ int row_block(int lane) { return ((lane >> 4) & 1) * 2 + (lane >> 5); }
+
+// Row values to each lane's (half 0, half 1) values.
+__device__ __forceinline__ void row_spread(float x, float *h) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    h[0] = __uint_as_float(r[0]);
+    h[1] = __uint_as_float(r[1]);
+}
+
+template <int ROR> __device__ __forceinline__ uint32_t max_ror(uint32_t x) {
+    return max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x120 + ROR, 0xf, 0xf, false));
+}
+// Lanes' maxima of half 0 and half 1 to the block's maximum in its row.
+__device__ __forceinline__ uint32_t row_max(uint32_t h0, uint32_t h1) {
+    const auto r = __builtin_amdgcn_permlane16_swap(h0, h1, false, false);
+    return max_ror<1>(max_ror<2>(max_ror<4>(max_ror<8>(max((uint32_t)r[0], (uint32_t)r[1])))));
+}
+
+// Code of v by nearest value, as an integer.  k = floor of the hardware root
+// (within an ulp) is floor(sqrt y) or its neighbour next to a perfect
+// square, where both give the same code; y > 2^-149 codes at least 1.
+__device__ __forceinline__ uint32_t v_code_near(float y, float v) {
+    const float k = floorf(__builtin_amdgcn_sqrtf(y));
+    const float d = __builtin_fmaf(-k, k, y);
+    const uint32_t code = (uint32_t)(int)k + (d > k + 0.5f ? 1u : 0u);
+    return max(code, min(__float_as_uint(v), 1u));
+}
+
+template <int GDT, int WDT, bool SR>
+__device__ __forceinline__ void task8_full(const ListTensor &T, int32_t tensor, int64_t e_task, int lane, float c, const AdamArgs &A) {
+    constexpr int N = 8, H = 2;
+    PackedOf<GDT, N> rg[H];
+    PackedOf<WDT, N> rw[H];
+    Packed<8> qm[H], qv[H];
+    const uint64_t bw = T.weight + (uint64_t)e_task * kSizeOf<WDT>, bm = T.m + (uint64_t)e_task, bv = T.v + (uint64_t)e_task;
+    float *pm = gmem<float>(T.m_absmax) + (e_task >> 8) + row_block(lane);
+    float *pv = gmem<float>(T.v_absmax) + (e_task >> 8) + row_block(lane);
+    const float old_m = *pm, old_v = *pv;
+    load_grad_task<GDT, N, H>(T, e_task, lane, rg);
+#pragma unroll
+    for (int h = 0; h < H; h++) {
+        const uint32_t i = h * 512 + lane * N;
+        qm[h] = load_bytes<8>(bm, i);
+        qv[h] = load_bytes<8>(bv, i);
+        rw[h] = load_bytes<N * kSizeOf<WDT>>(bw, i * kSizeOf<WDT>);
+    }
+    const float step = A.step * T.lr_scale, decay = A.lr * T.lr_scale * T.weight_decay;
+    float step_m[H], step_v[H], m[H][N], v[H][N];
+    row_spread(div_const<127>(old_m) * A.b1, step_m);
+    row_spread(div_const<65025>(old_v) * A.b2, step_v);
+    uint32_t top_m[H] = {}, top_v[H] = {};
+#pragma unroll
+    for (int h = 0; h < H; h++) {
+        const uint32_t i = h * 512 + lane * N;
+        float w[N];
+#pragma unroll
+        for (int j = 0; j < N; j++) {
+            const float g = unpack<GDT>(rg[h], j) * c;
+            const float cv = (float)((qv[h].w[j / 4] >> (8 * (j % 4))) & 0xffu);
+            m[h][j] = (float)(int8_t)(qm[h].w[j / 4] >> (8 * (j % 4))) * step_m[h] + A.omb1 * g;
+            v[h][j] = (cv * cv) * step_v[h] + A.omb2 * (g * g);
+            top_m[h] = max(top_m[h], __float_as_uint(m[h][j]) & 0x7fffffffu);
+            top_v[h] = max(top_v[h], __float_as_uint(v[h][j]) & 0x7fffffffu);
+            w[j] = new_weight(unpack<WDT>(rw[h], j), m[h][j], v[h][j], step, decay, A);
+        }
+        store_bytes(bw, i * kSizeOf<WDT>, pack<WDT, N>(w));
+        if (T.copy) {
+            const uint64_t bc = T.copy + (uint64_t)e_task * 2;
+            if (T.copy_dtype == QM_BF16) store_bytes(bc, i * 2, pack<QM_BF16, N>(w));
+            else store_bytes(bc, i * 2, pack<QM_F16, N>(w));
+        }
+    }
+    float am = __uint_as_float(row_max(top_m[0], top_m[1])), av = __uint_as_float(row_max(top_v[0], top_v[1]));
+    if (am < kTiny) am = 0.0f;
+    if (av < kTiny) av = 0.0f;
+    if ((lane & 15) == 0) {
+        *pm = am;
+        *pv = av;
+    }
+    float im[H], iv[H];
+    row_spread(am > 0.0f ? 127.0f / am : 0.0f, im);
+    row_spread(av > 0.0f ? 65025.0f / av : 0.0f, iv);
+    // blocks whose codes are all 0: a maximum that is not finite, or v's is 0
+    float keep_m[H] = {1.0f, 1.0f}, keep_v[H] = {1.0f, 1.0f};
+    const bool odd = __any(!(am < INFINITY) || !(av < INFINITY) || av == 0.0f);
+    if (odd) {
+        row_spread(am < INFINITY ? 1.0f : 0.0f, keep_m);
+        row_spread(av < INFINITY && av > 0.0f ? 1.0f : 0.0f, keep_v);
+    }
+#pragma unroll
+    for (int h = 0; h < H; h++) {
+        const uint32_t i = h * 512 + lane * N;
+        uint32_t cm[N], cv[N];
+        if constexpr (SR) {
+            uint32_t word[N];
+            const uint64_t quad = (uint64_t)(e_task + i) >> 2;
+#pragma unroll
+            for (int k = 0; k < N / 4; k++)
+                philox4x32_10((uint32_t)(quad + k), (uint32_t)((quad + k) >> 32), A.offset, (uint32_t)tensor, (uint32_t)A.seed,
+                              (uint32_t)(A.seed >> 32), word + 4 * k);
+#pragma unroll
+            for (int j = 0; j < N; j++) {
+                cm[j] = (uint32_t)m_code(m[h][j] * im[h], word[j], 1);
+                cv[j] = (uint32_t)v_code(v[h][j] * iv[h], v[h][j], word[j], 1);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; j++) {
+                // adding 1.5 * 2^23 rounds to a whole number, ties to even; |x| <= 127 (1 + 2^-23),
+                // so the sum's low byte is the code
+                cm[j] = __float_as_uint(m[h][j] * im[h] + 12582912.0f);
+                cv[j] = v_code_near(v[h][j] * iv[h], v[h][j]);
+            }
+        }
+        Packed<8> om, ov;
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+            om.w[k] = pack_low_bytes(cm[4 * k], cm[4 * k + 1], cm[4 * k + 2], cm[4 * k + 3]);
+            ov.w[k] = pack_low_bytes(cv[4 * k], cv[4 * k + 1], cv[4 * k + 2], cv[4 * k + 3]);
+        }
+        if (odd) {
+#pragma unroll
+            for (int k = 0; k < 2; k++) {
+                if (keep_m[h] == 0.0f) om.w[k] = 0;
+                if (keep_v[h] == 0.0f) ov.w[k] = 0;
+            }
+        }
+        store_bytes(bm, i, om);
+        store_bytes(bv, i, ov);
+    }
+}
+
 // ------------------------------------------------------------ kernels
 
-template <int BITS, int GDT, int WDT>
+template <int BITS, bool SR, int GDT, int WDT>
 __device__ __forceinline__ void run_task(const ListTensor &T, int32_t tensor, int64_t lt, int lane, float c, const AdamArgs &A) {
     const int64_t e_task = lt * kListTask, rem = T.numel - e_task;
     const int nvalid = rem < kListTask ? (int)rem : kListTask;
-    if constexpr (BITS == 32) task32<GDT, WDT>(T, e_task, nvalid, lane, c, A);
-    else task8<GDT, WDT>(T, tensor, e_task, nvalid, lane, c, A);
+    if constexpr (BITS == 32) {
+        if (nvalid == kListTask && grad_groups<4>(T)) task32_full<GDT, WDT>(T, e_task, lane, c, A);
+        else task32<GDT, WDT>(T, e_task, nvalid, lane, c, A);
+    }
+    else {
+        if (nvalid == kListTask && grad_groups<8>(T)) task8_full<GDT, WDT, SR>(T, tensor, e_task, lane, c, A);
+        else task8<GDT, WDT>(T, tensor, e_task, nvalid, lane, c, A);
+    }
 }
 
-template <int BITS> __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamArgs A) {
+template <int BITS, bool SR> __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamArgs A) {
     const int lane = threadIdx.x & 63;
     const int task = A.task_lo + __builtin_amdgcn_readfirstlane((int)(blockIdx.x * kWavesPerWG + (threadIdx.x >> 6)));
     if (task >= A.task_hi) return;
@@ -220,18 +416,18 @@ template <int BITS> __global__ __launch_bounds__(kThreads) void adamw_kernel(Ada
         if (c != c) return;   // the gradient's norm is not finite: leave everything as it is
     }
     const int32_t ti = __builtin_amdgcn_readfirstlane(gmem<const int32_t>(A.owner)[task]);
-    const ListTensor &T = gmem<const ListTensor>(A.tensors)[ti];
+    const ListTensor T = gmem<const ListTensor>(A.tensors)[ti];
     const int64_t lt = task - T.task_offset;
     switch (T.grad_dtype * 3 + T.weight_dtype) {
-        case QM_F32 * 3 + QM_F32: run_task<BITS, QM_F32, QM_F32>(T, ti, lt, lane, c, A); break;
-        case QM_F32 * 3 + QM_BF16: run_task<BITS, QM_F32, QM_BF16>(T, ti, lt, lane, c, A); break;
-        case QM_F32 * 3 + QM_F16: run_task<BITS, QM_F32, QM_F16>(T, ti, lt, lane, c, A); break;
-        case QM_BF16 * 3 + QM_F32: run_task<BITS, QM_BF16, QM_F32>(T, ti, lt, lane, c, A); break;
-        case QM_BF16 * 3 + QM_BF16: run_task<BITS, QM_BF16, QM_BF16>(T, ti, lt, lane, c, A); break;
-        case QM_BF16 * 3 + QM_F16: run_task<BITS, QM_BF16, QM_F16>(T, ti, lt, lane, c, A); break;
-        case QM_F16 * 3 + QM_F32: run_task<BITS, QM_F16, QM_F32>(T, ti, lt, lane, c, A); break;
-        case QM_F16 * 3 + QM_BF16: run_task<BITS, QM_F16, QM_BF16>(T, ti, lt, lane, c, A); break;
-        default: run_task<BITS, QM_F16, QM_F16>(T, ti, lt, lane, c, A); break;
+        case QM_F32 * 3 + QM_F32: run_task<BITS, SR, QM_F32, QM_F32>(T, ti, lt, lane, c, A); break;
+        case QM_F32 * 3 + QM_BF16: run_task<BITS, SR, QM_F32, QM_BF16>(T, ti, lt, lane, c, A); break;
+        case QM_F32 * 3 + QM_F16: run_task<BITS, SR, QM_F32, QM_F16>(T, ti, lt, lane, c, A); break;
+        case QM_BF16 * 3 + QM_F32: run_task<BITS, SR, QM_BF16, QM_F32>(T, ti, lt, lane, c, A); break;
+        case QM_BF16 * 3 + QM_BF16: run_task<BITS, SR, QM_BF16, QM_BF16>(T, ti, lt, lane, c, A); break;
+        case QM_BF16 * 3 + QM_F16: run_task<BITS, SR, QM_BF16, QM_F16>(T, ti, lt, lane, c, A); break;
+        case QM_F16 * 3 + QM_F32: run_task<BITS, SR, QM_F16, QM_F32>(T, ti, lt, lane, c, A); break;
+        case QM_F16 * 3 + QM_BF16: run_task<BITS, SR, QM_F16, QM_BF16>(T, ti, lt, lane, c, A); break;
+        default: run_task<BITS, SR, QM_F16, QM_F16>(T, ti, lt, lane, c, A); break;
     }
 }
 
@@ -242,39 +438,74 @@ __global__ __launch_bounds__(kThreads) void adamw_read_kernel(const ListTensor *
     const int task = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * kWavesPerWG + (threadIdx.x >> 6)));
     if (task >= n_tasks) return;
     const int32_t ti = __builtin_amdgcn_readfirstlane(gmem<const int32_t>(owner)[task]);
-    const ListTensor &T = gmem<const ListTensor>(tensors)[ti];
+    const ListTensor T = gmem<const ListTensor>(tensors)[ti];
     const int64_t e_task = (task - T.task_offset) * kListTask;
     const int64_t rem = T.numel - e_task;
     const int nvalid = rem < kListTask ? (int)rem : kListTask;
-    const int64_t out = T.block_offset * kBlock + e_task;
-    for (int p = 0; p < kListTask / 256; p++) {
+    const uint64_t out = (uint64_t)(T.block_offset * kBlock + e_task) * 4;
+    constexpr int P = kListTask / 256;
+    if (nvalid == kListTask) {
+        Packed<16> m[P], v[P];
+        if (T.state_bits == 32) {
+#pragma unroll
+            for (int p = 0; p < P; p++) {
+                m[p] = load_bytes<16>(T.m + (uint64_t)e_task * 4, (p * 256 + lane * 4) * 4);
+                v[p] = load_bytes<16>(T.v + (uint64_t)e_task * 4, (p * 256 + lane * 4) * 4);
+            }
+        } else {
+            Packed<4> qm[P], qv[P];
+            float am[P], av[P];
+#pragma unroll
+            for (int p = 0; p < P; p++) {
+                qm[p] = load_bytes<4>(T.m + (uint64_t)e_task, p * 256 + lane * 4);
+                qv[p] = load_bytes<4>(T.v + (uint64_t)e_task, p * 256 + lane * 4);
+                am[p] = gmem<const float>(T.m_absmax)[(e_task >> 8) + p];
+                av[p] = gmem<const float>(T.v_absmax)[(e_task >> 8) + p];
+            }
+#pragma unroll
+            for (int p = 0; p < P; p++) {
+                const float sm = am[p] / 127.0f, sv = av[p] / 65025.0f;
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const float cv = (float)((qv[p].w[0] >> (8 * j)) & 0xffu);
+                    m[p].w[j] = __float_as_uint((float)(int8_t)(qm[p].w[0] >> (8 * j)) * sm);
+                    v[p].w[j] = __float_as_uint((cv * cv) * sv);
+                }
+            }
+        }
+#pragma unroll
+        for (int p = 0; p < P; p++) {
+            store_bytes((uint64_t)m_out + out, (p * 256 + lane * 4) * 4, m[p]);
+            store_bytes((uint64_t)v_out + out, (p * 256 + lane * 4) * 4, v[p]);
+        }
+        return;
+    }
+    for (int p = 0; p < P; p++) {
         if (p * 256 >= nvalid) break;
         const int e0 = p * 256 + lane * 4;
         const int n = max(0, min(4, nvalid - e0));
-        const int64_t e = e_task + e0;
-        float m[4], v[4];
+        const int64_t e = e_task + e0, block = (e_task >> 8) + p;
+        Packed<16> m = {}, v = {};
         if (T.state_bits == 32) {
-            const Raw4<QM_F32> rm = n > 0 ? load_n<QM_F32>(T.m, e, n) : Raw4<QM_F32>{};
-            const Raw4<QM_F32> rv = n > 0 ? load_n<QM_F32>(T.v, e, n) : Raw4<QM_F32>{};
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                m[j] = elem<QM_F32>(rm, j);
-                v[j] = elem<QM_F32>(rv, j);
-            }
+            for (int j = 0; j < 4; j++)
+                if (j < n) {
+                    m.w[j] = gmem<const uint32_t>(T.m)[e + j];
+                    v.w[j] = gmem<const uint32_t>(T.v)[e + j];
+                }
         } else {
             const uint32_t qm = load_codes(T.m, e, n), qv = load_codes(T.v, e, n);
-            const int64_t block = (e_task >> 8) + p;
-            const float sm = gmem<const float>(T.m_absmax)[block] / 127.0f;
-            const float sv = gmem<const float>(T.v_absmax)[block] / 65025.0f;
+            const float sm = gmem<const float>(T.m_absmax)[block] / 127.0f, sv = gmem<const float>(T.v_absmax)[block] / 65025.0f;
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const float cv = (float)((qv >> (8 * j)) & 0xffu);
-                m[j] = j < n ? (float)(int8_t)(qm >> (8 * j)) * sm : 0.0f;
-                v[j] = j < n ? (cv * cv) * sv : 0.0f;
-            }
+            for (int j = 0; j < 4; j++)
+                if (j < n) {
+                    const float cv = (float)((qv >> (8 * j)) & 0xffu);
+                    m.w[j] = __float_as_uint((float)(int8_t)(qm >> (8 * j)) * sm);
+                    v.w[j] = __float_as_uint((cv * cv) * sv);
+                }
         }
-        store4<QM_F32>((uint64_t)m_out, out + e0, m);
-        store4<QM_F32>((uint64_t)v_out, out + e0, v);
+        store_bytes((uint64_t)m_out + out, e0 * 4, m);
+        store_bytes((uint64_t)v_out + out, e0 * 4, v);
     }
 }
 
@@ -314,7 +545,8 @@ extern "C" qm_status adamw_step(const void *host_plan, const void *dev_plan, con
     if (!isfinite(hp->lr)) return fail(QM_E_ARG, "lr must be finite");
     if (!(hp->beta1 >= 0.0 && hp->beta1 < 1.0) || !(hp->beta2 >= 0.0 && hp->beta2 < 1.0))
         return fail(QM_E_ARG, "beta1 and beta2 must lie in [0, 1)");
-    if (!((float)hp->eps > 0.0f) || !isfinite((float)hp->eps)) return fail(QM_E_ARG, "eps must be positive and finite");
+    if (!(hp->eps >= 0x1p-126) || !isfinite((float)hp->eps))   // a normal fp32 number: the reciprocal of it is finite
+        return fail(QM_E_ARG, "eps must be at least 2^-126 and finite");
     if (hp->step < 1) return fail(QM_E_ARG, "step is 1-based");
     if (hp->rounding != QM_ROUND_NEAREST && hp->rounding != QM_ROUND_STOCHASTIC)
         return fail(QM_E_ARG, "unknown rounding mode %d", hp->rounding);
@@ -339,13 +571,15 @@ extern "C" qm_status adamw_step(const void *host_plan, const void *dev_plan, con
     if (h->n_tasks32 > 0) {
         A.task_lo = 0;
         A.task_hi = (int32_t)h->n_tasks32;
-        adamw_kernel<32><<<grid_for(A.task_hi - A.task_lo), kThreads, 0, s>>>(A);
+        adamw_kernel<32, false><<<grid_for(A.task_hi - A.task_lo), kThreads, 0, s>>>(A);
         if (qm_status e = launched("AdamW")) return e;
     }
     if (h->n_tasks > h->n_tasks32) {
         A.task_lo = (int32_t)h->n_tasks32;
         A.task_hi = (int32_t)h->n_tasks;
-        adamw_kernel<8><<<grid_for(A.task_hi - A.task_lo), kThreads, 0, s>>>(A);
+        const unsigned grid = grid_for(A.task_hi - A.task_lo);
+        if (A.stochastic) adamw_kernel<8, true><<<grid, kThreads, 0, s>>>(A);
+        else adamw_kernel<8, false><<<grid, kThreads, 0, s>>>(A);
         if (qm_status e = launched("AdamW with 8-bit states")) return e;
     }
     return QM_OK;

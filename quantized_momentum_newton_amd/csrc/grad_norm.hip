@@ -36,7 +36,30 @@ __device__ __forceinline__ double wg_sum(double s) {
     return t;
 }
 
+// Elements per lane in one 16-byte access, and such accesses in a task.
+template <int DT> constexpr int kPer = 16 / kSizeOf<DT>;
+template <int DT> constexpr int kParts = kListTask / (64 * kPer<DT>);
+
+template <int DT> __device__ __forceinline__ double task_sum_full(const ListTensor &T, int64_t e_task, int lane) {
+    constexpr int N = kPer<DT>, P = kParts<DT>;
+    PackedOf<DT, N> r[P];
+    load_grad_task<DT, N, P>(T, e_task, lane, r);
+    double s[P] = {};
+#pragma unroll
+    for (int j = 0; j < N; j++)
+#pragma unroll
+        for (int p = 0; p < P; p++) {
+            const double x = (double)unpack<DT>(r[p], j);
+            s[p] += x * x;
+        }
+    double t = 0.0;
+#pragma unroll
+    for (int p = 0; p < P; p++) t += s[p];
+    return t;
+}
+
 template <int DT> __device__ __forceinline__ double task_sum(const ListTensor &T, int64_t e_task, int nvalid, int lane) {
+    if (nvalid == kListTask && grad_groups<kPer<DT>>(T)) return task_sum_full<DT>(T, e_task, lane);
     double s = 0.0;
     for (int p = 0; p < kListTask / 256; p++) {
         const int e0 = p * 256 + lane * 4;
@@ -59,7 +82,7 @@ __global__ __launch_bounds__(kThreads) void grad_sumsq_kernel(const ListTensor *
     double s = 0.0;
     for (int task = wave; task < n_tasks; task += (int)gridDim.x * kWavesPerWG) {
         const int32_t ti = __builtin_amdgcn_readfirstlane(gmem<const int32_t>(owner)[task]);
-        const ListTensor &T = gmem<const ListTensor>(tensors)[ti];
+        const ListTensor T = gmem<const ListTensor>(tensors)[ti];
         const int64_t e_task = (task - T.task_offset) * kListTask, rem = T.numel - e_task;
         const int nvalid = rem < kListTask ? (int)rem : kListTask;
         if (T.grad_dtype == QM_F32) s += task_sum<QM_F32>(T, e_task, nvalid, lane);
@@ -83,6 +106,20 @@ __global__ __launch_bounds__(kThreads) void grad_norm_finish_kernel(const double
 }
 
 template <int DT> __device__ __forceinline__ void task_scale(const ListTensor &T, int64_t e_task, int nvalid, int lane, float c) {
+    if (nvalid == kListTask && grad_groups<kPer<DT>>(T)) {
+        constexpr int N = kPer<DT>, P = kParts<DT>;
+        PackedOf<DT, N> r[P];
+        load_grad_task<DT, N, P>(T, e_task, lane, r);
+#pragma unroll
+        for (int p = 0; p < P; p++) {
+            float x[N];
+#pragma unroll
+            for (int j = 0; j < N; j++) x[j] = unpack<DT>(r[p], j) * c;
+            r[p] = pack<DT, N>(x);
+        }
+        store_grad_task<DT, N, P>(T, e_task, lane, r);
+        return;
+    }
     for (int p = 0; p < kListTask / 256; p++) {
         const int e0 = p * 256 + lane * 4;
         const int n = min(4, nvalid - e0);
@@ -103,7 +140,7 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(const ListTensor *
     const float c = *gmem<const float>(coef);
     if (c != c) return;
     const int32_t ti = __builtin_amdgcn_readfirstlane(gmem<const int32_t>(owner)[task]);
-    const ListTensor &T = gmem<const ListTensor>(tensors)[ti];
+    const ListTensor T = gmem<const ListTensor>(tensors)[ti];
     const int64_t e_task = (task - T.task_offset) * kListTask, rem = T.numel - e_task;
     const int nvalid = rem < kListTask ? (int)rem : kListTask;
     if (T.grad_dtype == QM_F32) task_scale<QM_F32>(T, e_task, nvalid, lane, c);

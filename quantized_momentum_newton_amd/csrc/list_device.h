@@ -78,10 +78,109 @@ template <int DT> __device__ __forceinline__ void store_upto4(uint64_t base, int
         if (j < n) store1<DT>(base, e + j, x[j]);
 }
 
+// N consecutive elements of one lane, still packed, loaded in 16-byte pieces
+// (8 for four 16-bit elements, 4 or 8 for N codes).  `base` is uniform over
+// the wave and `off` a 32-bit byte offset, so an access is one scalar base
+// plus one vector register.
+template <int BYTES> struct Packed { unsigned w[BYTES / 4]; };
+
+template <int BYTES> __device__ __forceinline__ Packed<BYTES> load_bytes(uint64_t base, uint32_t off) {
+    typedef unsigned v4 __attribute__((ext_vector_type(4), aligned(1)));
+    typedef unsigned v2 __attribute__((ext_vector_type(2), aligned(1)));
+    Packed<BYTES> r;
+    const char *p = gmem<const char>(base) + off;
+    if constexpr (BYTES % 16 == 0) {
+#pragma unroll
+        for (int k = 0; k < BYTES / 16; k++) {
+            const v4 v = __builtin_nontemporal_load(reinterpret_cast<const v4 *>(p + 16 * k));
+            r.w[4 * k] = v.x; r.w[4 * k + 1] = v.y; r.w[4 * k + 2] = v.z; r.w[4 * k + 3] = v.w;
+        }
+    } else if constexpr (BYTES == 8) {
+        const v2 v = __builtin_nontemporal_load(reinterpret_cast<const v2 *>(p));
+        r.w[0] = v.x; r.w[1] = v.y;
+    } else {
+        static_assert(BYTES == 4, "piece size");
+        r.w[0] = __builtin_nontemporal_load(reinterpret_cast<const u32_e *>(p));
+    }
+    return r;
+}
+template <int BYTES> __device__ __forceinline__ void store_bytes(uint64_t base, uint32_t off, const Packed<BYTES> &r) {
+    typedef unsigned v4 __attribute__((ext_vector_type(4), aligned(1)));
+    typedef unsigned v2 __attribute__((ext_vector_type(2), aligned(1)));
+    char *p = gmem<char>(base) + off;
+    if constexpr (BYTES % 16 == 0) {
+#pragma unroll
+        for (int k = 0; k < BYTES / 16; k++) {
+            const v4 v = {r.w[4 * k], r.w[4 * k + 1], r.w[4 * k + 2], r.w[4 * k + 3]};
+            __builtin_nontemporal_store(v, reinterpret_cast<v4 *>(p + 16 * k));
+        }
+    } else if constexpr (BYTES == 8) {
+        const v2 v = {r.w[0], r.w[1]};
+        __builtin_nontemporal_store(v, reinterpret_cast<v2 *>(p));
+    } else {
+        __builtin_nontemporal_store(r.w[0], reinterpret_cast<u32_e *>(p));
+    }
+}
+template <int DT> constexpr int kSizeOf = DT == QM_F32 ? 4 : 2;
+template <int DT, int N> using PackedOf = Packed<N * kSizeOf<DT>>;
+
+template <int DT, int BYTES> __device__ __forceinline__ float unpack(const Packed<BYTES> &r, int j) {
+    if constexpr (DT == QM_F32) return __uint_as_float(r.w[j]);
+    else {
+        const uint16_t h = (uint16_t)(r.w[j / 2] >> (16 * (j % 2)));
+        return DT == QM_BF16 ? bf16_val(h) : f16_val(h);
+    }
+}
+template <int DT, int N> __device__ __forceinline__ PackedOf<DT, N> pack(const float *x) {
+    PackedOf<DT, N> r;
+#pragma unroll
+    for (int j = 0; j < N; j++) {
+        if constexpr (DT == QM_F32) r.w[j] = __float_as_uint(x[j]);
+        else if (j % 2 == 0) {
+            if constexpr (DT == QM_BF16) r.w[j / 2] = bf16x2_rne(x[j], x[j + 1]);
+            else r.w[j / 2] = (unsigned)f16_rne(x[j]) | ((unsigned)f16_rne(x[j + 1]) << 16);
+        }
+    }
+    return r;
+}
+
+// Whether groups of N elements (aligned in the tensor) lie in one row.
+template <int N> __device__ __forceinline__ bool grad_groups(const ListTensor &T) {
+    return T.grad_cols == 0 || T.grad_cols % N == 0;
+}
+
 // Position in its buffer of element e of a strided gradient (numel < 2^32).
 __device__ __forceinline__ int64_t grad_pos(const ListTensor &T, int64_t e) {
     const uint32_t c = (uint32_t)T.grad_cols, u = (uint32_t)e, r = u / c;
     return (int64_t)r * T.grad_ld + (int64_t)(u - r * c);
+}
+
+// A full task's gradient: PARTS groups of N elements per lane, group p at
+// element p * 64 N + lane * N of the task.  grad_groups<N>(T) holds.
+template <int DT, int N, int PARTS>
+__device__ __forceinline__ void load_grad_task(const ListTensor &T, int64_t e_task, int lane, PackedOf<DT, N> *r) {
+    if (T.grad_cols == 0) {
+        const uint64_t base = T.grad + (uint64_t)e_task * kSizeOf<DT>;
+#pragma unroll
+        for (int p = 0; p < PARTS; p++) r[p] = load_bytes<N * kSizeOf<DT>>(base, (uint32_t)(p * 64 * N + lane * N) * kSizeOf<DT>);
+    } else {
+#pragma unroll
+        for (int p = 0; p < PARTS; p++)
+            r[p] = load_bytes<N * kSizeOf<DT>>(T.grad + (uint64_t)grad_pos(T, e_task + p * 64 * N + lane * N) * kSizeOf<DT>, 0);
+    }
+}
+
+template <int DT, int N, int PARTS>
+__device__ __forceinline__ void store_grad_task(const ListTensor &T, int64_t e_task, int lane, const PackedOf<DT, N> *r) {
+    if (T.grad_cols == 0) {
+        const uint64_t base = T.grad + (uint64_t)e_task * kSizeOf<DT>;
+#pragma unroll
+        for (int p = 0; p < PARTS; p++) store_bytes(base, (uint32_t)(p * 64 * N + lane * N) * kSizeOf<DT>, r[p]);
+    } else {
+#pragma unroll
+        for (int p = 0; p < PARTS; p++)
+            store_bytes(T.grad + (uint64_t)grad_pos(T, e_task + p * 64 * N + lane * N) * kSizeOf<DT>, 0, r[p]);
+    }
 }
 
 // Elements e .. e + n - 1 of the gradient, n <= 4.
