@@ -514,6 +514,15 @@ class GradPlan(_ListPlan):
         return torch.empty(self.workspace_bytes(), dtype=torch.uint8, device=self.device)
 
 
+def _queue(stream, plan):
+    """The given stream, or torch's current one on the plan's device, as the
+    raw handle (torch.cuda.current_stream() builds a Stream object, which
+    costs as much as a launch)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(plan.device.index)
+
+
 def _scalar(t, name, device):
     if t is None:
         return torch.empty(1, dtype=torch.float32, device=device)
@@ -529,7 +538,7 @@ def grad_norm(plan, max_norm=float("inf"), eps=1e-6, norm=None, coef=None, ws=No
     if ws is None:
         ws = plan.workspace()
     _check(_LIB.grad_norm(plan.hptr, plan.dptr, max_norm, eps, _ptr(norm), _ptr(coef), _ptr(ws), ws.numel(),
-                          _stream(stream)))
+                          _queue(stream, plan)))
     return norm, coef
 
 
@@ -537,7 +546,7 @@ def grad_scale(plan, coef, stream=None):
     """Every gradient of the plan times coef (device fp32 [1]) in place; a NaN
     coef leaves them as they are."""
     _require(coef, "coef", torch.float32, plan.device, numel=1)
-    _check(_LIB.grad_scale(plan.hptr, plan.dptr, _ptr(coef), _stream(stream)))
+    _check(_LIB.grad_scale(plan.hptr, plan.dptr, _ptr(coef), _queue(stream, plan)))
 
 
 class AdamWState:
@@ -625,7 +634,7 @@ def adamw_step(plan, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, grad_scale=Non
         _require(grad_scale, "grad_scale", torch.float32, plan.device, numel=1)
     hp = L.AdamWHparams(lr, betas[0], betas[1], eps, step, ROUNDING[rounding],
                         (step if offset is None else offset) & 0xFFFFFFFF, seed)
-    _check(_LIB.adamw_step(plan.hptr, plan.dptr, ctypes.byref(hp), _ptr(grad_scale), _stream(stream)))
+    _check(_LIB.adamw_step(plan.hptr, plan.dptr, ctypes.byref(hp), _ptr(grad_scale), _queue(stream, plan)))
 
 
 def adamw_read_state(plan, m=None, v=None, stream=None):
@@ -639,5 +648,5 @@ def adamw_read_state(plan, m=None, v=None, stream=None):
         else:
             _require(t, name, torch.float32, plan.device, numel=n)
         out.append(t)
-    _check(_LIB.adamw_read_state(plan.hptr, plan.dptr, _ptr(out[0]), _ptr(out[1]), _stream(stream)))
+    _check(_LIB.adamw_read_state(plan.hptr, plan.dptr, _ptr(out[0]), _ptr(out[1]), _queue(stream, plan)))
     return tuple(out)

@@ -241,9 +241,10 @@ __device__ __forceinline__ void task8(const ListTensor &T, int32_t tensor, int64
     }
 }
 
-// ---- a whole task: 8 elements per lane in each of 2 halves.  A lane's
-// accesses are 16 bytes of a 16-bit type or 8 of codes, and a block is 32
-// lanes of one half.
+// ---- a whole task: N = 8 elements per lane in each of H = 2 halves, a
+// block being 32 lanes of one half, or N = 4 in each of H = 4 parts, a block
+// being one part.  Eight make one 16-byte access of a 16-bit weight, four one
+// of an fp32 weight, so a weight's accesses cover whole contiguous KiB.
 
 // x / D for D = 127 or 65025, correctly rounded: quotient by the rounded
 // reciprocal, one step of its residual.  Equal to the division for every
@@ -255,25 +256,55 @@ template <int D> __device__ __forceinline__ float div_const(float x) {
     return __builtin_fmaf(__builtin_fmaf(-q, d, x), r, q);
 }
 
-// Rows are the 16-lane quarters of a wave.  Row r holds the scalars of block
-// (r & 1) * 2 + (r >> 1) of the task: after permlane16_swap the pairs (half
-// 0, half 1) of a lane's blocks come from two registers, and back.
+// Rows are the 16-lane quarters of a wave.  What is computed once a block
+// (scales, quotients) is held by the block's row: row r has block
+// (r & 1) * 2 + (r >> 1), which is where the swaps below put it.
 __device__ __forceinline__ int row_block(int lane) { return ((lane >> 4) & 1) * 2 + (lane >> 5); }
 
-// Row values to each lane's (half 0, half 1) values.
-__device__ __forceinline__ void row_spread(float x, float *h) {
-    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    h[0] = __uint_as_float(r[0]);
-    h[1] = __uint_as_float(r[1]);
+__device__ __forceinline__ void swap16(uint32_t &a, uint32_t &b) {   // odd rows of a with even rows of b
+    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+__device__ __forceinline__ void swap32(uint32_t &a, uint32_t &b) {   // upper half of a with lower half of b
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+
+// The rows' values to each lane's value per part: x[h] is that of the block
+// the lane's elements of part h are in.
+template <int H> __device__ __forceinline__ void row_spread(float row, float *x) {
+    uint32_t a = __float_as_uint(row), b = a;
+    swap16(a, b);   // a: rows 0 0 2 2, b: rows 1 1 3 3
+    if constexpr (H == 2) {
+        x[0] = __uint_as_float(a);
+        x[1] = __uint_as_float(b);
+    } else {
+        uint32_t c = a, d = b;
+        swap32(a, c);
+        swap32(b, d);
+        x[0] = __uint_as_float(a);
+        x[1] = __uint_as_float(c);
+        x[2] = __uint_as_float(b);
+        x[3] = __uint_as_float(d);
+    }
 }
 
 template <int ROR> __device__ __forceinline__ uint32_t max_ror(uint32_t x) {
     return max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x120 + ROR, 0xf, 0xf, false));
 }
-// Lanes' maxima of half 0 and half 1 to the block's maximum in its row.
-__device__ __forceinline__ uint32_t row_max(uint32_t h0, uint32_t h1) {
-    const auto r = __builtin_amdgcn_permlane16_swap(h0, h1, false, false);
-    return max_ror<1>(max_ror<2>(max_ror<4>(max_ror<8>(max((uint32_t)r[0], (uint32_t)r[1])))));
+// Each lane's maximum per part to the blocks' maxima in their rows: every
+// swap merges two registers, so all four blocks take one chain of steps.
+template <int H> __device__ __forceinline__ uint32_t row_max(uint32_t *t) {
+    if constexpr (H == 4) {
+        swap32(t[0], t[1]);
+        swap32(t[2], t[3]);
+        t[0] = max(t[0], t[1]);
+        t[1] = max(t[2], t[3]);
+    }
+    swap16(t[0], t[1]);
+    return max_ror<1>(max_ror<2>(max_ror<4>(max_ror<8>(max(t[0], t[1])))));
 }
 
 // Code of v by nearest value, as an integer.  k = floor of the hardware root
@@ -286,12 +317,14 @@ __device__ __forceinline__ uint32_t v_code_near(float y, float v) {
     return max(code, min(__float_as_uint(v), 1u));
 }
 
+template <int WDT> constexpr int kPer8 = 16 / kSizeOf<WDT>;
+
 template <int GDT, int WDT, bool SR>
 __device__ __forceinline__ void task8_full(const ListTensor &T, int32_t tensor, int64_t e_task, int lane, float c, const AdamArgs &A) {
-    constexpr int N = 8, H = 2;
+    constexpr int N = kPer8<WDT>, H = kListTask / (64 * N);
     PackedOf<GDT, N> rg[H];
     PackedOf<WDT, N> rw[H];
-    Packed<8> qm[H], qv[H];
+    Packed<N> qm[H], qv[H];
     const uint64_t bw = T.weight + (uint64_t)e_task * kSizeOf<WDT>, bm = T.m + (uint64_t)e_task, bv = T.v + (uint64_t)e_task;
     float *pm = gmem<float>(T.m_absmax) + (e_task >> 8) + row_block(lane);
     float *pv = gmem<float>(T.v_absmax) + (e_task >> 8) + row_block(lane);
@@ -299,19 +332,19 @@ __device__ __forceinline__ void task8_full(const ListTensor &T, int32_t tensor, 
     load_grad_task<GDT, N, H>(T, e_task, lane, rg);
 #pragma unroll
     for (int h = 0; h < H; h++) {
-        const uint32_t i = h * 512 + lane * N;
-        qm[h] = load_bytes<8>(bm, i);
-        qv[h] = load_bytes<8>(bv, i);
+        const uint32_t i = h * 64 * N + lane * N;
+        qm[h] = load_bytes<N>(bm, i);
+        qv[h] = load_bytes<N>(bv, i);
         rw[h] = load_bytes<N * kSizeOf<WDT>>(bw, i * kSizeOf<WDT>);
     }
     const float step = A.step * T.lr_scale, decay = A.lr * T.lr_scale * T.weight_decay;
     float step_m[H], step_v[H], m[H][N], v[H][N];
-    row_spread(div_const<127>(old_m) * A.b1, step_m);
-    row_spread(div_const<65025>(old_v) * A.b2, step_v);
+    row_spread<H>(div_const<127>(old_m) * A.b1, step_m);
+    row_spread<H>(div_const<65025>(old_v) * A.b2, step_v);
     uint32_t top_m[H] = {}, top_v[H] = {};
 #pragma unroll
     for (int h = 0; h < H; h++) {
-        const uint32_t i = h * 512 + lane * N;
+        const uint32_t i = h * 64 * N + lane * N;
         float w[N];
 #pragma unroll
         for (int j = 0; j < N; j++) {
@@ -330,7 +363,7 @@ __device__ __forceinline__ void task8_full(const ListTensor &T, int32_t tensor, 
             else store_bytes(bc, i * 2, pack<QM_F16, N>(w));
         }
     }
-    float am = __uint_as_float(row_max(top_m[0], top_m[1])), av = __uint_as_float(row_max(top_v[0], top_v[1]));
+    float am = __uint_as_float(row_max<H>(top_m)), av = __uint_as_float(row_max<H>(top_v));
     if (am < kTiny) am = 0.0f;
     if (av < kTiny) av = 0.0f;
     if ((lane & 15) == 0) {
@@ -338,18 +371,18 @@ __device__ __forceinline__ void task8_full(const ListTensor &T, int32_t tensor, 
         *pv = av;
     }
     float im[H], iv[H];
-    row_spread(am > 0.0f ? 127.0f / am : 0.0f, im);
-    row_spread(av > 0.0f ? 65025.0f / av : 0.0f, iv);
+    row_spread<H>(am > 0.0f ? 127.0f / am : 0.0f, im);
+    row_spread<H>(av > 0.0f ? 65025.0f / av : 0.0f, iv);
     // blocks whose codes are all 0: a maximum that is not finite, or v's is 0
-    float keep_m[H] = {1.0f, 1.0f}, keep_v[H] = {1.0f, 1.0f};
+    float keep_m[H] = {}, keep_v[H] = {};
     const bool odd = __any(!(am < INFINITY) || !(av < INFINITY) || av == 0.0f);
     if (odd) {
-        row_spread(am < INFINITY ? 1.0f : 0.0f, keep_m);
-        row_spread(av < INFINITY && av > 0.0f ? 1.0f : 0.0f, keep_v);
+        row_spread<H>(am < INFINITY ? 1.0f : 0.0f, keep_m);
+        row_spread<H>(av < INFINITY && av > 0.0f ? 1.0f : 0.0f, keep_v);
     }
 #pragma unroll
     for (int h = 0; h < H; h++) {
-        const uint32_t i = h * 512 + lane * N;
+        const uint32_t i = h * 64 * N + lane * N;
         uint32_t cm[N], cv[N];
         if constexpr (SR) {
             uint32_t word[N];
@@ -372,15 +405,15 @@ __device__ __forceinline__ void task8_full(const ListTensor &T, int32_t tensor, 
                 cv[j] = v_code_near(v[h][j] * iv[h], v[h][j]);
             }
         }
-        Packed<8> om, ov;
+        Packed<N> om, ov;
 #pragma unroll
-        for (int k = 0; k < 2; k++) {
+        for (int k = 0; k < N / 4; k++) {
             om.w[k] = pack_low_bytes(cm[4 * k], cm[4 * k + 1], cm[4 * k + 2], cm[4 * k + 3]);
             ov.w[k] = pack_low_bytes(cv[4 * k], cv[4 * k + 1], cv[4 * k + 2], cv[4 * k + 3]);
         }
         if (odd) {
 #pragma unroll
-            for (int k = 0; k < 2; k++) {
+            for (int k = 0; k < N / 4; k++) {
                 if (keep_m[h] == 0.0f) om.w[k] = 0;
                 if (keep_v[h] == 0.0f) ov.w[k] = 0;
             }
@@ -401,7 +434,7 @@ __device__ __forceinline__ void run_task(const ListTensor &T, int32_t tensor, in
         else task32<GDT, WDT>(T, e_task, nvalid, lane, c, A);
     }
     else {
-        if (nvalid == kListTask && grad_groups<8>(T)) task8_full<GDT, WDT, SR>(T, tensor, e_task, lane, c, A);
+        if (nvalid == kListTask && grad_groups<kPer8<WDT>>(T)) task8_full<GDT, WDT, SR>(T, tensor, e_task, lane, c, A);
         else task8<GDT, WDT>(T, tensor, e_task, nvalid, lane, c, A);
     }
 }
