@@ -155,32 +155,43 @@ __device__ __forceinline__ int64_t grad_pos(const ListTensor &T, int64_t e) {
     return (int64_t)r * T.grad_ld + (int64_t)(u - r * c);
 }
 
-// A full task's gradient: PARTS groups of N elements per lane, group p at
-// element p * 64 N + lane * N of the task.  grad_groups<N>(T) holds.
-template <int DT, int N, int PARTS>
-__device__ __forceinline__ void load_grad_task(const ListTensor &T, int64_t e_task, int lane, PackedOf<DT, N> *r) {
+// Calls access(p, base, off) for a lane's groups of N elements in a full task
+// of the gradient, group p at element p * 64 N + lane * N: base and byte
+// offset of its first element.  grad_groups<N>(T) holds.  Rows of a task's
+// length or more: a task meets at most one row end, so one scalar division
+// serves the wave (the other branch divides per group).
+template <int DT, int N, int PARTS, typename Access>
+__device__ __forceinline__ void grad_task(const ListTensor &T, int64_t e_task, int lane, Access access) {
+    constexpr int S = kSizeOf<DT>;
+    const uint32_t cols = (uint32_t)T.grad_cols, at = (uint32_t)e_task;
+    const int64_t jump = T.grad_ld - T.grad_cols;
     if (T.grad_cols == 0) {
-        const uint64_t base = T.grad + (uint64_t)e_task * kSizeOf<DT>;
 #pragma unroll
-        for (int p = 0; p < PARTS; p++) r[p] = load_bytes<N * kSizeOf<DT>>(base, (uint32_t)(p * 64 * N + lane * N) * kSizeOf<DT>);
+        for (int p = 0; p < PARTS; p++) access(p, T.grad + (uint64_t)e_task * S, (uint32_t)(p * 64 + lane) * N * S);
+    } else if (T.grad_cols >= kListTask && jump < 1 << 28) {
+        const uint32_t row = at / cols, col = at - row * cols;
+        const uint64_t base = T.grad + (uint64_t)((int64_t)row * T.grad_ld + col) * S;
+#pragma unroll
+        for (int p = 0; p < PARTS; p++) {
+            const uint32_t i = (p * 64 + lane) * N;
+            access(p, base, (i + (col + i >= cols ? (uint32_t)jump : 0u)) * S);
+        }
     } else {
 #pragma unroll
-        for (int p = 0; p < PARTS; p++)
-            r[p] = load_bytes<N * kSizeOf<DT>>(T.grad + (uint64_t)grad_pos(T, e_task + p * 64 * N + lane * N) * kSizeOf<DT>, 0);
+        for (int p = 0; p < PARTS; p++) {
+            const uint32_t u = at + (p * 64 + lane) * N, row = u / cols;
+            access(p, T.grad + (uint64_t)((int64_t)row * T.grad_ld + (int64_t)(u - row * cols)) * S, 0);
+        }
     }
 }
 
 template <int DT, int N, int PARTS>
+__device__ __forceinline__ void load_grad_task(const ListTensor &T, int64_t e_task, int lane, PackedOf<DT, N> *r) {
+    grad_task<DT, N, PARTS>(T, e_task, lane, [&](int p, uint64_t base, uint32_t off) { r[p] = load_bytes<N * kSizeOf<DT>>(base, off); });
+}
+template <int DT, int N, int PARTS>
 __device__ __forceinline__ void store_grad_task(const ListTensor &T, int64_t e_task, int lane, const PackedOf<DT, N> *r) {
-    if (T.grad_cols == 0) {
-        const uint64_t base = T.grad + (uint64_t)e_task * kSizeOf<DT>;
-#pragma unroll
-        for (int p = 0; p < PARTS; p++) store_bytes(base, (uint32_t)(p * 64 * N + lane * N) * kSizeOf<DT>, r[p]);
-    } else {
-#pragma unroll
-        for (int p = 0; p < PARTS; p++)
-            store_bytes(T.grad + (uint64_t)grad_pos(T, e_task + p * 64 * N + lane * N) * kSizeOf<DT>, 0, r[p]);
-    }
+    grad_task<DT, N, PARTS>(T, e_task, lane, [&](int p, uint64_t base, uint32_t off) { store_bytes(base, off, r[p]); });
 }
 
 // Elements e .. e + n - 1 of the gradient, n <= 4.
