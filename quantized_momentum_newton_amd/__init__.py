@@ -523,10 +523,20 @@ def _queue(stream, plan):
     return torch._C._cuda_getCurrentRawStream(plan.device.index)
 
 
-def _scalar(t, name, device):
+def _new(count, dtype, plan, stream):
+    """A new tensor on the plan's device, in the pool of the stream that will
+    write it (memory freed on another stream may still be in use there)."""
+    if stream is None:
+        return torch.empty(count, dtype=dtype, device=plan.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(count, dtype=dtype, device=plan.device)
+
+
+def _out(t, name, count, plan, stream):
+    """t if it is a contiguous fp32 tensor of `count` elements, a new one for None."""
     if t is None:
-        return torch.empty(1, dtype=torch.float32, device=device)
-    _require(t, name, torch.float32, device, numel=1)
+        return _new(count, torch.float32, plan, stream)
+    _require(t, name, torch.float32, plan.device, numel=count)
     return t
 
 
@@ -534,9 +544,9 @@ def grad_norm(plan, max_norm=float("inf"), eps=1e-6, norm=None, coef=None, ws=No
     """Norm of all gradients of the plan and min(1, max_norm / (norm + eps)),
     NaN where the norm is not finite, as device fp32 [1] tensors (given or
     new): (norm, coef)."""
-    norm, coef = _scalar(norm, "norm", plan.device), _scalar(coef, "coef", plan.device)
+    norm, coef = _out(norm, "norm", 1, plan, stream), _out(coef, "coef", 1, plan, stream)
     if ws is None:
-        ws = plan.workspace()
+        ws = _new(plan.workspace_bytes(), torch.uint8, plan, stream)
     _check(_LIB.grad_norm(plan.hptr, plan.dptr, max_norm, eps, _ptr(norm), _ptr(coef), _ptr(ws), ws.numel(),
                           _queue(stream, plan)))
     return norm, coef
@@ -641,12 +651,6 @@ def adamw_read_state(plan, m=None, v=None, stream=None):
     """The values the states stand for: fp32 [256 * plan.n_blocks] tensors
     (given or new); plan.view(m, i) is tensor i's part.  Returns (m, v)."""
     n = plan.n_blocks * BLOCK
-    out = []
-    for t, name in ((m, "m"), (v, "v")):
-        if t is None:
-            t = torch.empty(n, dtype=torch.float32, device=plan.device)
-        else:
-            _require(t, name, torch.float32, plan.device, numel=n)
-        out.append(t)
-    _check(_LIB.adamw_read_state(plan.hptr, plan.dptr, _ptr(out[0]), _ptr(out[1]), _queue(stream, plan)))
-    return tuple(out)
+    m, v = _out(m, "m", n, plan, stream), _out(v, "v", n, plan, stream)
+    _check(_LIB.adamw_read_state(plan.hptr, plan.dptr, _ptr(m), _ptr(v), _queue(stream, plan)))
+    return m, v

@@ -41,10 +41,13 @@ struct AdamArgs {
     int32_t stochastic;
 };
 
-// New weight from the new moments.  The root and the quotient are the
-// hardware's to within an ulp or two: the update is a small part of w.
+// New weight from the new moments.  The root and the reciprocal are the
+// hardware's, within an ulp; the root takes subnormal numbers for 0, so v
+// below 2^-96 is scaled by 2^64.  denom >= eps >= 2^-126 has a finite reciprocal.
 __device__ __forceinline__ float new_weight(float w, float m, float v, float step, float decay, const AdamArgs &A) {
-    const float denom = __builtin_fmaf(__builtin_amdgcn_sqrtf(v), A.root, A.eps);
+    const bool tiny = v < 0x1p-96f;
+    const float r = __builtin_amdgcn_sqrtf(v * (tiny ? 0x1p64f : 1.0f));
+    const float denom = __builtin_fmaf(r, tiny ? A.root * 0x1p-32f : A.root, A.eps);
     return __builtin_fmaf(-step, m * __builtin_amdgcn_rcpf(denom), __builtin_fmaf(-decay, w, w));
 }
 
@@ -307,9 +310,9 @@ template <int H> __device__ __forceinline__ uint32_t row_max(uint32_t *t) {
     return max_ror<1>(max_ror<2>(max_ror<4>(max_ror<8>(max(t[0], t[1])))));
 }
 
-// Code of v by nearest value, as an integer.  k = floor of the hardware root
-// (within an ulp) is floor(sqrt y) or its neighbour next to a perfect
-// square, where both give the same code; y > 2^-149 codes at least 1.
+// Code of v by nearest value.  k = floor of the hardware root (within an ulp)
+// is floor(sqrt y) or its neighbour next to a perfect square, where both give
+// the same code; v > 0 codes at least 1.
 __device__ __forceinline__ uint32_t v_code_near(float y, float v) {
     const float k = floorf(__builtin_amdgcn_sqrtf(y));
     const float d = __builtin_fmaf(-k, k, y);
@@ -318,24 +321,24 @@ __device__ __forceinline__ uint32_t v_code_near(float y, float v) {
 }
 
 // The same by a 16-bit and a 15-bit random number (the two halves of the
-// element's word).  The comparisons are the definition's times 2^16 and 2^15:
-// x - k and y - k^2 have at most 24 bits, as has a 15-bit number times 2k + 1.
-__device__ __forceinline__ uint32_t m_code_random(float x, uint32_t word) {
-    const float k = floorf(x);
-    const int code = (int)k + ((float)(word >> 16) < (x - k) * 0x1p16f ? 1 : 0);
-    return (uint32_t)min(code, 127);   // x >= -127 (1 + 2^-23) rounds up unless its number is past 1 - 2^-17
+// element's word).
+//
+// m: with x' = 2^16 x exact and u a whole number, u < 2^16 frac(x) is
+// u < ceil(x') - 2^16 floor(x), so the code is the sum ceil(x') - u + 65535
+// without its 16 low bits; x past 127 by its own rounding is held back.
+// Returns the code in byte 2.
+__device__ __forceinline__ uint32_t m_code_random(float x16, uint32_t word) {
+    const int s = (int)ceilf(x16) - (int)(word >> 16) + 65535;
+    return (uint32_t)min(s, 127 * 65536 + 65535);
 }
+// v: k = floor of the hardware root is floor(sqrt y) or, next below a square,
+// one above (checked for every y up to 65026); there y - k^2 < 0 keeps k,
+// as the exact comparison does by a margin of 2 (it misses 2 k + 1 by less
+// than 2^-15 of it).  u (2k + 1) has 24 bits.
 __device__ __forceinline__ uint32_t v_code_random(float y, float v, uint32_t word) {
-    // k = floor(sqrt y), or its neighbour where y is within 2 k ulp(k) of a
-    // square.  One above: d < 0 keeps k, as the exact comparison does there, by
-    // a margin of 2 (it misses 2k + 1 by less than 2^-15 of it).  One below:
-    // the first sum gives the square's root, and the exact comparison asks
-    // for one more only where its random number is 0.
     const float k = floorf(__builtin_amdgcn_sqrtf(y));
-    const float d = __builtin_fmaf(-k, k, y), t = 2.0f * k + 1.0f;
-    const float lhs = (float)(word & 0x7fffu) * t, rhs = d * 0x1p15f;
-    uint32_t code = (uint32_t)(int)k + (lhs < rhs ? 1u : 0u);
-    code += __builtin_fmaf(lhs, 0x1p16f, t) < d ? 1u : 0u;   // random number 0 and d > 2k + 1
+    const float d = __builtin_fmaf(-k, k, y), t = __builtin_fmaf(k, 0x1p-14f, 0x1p-15f);   // 2^-15 (2k + 1)
+    const uint32_t code = (uint32_t)(int)k + ((float)(word & 0x7fffu) * t < d ? 1u : 0u);
     return min(max(code, min(__float_as_uint(v), 1u)), 255u);
 }
 
@@ -418,7 +421,7 @@ __device__ __forceinline__ void task8_full(const ListTensor &T, int32_t tensor, 
                 philox4x32_10(low + k, high, A.offset, (uint32_t)tensor, (uint32_t)A.seed, (uint32_t)(A.seed >> 32), word + 4 * k);
 #pragma unroll
             for (int j = 0; j < N; j++) {
-                cm[j] = m_code_random(m[h][j] * im[h], word[j]);
+                cm[j] = m_code_random(m[h][j] * (im[h] * 0x1p16f), word[j]) >> 16;
                 cv[j] = v_code_random(v[h][j] * iv[h], v[h][j], word[j]);
             }
         } else {

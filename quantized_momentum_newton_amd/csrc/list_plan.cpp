@@ -3,7 +3,7 @@
 #include <math.h>
 #include <string.h>
 
-#include <new>
+#include <exception>
 #include <vector>
 
 #include "internal.h"
@@ -182,7 +182,7 @@ qm_status encode(const Tensor *tensors, int32_t n, int kind, void *host_blob, si
         memcpy(base + h.off_tensors, table.data(), table.size() * sizeof(ListTensor));
         *inout_blob_bytes = (size_t)h.total_bytes;
         return QM_OK;
-    } catch (const std::bad_alloc &) {
+    } catch (const std::exception &) {   // no C++ exception leaves a C entry
         return fail(QM_E_ARG, "out of host memory for a list of %d tensors", n);
     }
 }

@@ -190,6 +190,26 @@ def test_mixed_list_and_state_values():
     assert torch.all(m[~inside] == 0) and torch.all(v[~inside] == 0)
 
 
+@pytest.mark.parametrize("eps", [1e-30, 1e-12])
+def test_roots_of_subnormal_moments(eps):
+    """v far below fp32's normal range next to a small eps: the update from
+    the m and v that the step wrote, within the bound's share of the root,
+    the reciprocal and the products."""
+    n = 3000
+    p = Param(n, 32, torch.float32, torch.float32, 15, decay=0.0, zero=True)
+    p.weight.zero_()
+    p.grad.copy_(torch.logspace(-22, -12, n))
+    plan = q.AdamWPlan([p.tuple()])
+    q.adamw_step(plan, 1, lr=1.0, betas=(0.9, 0.999), eps=eps)
+    torch.cuda.synchronize()
+    m, v = p.state.m.double().cpu().numpy(), p.state.v.double().cpu().numpy()
+    want = -(m / 0.1) / (np.sqrt(v / 0.001) + eps)
+    got = p.weight.double().cpu().numpy()
+    assert np.any((v > 0) & (v < 2.0 ** -126))
+    # 1 - beta to a part in 2^50, the constants' roundings in the 24 u
+    assert np.all(np.abs(got - want) <= 24 * U * np.abs(want) + SUBNORMAL[torch.float32])
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_nan_factor_writes_nothing(bits):
     p = Param(5000, bits, torch.bfloat16, torch.float32, 77)
