@@ -455,8 +455,8 @@ __device__ __forceinline__ void task8_full(const ListTensor &T, int32_t tensor, 
 
 template <int BITS, bool SR, int GDT, int WDT>
 __device__ __forceinline__ void run_task(const ListTensor &T, int32_t tensor, int64_t lt, int lane, float c, const AdamArgs &A) {
-    const int64_t e_task = lt * kListTask, rem = T.numel - e_task;
-    const int nvalid = rem < kListTask ? (int)rem : kListTask;
+    int nvalid;
+    const int64_t e_task = task_start(T, lt, nvalid);
     if constexpr (BITS == 32) {
         if (nvalid == kListTask && grad_groups<4>(T)) task32_full<GDT, WDT>(T, e_task, lane, c, A);
         else task32<GDT, WDT>(T, e_task, nvalid, lane, c, A);
@@ -505,9 +505,8 @@ __global__ __launch_bounds__(kThreads) void adamw_read_kernel(const ListTensor *
     if (task >= n_tasks) return;
     const int32_t ti = __builtin_amdgcn_readfirstlane(gmem<const int32_t>(owner)[task]);
     const ListTensor T = gmem<const ListTensor>(tensors)[ti];
-    const int64_t e_task = (task - T.task_offset) * kListTask;
-    const int64_t rem = T.numel - e_task;
-    const int nvalid = rem < kListTask ? (int)rem : kListTask;
+    int nvalid;
+    const int64_t e_task = task_start(T, task - T.task_offset, nvalid);
     const uint64_t from = (is_v ? T.v : T.m) + (uint64_t)e_task * (T.state_bits == 32 ? 4 : 1);
     const uint64_t to = (uint64_t)(is_v ? v_out : m_out) + (uint64_t)(T.block_offset * kBlock + e_task) * 4;
     constexpr int P = kListTask / 256;

@@ -87,8 +87,8 @@ __global__ __launch_bounds__(kThreads) void grad_sumsq_kernel(const ListTensor *
     for (int task = wave; task < n_tasks; task += (int)gridDim.x * kWavesPerWG) {
         const int32_t ti = __builtin_amdgcn_readfirstlane(gmem<const int32_t>(owner)[task]);
         const ListTensor T = gmem<const ListTensor>(tensors)[ti];
-        const int64_t e_task = (task - T.task_offset) * kListTask, rem = T.numel - e_task;
-        const int nvalid = rem < kListTask ? (int)rem : kListTask;
+        int nvalid;
+        const int64_t e_task = task_start(T, task - T.task_offset, nvalid);
         if (T.grad_dtype == QM_F32) s += task_sum<QM_F32>(T, e_task, nvalid, lane);
         else if (T.grad_dtype == QM_BF16) s += task_sum<QM_BF16>(T, e_task, nvalid, lane);
         else s += task_sum<QM_F16>(T, e_task, nvalid, lane);
@@ -151,8 +151,8 @@ __global__ __launch_bounds__(kScaleThreads) void grad_scale_kernel(const ListTen
     if (c != c) return;
     const int32_t ti = __builtin_amdgcn_readfirstlane(gmem<const int32_t>(owner)[task]);
     const ListTensor T = gmem<const ListTensor>(tensors)[ti];
-    const int64_t e_task = (task - T.task_offset) * kListTask, rem = T.numel - e_task;
-    const int nvalid = rem < kListTask ? (int)rem : kListTask;
+    int nvalid;
+    const int64_t e_task = task_start(T, task - T.task_offset, nvalid);
     if (T.grad_dtype == QM_F32) task_scale<QM_F32>(T, e_task, nvalid, lane, c);
     else if (T.grad_dtype == QM_BF16) task_scale<QM_BF16>(T, e_task, nvalid, lane, c);
     else task_scale<QM_F16>(T, e_task, nvalid, lane, c);

@@ -144,6 +144,14 @@ template <int DT, int N> __device__ __forceinline__ PackedOf<DT, N> pack(const f
     return r;
 }
 
+// First element of the tensor's task k, and how many it has: 1024, or at most
+// 256 at the tensor's end.
+__device__ __forceinline__ int64_t task_start(const ListTensor &T, int64_t k, int &count) {
+    const int64_t full = T.numel / kListTask, e = list_task_start(T.numel, k);
+    count = k < full ? kListTask : (int)min(T.numel - e, (int64_t)256);
+    return e;
+}
+
 // Whether groups of N elements (aligned in the tensor) lie in one row.
 template <int N> __device__ __forceinline__ bool grad_groups(const ListTensor &T) {
     return T.grad_cols == 0 || T.grad_cols % N == 0;

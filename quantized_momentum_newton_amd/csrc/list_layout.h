@@ -2,8 +2,11 @@
 // norm read on the device.  The host encoder (list_plan.cpp) writes it, the
 // caller copies it verbatim.
 //
-// The work is cut into tasks of up to 1024 consecutive elements (four
-// 256-element blocks) of one tensor, one wave64 each.  Tasks of tensors with
+// The work is cut into tasks of one tensor's consecutive elements, one wave64
+// each: 1024 (four 256-element blocks), and what is left at the tensor's end
+// one block a task, so that no wave goes through several partly filled blocks
+// one after the other (a list of small tensors is bound by that latency).
+// Tasks of tensors with
 // 32-bit states come first, then those with 8-bit states, each in list
 // order, so that one launch covers one kind.  A table names every task's
 // tensor (4 bytes per 1024 elements, one scalar load instead of a search).
@@ -40,6 +43,13 @@ struct ListTensor {
     float lr_scale, weight_decay;
     int32_t pad[2];
 };
+
+// Tasks of a tensor of n elements, and the first element of task k.
+constexpr int64_t list_tasks(int64_t n) { return n / kListTask + (n % kListTask + 255) / 256; }
+constexpr int64_t list_task_start(int64_t n, int64_t k) {
+    const int64_t full = n / kListTask;
+    return k < full ? k * kListTask : full * kListTask + (k - full) * 256;
+}
 
 static_assert(sizeof(ListHeader) == 72, "list header layout");
 static_assert(sizeof(ListTensor) == 128, "list tensor layout");
