@@ -38,7 +38,6 @@ struct AdamArgs {
     float root, eps;           // 1 / sqrt(1 - beta2^t), eps
     uint64_t seed;
     uint32_t offset;
-    int32_t stochastic;
 };
 
 // New weight from the new moments.  The root and the reciprocal are the
@@ -52,41 +51,35 @@ __device__ __forceinline__ float new_weight(float w, float m, float v, float ste
 }
 
 template <int DT> __device__ __forceinline__ void store_weight(const ListTensor &T, int64_t e, int n, const float *w) {
-    store_upto4<DT>(T.weight, e, n, w);
+    store_edge<DT>(T.weight, e, n, w);
     if (T.copy == 0) return;
-    if (T.copy_dtype == QM_BF16) store_upto4<QM_BF16>(T.copy, e, n, w);
-    else store_upto4<QM_F16>(T.copy, e, n, w);
-}
-
-template <int DT> __device__ __forceinline__ Raw4<DT> load_n(uint64_t base, int64_t e, int n) {
-    return n == 4 ? load4<DT>(base, e) : load_upto4<DT>(base, e, n);
+    if (T.copy_dtype == QM_BF16) store_edge<QM_BF16>(T.copy, e, n, w);
+    else store_edge<QM_F16>(T.copy, e, n, w);
 }
 
 // ------------------------------------------------------------ 32-bit states
 
+// At most one block.
 template <int GDT, int WDT>
 __device__ __forceinline__ void task32(const ListTensor &T, int64_t e_task, int nvalid, int lane, float c, const AdamArgs &A) {
     const float step = A.step * T.lr_scale, decay = A.lr * T.lr_scale * T.weight_decay;
-    for (int p = 0; p < kListTask / 256; p++) {
-        const int e0 = p * 256 + lane * 4;
-        const int n = min(4, nvalid - e0);
-        if (n <= 0) continue;
-        const int64_t e = e_task + e0;
-        const Raw4<GDT> rg = load_grad<GDT>(T, e, n);
-        const Raw4<WDT> rw = load_n<WDT>(T.weight, e, n);
-        const Raw4<QM_F32> rm = load_n<QM_F32>(T.m, e, n), rv = load_n<QM_F32>(T.v, e, n);
-        float m[4], v[4], w[4];
+    const int n = min(4, nvalid - lane * 4);
+    if (n <= 0) return;
+    const int64_t e = e_task + lane * 4;
+    const PackedOf<GDT, 4> rg = load_grad<GDT>(T, e, n);
+    const PackedOf<WDT, 4> rw = load_edge<WDT>(T.weight, e, n);
+    const Packed<16> rm = load_edge<QM_F32>(T.m, e, n), rv = load_edge<QM_F32>(T.v, e, n);
+    float m[4], v[4], w[4];
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const float g = elem<GDT>(rg, j) * c;
-            m[j] = A.b1 * elem<QM_F32>(rm, j) + A.omb1 * g;
-            v[j] = A.b2 * elem<QM_F32>(rv, j) + A.omb2 * (g * g);
-            w[j] = new_weight(elem<WDT>(rw, j), m[j], v[j], step, decay, A);
-        }
-        store_upto4<QM_F32>(T.m, e, n, m);
-        store_upto4<QM_F32>(T.v, e, n, v);
-        store_weight<WDT>(T, e, n, w);
+    for (int j = 0; j < 4; j++) {
+        const float g = unpack<GDT>(rg, j) * c;
+        m[j] = A.b1 * unpack<QM_F32>(rm, j) + A.omb1 * g;
+        v[j] = A.b2 * unpack<QM_F32>(rv, j) + A.omb2 * (g * g);
+        w[j] = new_weight(unpack<WDT>(rw, j), m[j], v[j], step, decay, A);
     }
+    store_edge<QM_F32>(T.m, e, n, m);
+    store_edge<QM_F32>(T.v, e, n, v);
+    store_weight<WDT>(T, e, n, w);
 }
 
 // A whole task with every load issued before the arithmetic: 4 elements per
@@ -150,105 +143,6 @@ __device__ __forceinline__ void store_codes(uint64_t base, int64_t e, int n, uin
         if (j < n) *gmem<uint8_t>(base + (uint64_t)(e + j)) = (uint8_t)(q >> (8 * j));
 }
 
-// Largest of the bit patterns over the wave.  Patterns of values without
-// their sign order as the values do, with infinity above every number and
-// NaN above that.
-__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
-#pragma unroll
-    for (int k = 1; k < 64; k <<= 1) x = max(x, (uint32_t)xor_lanes((int)x, k));
-    return x;
-}
-
-// m's code: x = m (127 / absmax) rounded, |x| <= 127 (1 + 2^-23).
-__device__ __forceinline__ int m_code(float x, uint32_t word, int stochastic) {
-    if (!stochastic) return (int)rintf(x);
-    const float k = floorf(x);
-    const float up = (float)(word >> 16) * 0x1p-16f < x - k ? 1.0f : 0.0f;
-    return (int)fminf(fmaxf(k + up, -127.0f), 127.0f);
-}
-
-// v's code: y = v (65025 / max) in [0, 65025 (1 + 2^-23)].  k = floor(sqrt y)
-// exactly (k and k^2 are whole numbers below 2^17, y - k^2 is exact); the
-// code is k + 1 where y - k^2 is past u (2k + 1), u = 1/2 for nearest.  u
-// has 15 bits and 2k + 1 at most 9, so their product is exact.
-__device__ __forceinline__ int v_code(float y, float v, uint32_t word, int stochastic) {
-    float k = floorf(sqrtf(y));
-    float d = y - k * k;
-    if (d < 0.0f) {   // the root rounded up to a whole number
-        k -= 1.0f;
-        d = y - k * k;
-    }
-    const float u = stochastic ? (float)(word & 0x7fffu) * 0x1p-15f : 0.5f;
-    const int code = (int)k + (d > u * (2.0f * k + 1.0f) ? 1 : 0);
-    return v > 0.0f ? max(1, min(code, 255)) : 0;
-}
-
-template <int GDT, int WDT>
-__device__ __forceinline__ void task8(const ListTensor &T, int32_t tensor, int64_t e_task, int nvalid, int lane, float c,
-                                      const AdamArgs &A) {
-    const float step = A.step * T.lr_scale, decay = A.lr * T.lr_scale * T.weight_decay;
-    for (int p = 0; p < kListTask / 256; p++) {
-        if (p * 256 >= nvalid) break;
-        const int e0 = p * 256 + lane * 4;
-        const int n = max(0, min(4, nvalid - e0));
-        const int64_t e = e_task + e0, block = (e_task >> 8) + p;
-        Raw4<GDT> rg = {};
-        Raw4<WDT> rw = {};
-        uint32_t qm = 0, qv = 0;
-        if (n > 0) {
-            rg = load_grad<GDT>(T, e, n);
-            rw = load_n<WDT>(T.weight, e, n);
-            qm = load_codes(T.m, e, n);
-            qv = load_codes(T.v, e, n);
-        }
-        float *pm = gmem<float>(T.m_absmax) + block, *pv = gmem<float>(T.v_absmax) + block;
-        const float step_m = (*pm / 127.0f) * A.b1, step_v = (*pv / 65025.0f) * A.b2;
-        float m[4], v[4], w[4];
-        uint32_t top_m = 0, top_v = 0;
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const float g = elem<GDT>(rg, j) * c;
-            const float cv = (float)((qv >> (8 * j)) & 0xffu);
-            m[j] = (float)(int8_t)(qm >> (8 * j)) * step_m + A.omb1 * g;
-            v[j] = (cv * cv) * step_v + A.omb2 * (g * g);
-            w[j] = new_weight(elem<WDT>(rw, j), m[j], v[j], step, decay, A);
-            if (j < n) {
-                top_m = max(top_m, __float_as_uint(m[j]) & 0x7fffffffu);
-                top_v = max(top_v, __float_as_uint(v[j]) & 0x7fffffffu);
-            }
-        }
-        store_weight<WDT>(T, e, n, w);
-        float am = __uint_as_float(wave_max(top_m)), av = __uint_as_float(wave_max(top_v));
-        if (am < kTiny) am = 0.0f;
-        if (av < kTiny) av = 0.0f;
-        const float im = am > 0.0f ? 127.0f / am : 0.0f, iv = av > 0.0f ? 65025.0f / av : 0.0f;
-        uint32_t word[4] = {};
-        if (A.stochastic) {
-            const uint64_t quad = (uint64_t)e >> 2;
-            philox4x32_10((uint32_t)quad, (uint32_t)(quad >> 32), A.offset, (uint32_t)tensor, (uint32_t)A.seed,
-                          (uint32_t)(A.seed >> 32), word);
-        }
-        uint32_t nm = 0, nv = 0;
-        if (am < INFINITY)
-#pragma unroll
-            for (int j = 0; j < 4; j++) nm |= (uint32_t)(m_code(m[j] * im, word[j], A.stochastic) & 0xff) << (8 * j);
-        if (av < INFINITY && av > 0.0f)
-#pragma unroll
-            for (int j = 0; j < 4; j++) nv |= (uint32_t)v_code(v[j] * iv, v[j], word[j], A.stochastic) << (8 * j);
-        store_codes(T.m, e, n, nm);
-        store_codes(T.v, e, n, nv);
-        if (lane == 0) {
-            *pm = am;
-            *pv = av;
-        }
-    }
-}
-
-// ---- a whole task: N = 8 elements per lane in each of H = 2 halves, a
-// block being 32 lanes of one half, or N = 4 in each of H = 4 parts, a block
-// being one part.  Eight make one 16-byte access of a 16-bit weight, four one
-// of an fp32 weight, so a weight's accesses cover whole contiguous KiB.
-
 // x / D for D = 127 or 65025, correctly rounded: quotient by the rounded
 // reciprocal, one step of its residual.  Equal to the division for every
 // significand (checked exhaustively) and every x that a block maximum can be
@@ -310,6 +204,19 @@ template <int H> __device__ __forceinline__ uint32_t row_max(uint32_t *t) {
     return max_ror<1>(max_ror<2>(max_ror<4>(max_ror<8>(max(t[0], t[1])))));
 }
 
+// Maximum over the wave.
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+    x = max_ror<1>(max_ror<2>(max_ror<4>(max_ror<8>(x))));
+    uint32_t y = x;
+    swap16(x, y);
+    x = y = max(x, y);
+    swap32(x, y);
+    return max(x, y);
+}
+
+// y = v (65025 / max) lies in [0, 65025 (1 + 2^-23)], x = m (127 / max) in
+// +-127 (1 + 2^-23).
+//
 // Code of v by nearest value.  k = floor of the hardware root (within an ulp)
 // is floor(sqrt y) or its neighbour next to a perfect square, where both give
 // the same code; v > 0 codes at least 1.
@@ -342,6 +249,101 @@ __device__ __forceinline__ uint32_t v_code_random(float y, float v, uint32_t wor
     return min(max(code, min(__float_as_uint(v), 1u)), 255u);
 }
 
+// Codes of N elements of a block: im = 127 / (max of |m|), iv = 65025 / (max
+// of v), 0 for a block of zeros; the elements' group of four number `group`
+// (64 bits in two words) is the counter of their random words.
+template <bool SR, int N>
+__device__ __forceinline__ void code_group(const float *m, const float *v, float im, float iv, uint32_t group_lo, uint32_t group_hi,
+                                           uint32_t tensor, const AdamArgs &A, Packed<N> &om, Packed<N> &ov) {
+    uint32_t cm[N], cv[N];
+    if constexpr (SR) {
+        uint32_t word[N];
+#pragma unroll
+        for (int k = 0; k < N / 4; k++)
+            philox4x32_10(group_lo + k, group_hi, A.offset, tensor, (uint32_t)A.seed, (uint32_t)(A.seed >> 32), word + 4 * k);
+        const float im16 = im * 0x1p16f;
+#pragma unroll
+        for (int j = 0; j < N; j++) {
+            cm[j] = m_code_random(m[j] * im16, word[j]);
+            cv[j] = v_code_random(v[j] * iv, v[j], word[j]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; j++) {
+            // adding 1.5 * 2^23 rounds to a whole number, ties to even: the sum's low byte is the code
+            cm[j] = __float_as_uint(m[j] * im + 12582912.0f);
+            cv[j] = v_code_near(v[j] * iv, v[j]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < N; k += 4) {
+        om.w[k / 4] = pack_bytes<SR ? 2 : 0>(cm[k], cm[k + 1], cm[k + 2], cm[k + 3]);
+        ov.w[k / 4] = pack_bytes<0>(cv[k], cv[k + 1], cv[k + 2], cv[k + 3]);
+    }
+}
+
+// New moments of N elements, their largest magnitudes into tm and tv (NaN if
+// one is), and the new weights.
+template <int N, typename Grad, typename Weight>
+__device__ __forceinline__ void update_group(Grad grad, Weight weight, const Packed<N> &qm, const Packed<N> &qv, float step_m, float step_v,
+                                             float c, float step, float decay, const AdamArgs &A, float *m, float *v, float *w,
+                                             float &tm, float &tv) {
+#pragma unroll
+    for (int j = 0; j < N; j++) {
+        const float g = grad(j) * c;
+        const float cv = (float)((qv.w[j / 4] >> (8 * (j % 4))) & 0xffu);
+        m[j] = (float)(int8_t)(qm.w[j / 4] >> (8 * (j % 4))) * step_m + A.omb1 * g;
+        v[j] = (cv * cv) * step_v + A.omb2 * (g * g);
+        tm = __builtin_elementwise_maximum(tm, fabsf(m[j]));
+        tv = __builtin_elementwise_maximum(tv, fabsf(v[j]));
+        w[j] = new_weight(weight(j), m[j], v[j], step, decay, A);
+    }
+}
+
+// At most one block.  Elements past its end are zeros: they leave the maxima
+// alone and are not stored.
+template <int GDT, int WDT, bool SR>
+__device__ __forceinline__ void task8(const ListTensor &T, int32_t tensor, int64_t e_task, int nvalid, int lane, float c,
+                                      const AdamArgs &A) {
+    const float step = A.step * T.lr_scale, decay = A.lr * T.lr_scale * T.weight_decay;
+    const int n = max(0, min(4, nvalid - lane * 4));
+    const int64_t e = e_task + lane * 4;
+    float *pm = gmem<float>(T.m_absmax) + (e_task >> 8), *pv = gmem<float>(T.v_absmax) + (e_task >> 8);
+    const float old_m = *pm, old_v = *pv;
+    PackedOf<GDT, 4> rg = {};
+    PackedOf<WDT, 4> rw = {};
+    Packed<4> qm = {}, qv = {};
+    if (n > 0) {
+        rg = load_grad<GDT>(T, e, n);
+        rw = load_edge<WDT>(T.weight, e, n);
+        qm.w[0] = load_codes(T.m, e, n);
+        qv.w[0] = load_codes(T.v, e, n);
+    }
+    // past the end no scale either: it may be NaN
+    const float step_m = n > 0 ? div_const<127>(old_m) * A.b1 : 0.0f, step_v = n > 0 ? div_const<65025>(old_v) * A.b2 : 0.0f;
+    float m[4], v[4], w[4], tm = 0.0f, tv = 0.0f;
+    update_group<4>([&](int j) { return unpack<GDT>(rg, j); }, [&](int j) { return unpack<WDT>(rw, j); }, qm, qv, step_m, step_v, c, step, decay,
+                    A, m, v, w, tm, tv);
+    store_weight<WDT>(T, e, n, w);
+    float am = __uint_as_float(wave_max(__float_as_uint(tm))), av = __uint_as_float(wave_max(__float_as_uint(tv)));
+    if (am < kTiny) am = 0.0f;
+    if (av < kTiny) av = 0.0f;
+    if (lane == 0) {
+        *pm = am;
+        *pv = av;
+    }
+    Packed<4> om, ov;
+    code_group<SR, 4>(m, v, am > 0.0f ? 127.0f / am : 0.0f, av > 0.0f ? 65025.0f / av : 0.0f, (uint32_t)((uint64_t)e_task >> 2) + lane,
+                      (uint32_t)((uint64_t)e_task >> 34), (uint32_t)tensor, A, om, ov);
+    store_codes(T.m, e, n, am < INFINITY ? om.w[0] : 0u);
+    store_codes(T.v, e, n, av < INFINITY && av > 0.0f ? ov.w[0] : 0u);
+}
+
+// ---- a whole task: N = 8 elements per lane in each of H = 2 halves, a
+// block being 32 lanes of one half, or N = 4 in each of H = 4 parts, a block
+// being one part.  Eight make one 16-byte access of a 16-bit weight, four one
+// of an fp32 weight, so a weight's accesses cover whole contiguous KiB.
+
 template <int WDT> constexpr int kPer8 = 16 / kSizeOf<WDT>;
 
 template <int GDT, int WDT, bool SR>
@@ -371,16 +373,8 @@ __device__ __forceinline__ void task8_full(const ListTensor &T, int32_t tensor, 
     for (int h = 0; h < H; h++) {
         const uint32_t i = h * 64 * N + lane * N;
         float w[N], tm = 0.0f, tv = 0.0f;
-#pragma unroll
-        for (int j = 0; j < N; j++) {
-            const float g = unpack<GDT>(rg[h], j) * c;
-            const float cv = (float)((qv[h].w[j / 4] >> (8 * (j % 4))) & 0xffu);
-            m[h][j] = (float)(int8_t)(qm[h].w[j / 4] >> (8 * (j % 4))) * step_m[h] + A.omb1 * g;
-            v[h][j] = (cv * cv) * step_v[h] + A.omb2 * (g * g);
-            tm = __builtin_elementwise_maximum(tm, fabsf(m[h][j]));   // NaN if either is
-            tv = __builtin_elementwise_maximum(tv, fabsf(v[h][j]));
-            w[j] = new_weight(unpack<WDT>(rw[h], j), m[h][j], v[h][j], step, decay, A);
-        }
+        update_group<N>([&](int j) { return unpack<GDT>(rg[h], j); }, [&](int j) { return unpack<WDT>(rw[h], j); }, qm[h], qv[h], step_m[h],
+                        step_v[h], c, step, decay, A, m[h], v[h], w, tm, tv);
         top_m[h] = __float_as_uint(tm);
         top_v[h] = __float_as_uint(tv);
         store_bytes(bw, i * kSizeOf<WDT>, pack<WDT, N>(w));
@@ -410,35 +404,11 @@ __device__ __forceinline__ void task8_full(const ListTensor &T, int32_t tensor, 
 #pragma unroll
     for (int h = 0; h < H; h++) {
         const uint32_t i = h * 64 * N + lane * N;
-        uint32_t cm[N], cv[N];
-        if constexpr (SR) {
-            // the counter's upper word, the offset and the tensor are uniform, which
-            // leaves the first two rounds one product each per lane
-            uint32_t word[N];
-            const uint32_t low = (uint32_t)((uint64_t)e_task >> 2) + (i >> 2), high = (uint32_t)((uint64_t)e_task >> 34);
-#pragma unroll
-            for (int k = 0; k < N / 4; k++)
-                philox4x32_10(low + k, high, A.offset, (uint32_t)tensor, (uint32_t)A.seed, (uint32_t)(A.seed >> 32), word + 4 * k);
-#pragma unroll
-            for (int j = 0; j < N; j++) {
-                cm[j] = m_code_random(m[h][j] * (im[h] * 0x1p16f), word[j]) >> 16;
-                cv[j] = v_code_random(v[h][j] * iv[h], v[h][j], word[j]);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < N; j++) {
-                // adding 1.5 * 2^23 rounds to a whole number, ties to even; |x| <= 127 (1 + 2^-23),
-                // so the sum's low byte is the code
-                cm[j] = __float_as_uint(m[h][j] * im[h] + 12582912.0f);
-                cv[j] = v_code_near(v[h][j] * iv[h], v[h][j]);
-            }
-        }
+        // the counter's upper word, the offset and the tensor are uniform, which
+        // leaves the first two rounds one product each per lane
         Packed<N> om, ov;
-#pragma unroll
-        for (int k = 0; k < N / 4; k++) {
-            om.w[k] = pack_low_bytes(cm[4 * k], cm[4 * k + 1], cm[4 * k + 2], cm[4 * k + 3]);
-            ov.w[k] = pack_low_bytes(cv[4 * k], cv[4 * k + 1], cv[4 * k + 2], cv[4 * k + 3]);
-        }
+        code_group<SR, N>(m[h], v[h], im[h], iv[h], (uint32_t)((uint64_t)e_task >> 2) + (i >> 2), (uint32_t)((uint64_t)e_task >> 34),
+                          (uint32_t)tensor, A, om, ov);
         if (odd) {
 #pragma unroll
             for (int k = 0; k < N / 4; k++) {
@@ -458,12 +428,12 @@ __device__ __forceinline__ void run_task(const ListTensor &T, int32_t tensor, in
     int nvalid;
     const int64_t e_task = task_start(T, lt, nvalid);
     if constexpr (BITS == 32) {
-        if (nvalid == kListTask && grad_groups<4>(T)) task32_full<GDT, WDT>(T, e_task, lane, c, A);
+        if (nvalid == kListTask) task32_full<GDT, WDT>(T, e_task, lane, c, A);
         else task32<GDT, WDT>(T, e_task, nvalid, lane, c, A);
     }
     else {
-        if (nvalid == kListTask && grad_groups<kPer8<WDT>>(T)) task8_full<GDT, WDT, SR>(T, tensor, e_task, lane, c, A);
-        else task8<GDT, WDT>(T, tensor, e_task, nvalid, lane, c, A);
+        if (nvalid == kListTask) task8_full<GDT, WDT, SR>(T, tensor, e_task, lane, c, A);
+        else task8<GDT, WDT, SR>(T, tensor, e_task, nvalid, lane, c, A);
     }
 }
 
@@ -608,7 +578,6 @@ extern "C" qm_status adamw_step(const void *host_plan, const void *dev_plan, con
     A.eps = (float)hp->eps;
     A.seed = hp->seed;
     A.offset = hp->offset;
-    A.stochastic = hp->rounding == QM_ROUND_STOCHASTIC;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if (h->n_tasks32 > 0) {
         A.task_lo = 0;
@@ -620,7 +589,7 @@ extern "C" qm_status adamw_step(const void *host_plan, const void *dev_plan, con
         A.task_lo = (int32_t)h->n_tasks32;
         A.task_hi = (int32_t)h->n_tasks;
         const unsigned grid = grid_for(A.task_hi - A.task_lo);
-        if (A.stochastic) adamw_kernel<8, true><<<grid, kThreads, 0, s>>>(A);
+        if (hp->rounding == QM_ROUND_STOCHASTIC) adamw_kernel<8, true><<<grid, kThreads, 0, s>>>(A);
         else adamw_kernel<8, false><<<grid, kThreads, 0, s>>>(A);
         if (qm_status e = launched("AdamW with 8-bit states")) return e;
     }

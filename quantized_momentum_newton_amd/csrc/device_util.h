@@ -73,12 +73,14 @@ typedef unsigned ntv4 __attribute__((ext_vector_type(4)));
 typedef unsigned ntv2 __attribute__((ext_vector_type(2)));
 // ------------------------------------------------------------ bytes and random numbers
 
-// Four codes from the low bytes of a, b, c, d (a in the lowest byte): three
-// byte permutes.
+// Four codes from byte BYTE of a, b, c, d (a's lowest): three byte permutes.
+template <int BYTE> __device__ __forceinline__ uint32_t pack_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    const uint32_t ab = __builtin_amdgcn_perm(b, a, 0x0c0c0400u + 0x0101u * BYTE);   // a, b, 0, 0
+    const uint32_t cd = __builtin_amdgcn_perm(d, c, 0x0c0c0400u + 0x0101u * BYTE);   // c, d, 0, 0
+    return __builtin_amdgcn_perm(cd, ab, 0x05040100u);                               // a, b, c, d
+}
 __device__ __forceinline__ uint32_t pack_low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    const uint32_t ab = __builtin_amdgcn_perm(b, a, 0x0c0c0400u);   // a.0, b.0, 0, 0
-    const uint32_t cd = __builtin_amdgcn_perm(d, c, 0x0c0c0400u);   // c.0, d.0, 0, 0
-    return __builtin_amdgcn_perm(cd, ab, 0x05040100u);              // a.0, b.0, c.0, d.0
+    return pack_bytes<0>(a, b, c, d);
 }
 // Philox4x32-10 ("Parallel random numbers: as easy as 1, 2, 3", Salmon,
 // Moraes, Dror and Shaw, SC 2011).

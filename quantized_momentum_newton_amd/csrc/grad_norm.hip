@@ -63,18 +63,14 @@ template <int DT> __device__ __forceinline__ double task_sum_full(const ListTens
 }
 
 template <int DT> __device__ __forceinline__ double task_sum(const ListTensor &T, int64_t e_task, int nvalid, int lane) {
-    if (nvalid == kListTask && grad_groups<kPer<DT>>(T)) return task_sum_full<DT>(T, e_task, lane);
+    if (nvalid == kListTask) return task_sum_full<DT>(T, e_task, lane);
+    const int n = max(0, min(4, nvalid - lane * 4));
+    const PackedOf<DT, 4> r = load_grad<DT>(T, e_task + lane * 4, n);   // zeros past the end
     double s = 0.0;
-    for (int p = 0; p < kListTask / 256; p++) {
-        const int e0 = p * 256 + lane * 4;
-        const int n = min(4, nvalid - e0);
-        if (n <= 0) continue;
-        const Raw4<DT> r = load_grad<DT>(T, e_task + e0, n);
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const double x = (double)elem<DT>(r, j);
-            s += x * x;
-        }
+    for (int j = 0; j < 4; j++) {
+        const double x = (double)unpack<DT>(r, j);
+        s += x * x;
     }
     return s;
 }
@@ -116,7 +112,7 @@ __global__ __launch_bounds__(kFinishThreads) void grad_norm_finish_kernel(const 
 }
 
 template <int DT> __device__ __forceinline__ void task_scale(const ListTensor &T, int64_t e_task, int nvalid, int lane, float c) {
-    if (nvalid == kListTask && grad_groups<kPer<DT>>(T)) {
+    if (nvalid == kListTask) {
         constexpr int N = kPer<DT>, P = kParts<DT>;
         PackedOf<DT, N> r[P];
         load_grad_task<DT, N, P>(T, e_task, lane, r);
@@ -130,16 +126,12 @@ template <int DT> __device__ __forceinline__ void task_scale(const ListTensor &T
         store_grad_task<DT, N, P>(T, e_task, lane, r);
         return;
     }
-    for (int p = 0; p < kListTask / 256; p++) {
-        const int e0 = p * 256 + lane * 4;
-        const int n = min(4, nvalid - e0);
-        if (n <= 0) continue;
-        const Raw4<DT> r = load_grad<DT>(T, e_task + e0, n);
-        float x[4];
+    const int n = max(0, min(4, nvalid - lane * 4));
+    const PackedOf<DT, 4> r = load_grad<DT>(T, e_task + lane * 4, n);
+    float x[4];
 #pragma unroll
-        for (int j = 0; j < 4; j++) x[j] = elem<DT>(r, j) * c;
-        store_grad<DT>(T, e_task + e0, n, x);
-    }
+    for (int j = 0; j < 4; j++) x[j] = unpack<DT>(r, j) * c;
+    store_grad<DT>(T, e_task + lane * 4, n, x);
 }
 
 __global__ __launch_bounds__(kScaleThreads) void grad_scale_kernel(const ListTensor *tensors, const int32_t *owner, int n_tasks,

@@ -1,5 +1,5 @@
-// Device side of the tensor lists: groups of four elements of any type,
-// loaded and stored at element alignment.
+// Device side of the tensor lists: a lane's groups of elements of any type,
+// and where a task's elements lie.
 #pragma once
 #include "device_util.h"
 #include "list_layout.h"
@@ -7,96 +7,28 @@
 namespace qm {
 namespace {
 
-// Four elements as loaded, still packed: 16 bytes of fp32, 8 of 16-bit
-// types, 4 of codes.  The vector types carry the elements' alignment only:
-// gfx950 takes unaligned vector accesses, so a tensor may start at any
-// element of its buffer and aligned ones lose nothing.
-typedef unsigned u32x4_e __attribute__((ext_vector_type(4), aligned(4)));
-typedef unsigned u32x2_e __attribute__((ext_vector_type(2), aligned(2)));
+// N consecutive elements of one lane, still packed, loaded in 16-byte pieces
+// (8 for four 16-bit elements, 4 or 8 for N codes).  The vector types carry no
+// alignment: gfx950 takes unaligned vector accesses, so a tensor may start at
+// any element of its buffer and aligned ones lose nothing.  Where `base` is
+// uniform over the wave and `off` a 32-bit byte offset, an access is one
+// scalar base plus one vector register.
+template <int BYTES> struct Packed { unsigned w[BYTES / 4]; };
+typedef unsigned u32x4_e __attribute__((ext_vector_type(4), aligned(1)));
+typedef unsigned u32x2_e __attribute__((ext_vector_type(2), aligned(1)));
 typedef unsigned u32_e __attribute__((aligned(1)));
 
-template <int DT> struct Raw4 { unsigned w[DT == QM_F32 ? 4 : 2]; };
-
-template <int DT> __device__ __forceinline__ Raw4<DT> load4(uint64_t base, int64_t e) {
-    Raw4<DT> r;
-    if constexpr (DT == QM_F32) {
-        const u32x4_e v = __builtin_nontemporal_load(gmem<const u32x4_e>(base + (uint64_t)e * 4));
-        r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
-    } else {
-        const u32x2_e v = __builtin_nontemporal_load(gmem<const u32x2_e>(base + (uint64_t)e * 2));
-        r.w[0] = v.x; r.w[1] = v.y;
-    }
-    return r;
-}
-// The first n of four elements (0 <= n <= 4), zeros for the others.
-template <int DT> __device__ __forceinline__ Raw4<DT> load_upto4(uint64_t base, int64_t e, int n) {
-    Raw4<DT> r = {};
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-        if (j >= n) continue;
-        if constexpr (DT == QM_F32) r.w[j] = *gmem<const uint32_t>(base + (uint64_t)(e + j) * 4);
-        else r.w[j / 2] |= (unsigned)*gmem<const uint16_t>(base + (uint64_t)(e + j) * 2) << (16 * (j % 2));
-    }
-    return r;
-}
-template <int DT> __device__ __forceinline__ float elem(const Raw4<DT> &r, int j) {
-    if constexpr (DT == QM_F32) return __uint_as_float(r.w[j]);
-    else {
-        const uint16_t h = (uint16_t)(r.w[j / 2] >> (16 * (j % 2)));
-        return DT == QM_BF16 ? bf16_val(h) : f16_val(h);
-    }
-}
-
-template <int DT> __device__ __forceinline__ void store4(uint64_t base, int64_t e, const float *x) {
-    if constexpr (DT == QM_F32) {
-        const u32x4_e v = {__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
-        __builtin_nontemporal_store(v, gmem<u32x4_e>(base + (uint64_t)e * 4));
-    } else {
-        u32x2_e v;
-        if constexpr (DT == QM_BF16) {
-            v.x = bf16x2_rne(x[0], x[1]);
-            v.y = bf16x2_rne(x[2], x[3]);
-        } else {
-            v.x = (unsigned)f16_rne(x[0]) | ((unsigned)f16_rne(x[1]) << 16);
-            v.y = (unsigned)f16_rne(x[2]) | ((unsigned)f16_rne(x[3]) << 16);
-        }
-        __builtin_nontemporal_store(v, gmem<u32x2_e>(base + (uint64_t)e * 2));
-    }
-}
-template <int DT> __device__ __forceinline__ void store1(uint64_t base, int64_t e, float x) {
-    if constexpr (DT == QM_F32) *gmem<float>(base + (uint64_t)e * 4) = x;
-    else if constexpr (DT == QM_BF16) *gmem<uint16_t>(base + (uint64_t)e * 2) = bf16_rne(x);
-    else *gmem<uint16_t>(base + (uint64_t)e * 2) = f16_rne(x);
-}
-template <int DT> __device__ __forceinline__ void store_upto4(uint64_t base, int64_t e, int n, const float *x) {
-    if (n == 4) {
-        store4<DT>(base, e, x);
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < 4; j++)
-        if (j < n) store1<DT>(base, e + j, x[j]);
-}
-
-// N consecutive elements of one lane, still packed, loaded in 16-byte pieces
-// (8 for four 16-bit elements, 4 or 8 for N codes).  `base` is uniform over
-// the wave and `off` a 32-bit byte offset, so an access is one scalar base
-// plus one vector register.
-template <int BYTES> struct Packed { unsigned w[BYTES / 4]; };
-
 template <int BYTES> __device__ __forceinline__ Packed<BYTES> load_bytes(uint64_t base, uint32_t off) {
-    typedef unsigned v4 __attribute__((ext_vector_type(4), aligned(1)));
-    typedef unsigned v2 __attribute__((ext_vector_type(2), aligned(1)));
     Packed<BYTES> r;
     const char *p = gmem<const char>(base) + off;
     if constexpr (BYTES % 16 == 0) {
 #pragma unroll
         for (int k = 0; k < BYTES / 16; k++) {
-            const v4 v = __builtin_nontemporal_load(reinterpret_cast<const v4 *>(p + 16 * k));
+            const u32x4_e v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_e *>(p + 16 * k));
             r.w[4 * k] = v.x; r.w[4 * k + 1] = v.y; r.w[4 * k + 2] = v.z; r.w[4 * k + 3] = v.w;
         }
     } else if constexpr (BYTES == 8) {
-        const v2 v = __builtin_nontemporal_load(reinterpret_cast<const v2 *>(p));
+        const u32x2_e v = __builtin_nontemporal_load(reinterpret_cast<const u32x2_e *>(p));
         r.w[0] = v.x; r.w[1] = v.y;
     } else {
         static_assert(BYTES == 4, "piece size");
@@ -105,18 +37,16 @@ template <int BYTES> __device__ __forceinline__ Packed<BYTES> load_bytes(uint64_
     return r;
 }
 template <int BYTES> __device__ __forceinline__ void store_bytes(uint64_t base, uint32_t off, const Packed<BYTES> &r) {
-    typedef unsigned v4 __attribute__((ext_vector_type(4), aligned(1)));
-    typedef unsigned v2 __attribute__((ext_vector_type(2), aligned(1)));
     char *p = gmem<char>(base) + off;
     if constexpr (BYTES % 16 == 0) {
 #pragma unroll
         for (int k = 0; k < BYTES / 16; k++) {
-            const v4 v = {r.w[4 * k], r.w[4 * k + 1], r.w[4 * k + 2], r.w[4 * k + 3]};
-            __builtin_nontemporal_store(v, reinterpret_cast<v4 *>(p + 16 * k));
+            const u32x4_e v = {r.w[4 * k], r.w[4 * k + 1], r.w[4 * k + 2], r.w[4 * k + 3]};
+            __builtin_nontemporal_store(v, reinterpret_cast<u32x4_e *>(p + 16 * k));
         }
     } else if constexpr (BYTES == 8) {
-        const v2 v = {r.w[0], r.w[1]};
-        __builtin_nontemporal_store(v, reinterpret_cast<v2 *>(p));
+        const u32x2_e v = {r.w[0], r.w[1]};
+        __builtin_nontemporal_store(v, reinterpret_cast<u32x2_e *>(p));
     } else {
         __builtin_nontemporal_store(r.w[0], reinterpret_cast<u32_e *>(p));
     }
@@ -144,17 +74,39 @@ template <int DT, int N> __device__ __forceinline__ PackedOf<DT, N> pack(const f
     return r;
 }
 
-// First element of the tensor's task k, and how many it has: 1024, or at most
-// 256 at the tensor's end.
-__device__ __forceinline__ int64_t task_start(const ListTensor &T, int64_t k, int &count) {
-    const int64_t full = T.numel / kListTask, e = list_task_start(T.numel, k);
-    count = k < full ? kListTask : (int)min(T.numel - e, (int64_t)256);
-    return e;
+// The same of four elements at a tensor's end, of which n are inside
+// (0 <= n <= 4; zeros for the others, which are not stored).
+template <int DT> __device__ __forceinline__ PackedOf<DT, 4> load_edge(uint64_t base, int64_t e, int n) {
+    if (n == 4) return load_bytes<4 * kSizeOf<DT>>(base + (uint64_t)e * kSizeOf<DT>, 0);
+    PackedOf<DT, 4> r = {};
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        if (j >= n) continue;
+        if constexpr (DT == QM_F32) r.w[j] = gmem<const uint32_t>(base)[e + j];
+        else r.w[j / 2] |= (unsigned)gmem<const uint16_t>(base)[e + j] << (16 * (j % 2));
+    }
+    return r;
+}
+template <int DT> __device__ __forceinline__ void store_one(uint64_t base, int64_t e, float x) {
+    if constexpr (DT == QM_F32) gmem<float>(base)[e] = x;
+    else gmem<uint16_t>(base)[e] = DT == QM_BF16 ? bf16_rne(x) : f16_rne(x);
+}
+template <int DT> __device__ __forceinline__ void store_edge(uint64_t base, int64_t e, int n, const float *x) {
+    if (n == 4) {
+        store_bytes(base + (uint64_t)e * kSizeOf<DT>, 0, pack<DT, 4>(x));
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+        if (j < n) store_one<DT>(base, e + j, x[j]);
 }
 
-// Whether groups of N elements (aligned in the tensor) lie in one row.
-template <int N> __device__ __forceinline__ bool grad_groups(const ListTensor &T) {
-    return T.grad_cols == 0 || T.grad_cols % N == 0;
+// First element of the tensor's task k, and how many it has: 1024, or at most
+// 256.
+__device__ __forceinline__ int64_t task_start(const ListTensor &T, int64_t k, int &count) {
+    const int64_t e = list_task_start(T.full_tasks, k);
+    count = k < T.full_tasks ? kListTask : (int)min(T.numel - e, (int64_t)256);
+    return e;
 }
 
 // Position in its buffer of element e of a strided gradient (numel < 2^32).
@@ -163,9 +115,9 @@ __device__ __forceinline__ int64_t grad_pos(const ListTensor &T, int64_t e) {
     return (int64_t)r * T.grad_ld + (int64_t)(u - r * c);
 }
 
-// Calls access(p, base, off) for a lane's groups of N elements in a full task
+// Calls access(p, base, off) for a lane's groups of N elements in a whole task
 // of the gradient, group p at element p * 64 N + lane * N: base and byte
-// offset of its first element.  grad_groups<N>(T) holds.  Rows of a task's
+// offset of its first element (a group lies in one row).  Rows of a task's
 // length or more: a task meets at most one row end, so one scalar division
 // serves the wave (the other branch divides per group).
 template <int DT, int N, int PARTS, typename Access>
@@ -203,29 +155,26 @@ __device__ __forceinline__ void store_grad_task(const ListTensor &T, int64_t e_t
 }
 
 // Elements e .. e + n - 1 of the gradient, n <= 4.
-template <int DT> __device__ __forceinline__ Raw4<DT> load_grad(const ListTensor &T, int64_t e, int n) {
-    if (T.grad_cols == 0 || T.grad_cols % 4 == 0) {   // four elements never straddle two rows
-        const int64_t p = T.grad_cols == 0 ? e : grad_pos(T, e);
-        return n == 4 ? load4<DT>(T.grad, p) : load_upto4<DT>(T.grad, p, n);
-    }
-    Raw4<DT> r = {};
+template <int DT> __device__ __forceinline__ PackedOf<DT, 4> load_grad(const ListTensor &T, int64_t e, int n) {
+    if (T.grad_cols % 4 == 0) return load_edge<DT>(T.grad, T.grad_cols == 0 ? e : grad_pos(T, e), n);   // in one row
+    PackedOf<DT, 4> r = {};
 #pragma unroll
     for (int j = 0; j < 4; j++) {
         if (j >= n) continue;
         const int64_t p = grad_pos(T, e + j);
-        if constexpr (DT == QM_F32) r.w[j] = *gmem<const uint32_t>(T.grad + (uint64_t)p * 4);
-        else r.w[j / 2] |= (unsigned)*gmem<const uint16_t>(T.grad + (uint64_t)p * 2) << (16 * (j % 2));
+        if constexpr (DT == QM_F32) r.w[j] = gmem<const uint32_t>(T.grad)[p];
+        else r.w[j / 2] |= (unsigned)gmem<const uint16_t>(T.grad)[p] << (16 * (j % 2));
     }
     return r;
 }
 template <int DT> __device__ __forceinline__ void store_grad(const ListTensor &T, int64_t e, int n, const float *x) {
-    if (T.grad_cols == 0 || T.grad_cols % 4 == 0) {
-        store_upto4<DT>(T.grad, T.grad_cols == 0 ? e : grad_pos(T, e), n, x);
+    if (T.grad_cols % 4 == 0) {
+        store_edge<DT>(T.grad, T.grad_cols == 0 ? e : grad_pos(T, e), n, x);
         return;
     }
 #pragma unroll
     for (int j = 0; j < 4; j++)
-        if (j < n) store1<DT>(T.grad, grad_pos(T, e + j), x[j]);
+        if (j < n) store_one<DT>(T.grad, grad_pos(T, e + j), x[j]);
 }
 
 }  // namespace

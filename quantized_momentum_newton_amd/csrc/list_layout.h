@@ -3,9 +3,11 @@
 // caller copies it verbatim.
 //
 // The work is cut into tasks of one tensor's consecutive elements, one wave64
-// each: 1024 (four 256-element blocks), and what is left at the tensor's end
-// one block a task, so that no wave goes through several partly filled blocks
-// one after the other (a list of small tensors is bound by that latency).
+// each: 1024 (four 256-element blocks) with 16-byte accesses throughout, and
+// one block a task for what is left at the tensor's end, and for the whole
+// tensor where a strided gradient's rows are not multiples of 8 elements and
+// cut a lane's group.  No wave goes through several such blocks one after the
+// other (a list of small tensors is bound by that latency).
 // Tasks of tensors with
 // 32-bit states come first, then those with 8-bit states, each in list
 // order, so that one launch covers one kind.  A table names every task's
@@ -41,15 +43,12 @@ struct ListTensor {
     int64_t block_offset;         // its first block, list order
     int32_t grad_dtype, weight_dtype, copy_dtype, state_bits;
     float lr_scale, weight_decay;
-    int32_t pad[2];
+    int64_t full_tasks;           // tasks of 1024 elements; the others have at most 256
 };
 
-// Tasks of a tensor of n elements, and the first element of task k.
-constexpr int64_t list_tasks(int64_t n) { return n / kListTask + (n % kListTask + 255) / 256; }
-constexpr int64_t list_task_start(int64_t n, int64_t k) {
-    const int64_t full = n / kListTask;
-    return k < full ? k * kListTask : full * kListTask + (k - full) * 256;
-}
+// Tasks of a tensor of n elements, `full` of them whole; task k's first element.
+constexpr int64_t list_tasks(int64_t n, int64_t full) { return full + (n - full * kListTask + 255) / 256; }
+constexpr int64_t list_task_start(int64_t full, int64_t k) { return k < full ? k * kListTask : full * kListTask + (k - full) * 256; }
 
 static_assert(sizeof(ListHeader) == 72, "list header layout");
 static_assert(sizeof(ListTensor) == 128, "list tensor layout");

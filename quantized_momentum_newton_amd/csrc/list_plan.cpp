@@ -148,7 +148,8 @@ qm_status encode(const Tensor *tensors, int32_t n, int kind, void *host_blob, si
             h.total_numel += e.numel;
             int64_t &k = tasks[e.state_bits == 8];
             e.task_offset = k;
-            k += list_tasks(e.numel);
+            e.full_tasks = e.grad_cols % 8 == 0 ? e.numel / kListTask : 0;
+            k += list_tasks(e.numel, e.full_tasks);
         }
         if (any_overlap(spans)) return fail(QM_E_ARG, "buffers of the list overlap");
         h.magic = kListMagic;
@@ -175,7 +176,7 @@ qm_status encode(const Tensor *tensors, int32_t n, int kind, void *host_blob, si
         for (int32_t i = 0; i < n; i++) {
             ListTensor &e = table[(size_t)i];
             if (e.state_bits == 8) e.task_offset += tasks[0];
-            const int64_t nt = list_tasks(e.numel);
+            const int64_t nt = list_tasks(e.numel, e.full_tasks);
             for (int64_t k = 0; k < nt; k++) owner[e.task_offset + k] = i;
         }
         memcpy(base, &h, sizeof h);
