@@ -191,6 +191,8 @@ def test_lists_encode():
     (dict(grad_cols=3, grad_ld=4), SHAPE), (dict(grad_cols=8, grad_ld=4), SHAPE), (dict(grad_cols=-8, grad_ld=8), SHAPE),
     (dict(grad_cols=8, grad_ld=1 << 60), SHAPE), (dict(numel=1 << 45), UNSUPPORTED),
     (dict(numel=1 << 33, grad_cols=8, grad_ld=16), UNSUPPORTED),
+    (dict(numel=1 << 36, grad=1 << 44, weight=1 << 45, m=1 << 43, v=1 << 42, m_absmax=1 << 41, v_absmax=3 << 40,
+          copy=1 << 46), UNSUPPORTED),
     (dict(weight="grad"), ARG), (dict(m="v"), ARG), (dict(copy="m_absmax"), ARG),
 ])
 def test_adamw_list_refusals(change, status):

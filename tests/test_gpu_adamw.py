@@ -12,6 +12,8 @@ an fp32 step):
   weight: decay as fp32 with three products: 5 u decay |w|, two sums: u (|w| + |w'|),
   then its own type's rounding, eps / 2 relative or half the smallest subnormal.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -340,6 +342,45 @@ def test_side_stream_and_graph():
         torch.cuda.synchronize()
         for t, w in zip(live, want):
             assert torch.equal(t, w), k
+
+
+def test_threads_with_their_own_streams():
+    """Four host threads, each its own tensors, list, stream and workspace,
+    against the same calls made alone."""
+    def job(k):
+        p = Param(20001 + 777 * k, 8 if k % 2 else 32, torch.bfloat16, torch.float32, 300 + k)
+        grads = q.GradPlan([p.grad])
+        return p, q.AdamWPlan([p.tuple()]), grads, grads.workspace(), torch.zeros(2, device=DEV)
+
+    def go(j, stream):
+        p, plan, grads, ws, out = j
+        for step in range(1, 6):
+            q.grad_norm(grads, 0.3, norm=out[:1], coef=out[1:], ws=ws, stream=stream)
+            q.adamw_step(plan, step, **HP, grad_scale=out[1:], rounding="stochastic", seed=4, stream=stream)
+
+    alone, threaded = ([job(k) for k in range(4)] for _ in range(2))
+    for j in alone:
+        go(j, None)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in threaded]
+    failed = []
+
+    def run(k):
+        try:
+            go(threaded[k], streams[k])
+        except Exception as e:
+            failed.append((k, repr(e)))
+
+    threads = [threading.Thread(target=run, args=(k,)) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed
+    for a, b in zip(alone, threaded):
+        for x, y in zip([a[0].weight, a[4]] + a[0].state.tensors(), [b[0].weight, b[4]] + b[0].state.tensors()):
+            assert torch.equal(x, y)
 
 
 @pytest.mark.parametrize("bits", [32, 8])
