@@ -547,8 +547,8 @@ def grad_norm(plan, max_norm=float("inf"), eps=1e-6, norm=None, coef=None, ws=No
     norm, coef = _out(norm, "norm", 1, plan, stream), _out(coef, "coef", 1, plan, stream)
     if ws is None:
         ws = _new(plan.workspace_bytes(), torch.uint8, plan, stream)
-    _check(_LIB.grad_norm(plan.hptr, plan.dptr, max_norm, eps, _ptr(norm), _ptr(coef), _ptr(ws), ws.numel(),
-                          _queue(stream, plan)))
+    _check(_LIB.grad_norm(plan.hptr, plan.dptr, max_norm, eps, norm.data_ptr(), coef.data_ptr(), ws.data_ptr(),
+                          ws.numel(), _queue(stream, plan)))
     return norm, coef
 
 
@@ -556,7 +556,7 @@ def grad_scale(plan, coef, stream=None):
     """Every gradient of the plan times coef (device fp32 [1]) in place; a NaN
     coef leaves them as they are."""
     _require(coef, "coef", torch.float32, plan.device, numel=1)
-    _check(_LIB.grad_scale(plan.hptr, plan.dptr, _ptr(coef), _queue(stream, plan)))
+    _check(_LIB.grad_scale(plan.hptr, plan.dptr, coef.data_ptr(), _queue(stream, plan)))
 
 
 class AdamWState:
@@ -644,7 +644,8 @@ def adamw_step(plan, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, grad_scale=Non
         _require(grad_scale, "grad_scale", torch.float32, plan.device, numel=1)
     hp = L.AdamWHparams(lr, betas[0], betas[1], eps, step, ROUNDING[rounding],
                         (step if offset is None else offset) & 0xFFFFFFFF, seed)
-    _check(_LIB.adamw_step(plan.hptr, plan.dptr, ctypes.byref(hp), _ptr(grad_scale), _queue(stream, plan)))
+    _check(_LIB.adamw_step(plan.hptr, plan.dptr, ctypes.byref(hp),
+                           grad_scale.data_ptr() if grad_scale is not None else None, _queue(stream, plan)))
 
 
 def adamw_read_state(plan, m=None, v=None, stream=None):
@@ -652,5 +653,5 @@ def adamw_read_state(plan, m=None, v=None, stream=None):
     (given or new); plan.view(m, i) is tensor i's part.  Returns (m, v)."""
     n = plan.n_blocks * BLOCK
     m, v = _out(m, "m", n, plan, stream), _out(v, "v", n, plan, stream)
-    _check(_LIB.adamw_read_state(plan.hptr, plan.dptr, _ptr(m), _ptr(v), _queue(stream, plan)))
+    _check(_LIB.adamw_read_state(plan.hptr, plan.dptr, m.data_ptr(), v.data_ptr(), _queue(stream, plan)))
     return m, v
