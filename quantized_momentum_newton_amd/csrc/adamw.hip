@@ -41,11 +41,14 @@ struct AdamArgs {
 };
 
 // New weight from the new moments.  The root and the reciprocal are the
-// hardware's, within an ulp; the root takes subnormal numbers for 0, so v
-// below 2^-96 is scaled by 2^64.  denom >= eps >= 2^-126 has a finite reciprocal.
+// hardware's, within an ulp.  The root takes subnormal numbers for 0: SCALED
+// keeps it right there too (v below 2^-96 times 2^64), which a step needs only
+// where the root of 2^-126 counts next to eps.  denom >= eps >= 2^-126 has a
+// finite reciprocal.
+template <bool SCALED>
 __device__ __forceinline__ float new_weight(float w, float m, float v, float step, float decay, const AdamArgs &A) {
-    const bool tiny = v < 0x1p-96f;
-    const float r = __builtin_amdgcn_sqrtf(v * (tiny ? 0x1p64f : 1.0f));
+    const bool tiny = SCALED && v < 0x1p-96f;
+    const float r = __builtin_amdgcn_sqrtf(tiny ? v * 0x1p64f : v);
     const float denom = __builtin_fmaf(r, tiny ? A.root * 0x1p-32f : A.root, A.eps);
     return __builtin_fmaf(-step, m * __builtin_amdgcn_rcpf(denom), __builtin_fmaf(-decay, w, w));
 }
@@ -75,7 +78,7 @@ __device__ __forceinline__ void task32(const ListTensor &T, int64_t e_task, int 
         const float g = unpack<GDT>(rg, j) * c;
         m[j] = A.b1 * unpack<QM_F32>(rm, j) + A.omb1 * g;
         v[j] = A.b2 * unpack<QM_F32>(rv, j) + A.omb2 * (g * g);
-        w[j] = new_weight(unpack<WDT>(rw, j), m[j], v[j], step, decay, A);
+        w[j] = new_weight<true>(unpack<WDT>(rw, j), m[j], v[j], step, decay, A);
     }
     store_edge<QM_F32>(T.m, e, n, m);
     store_edge<QM_F32>(T.v, e, n, v);
@@ -110,7 +113,7 @@ __device__ __forceinline__ void task32_full(const ListTensor &T, int64_t e_task,
             const float g = unpack<GDT>(rg[p], j) * c;
             m[j] = A.b1 * unpack<QM_F32>(rm[p], j) + A.omb1 * g;
             v[j] = A.b2 * unpack<QM_F32>(rv[p], j) + A.omb2 * (g * g);
-            w[j] = new_weight(unpack<WDT>(rw[p], j), m[j], v[j], step, decay, A);
+            w[j] = new_weight<true>(unpack<WDT>(rw[p], j), m[j], v[j], step, decay, A);
         }
         store_bytes(bm, i * 4, pack<QM_F32, 4>(m));
         store_bytes(bv, i * 4, pack<QM_F32, 4>(v));
@@ -217,14 +220,16 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t x) {
 // y = v (65025 / max) lies in [0, 65025 (1 + 2^-23)], x = m (127 / max) in
 // +-127 (1 + 2^-23).
 //
+// k = 0 and v > 0: the code is 1 all the same.
+__device__ __forceinline__ bool alone(float k, float v) { return v > k * 0x1.fffffep127f; }
+
 // Code of v by nearest value.  k = floor of the hardware root (within an ulp)
 // is floor(sqrt y) or its neighbour next to a perfect square, where both give
 // the same code; v > 0 codes at least 1.
 __device__ __forceinline__ uint32_t v_code_near(float y, float v) {
     const float k = floorf(__builtin_amdgcn_sqrtf(y));
     const float d = __builtin_fmaf(-k, k, y);
-    const uint32_t code = (uint32_t)(int)k + (d > k + 0.5f ? 1u : 0u);
-    return max(code, min(__float_as_uint(v), 1u));
+    return (uint32_t)(int)k + (uint32_t)((d > k + 0.5f) | alone(k, v));
 }
 
 // The same by a 16-bit and a 15-bit random number (the two halves of the
@@ -245,8 +250,7 @@ __device__ __forceinline__ uint32_t m_code_random(float x16, uint32_t word) {
 __device__ __forceinline__ uint32_t v_code_random(float y, float v, uint32_t word) {
     const float k = floorf(__builtin_amdgcn_sqrtf(y));
     const float d = __builtin_fmaf(-k, k, y), t = __builtin_fmaf(k, 0x1p-14f, 0x1p-15f);   // 2^-15 (2k + 1)
-    const uint32_t code = (uint32_t)(int)k + ((float)(word & 0x7fffu) * t < d ? 1u : 0u);
-    return min(max(code, min(__float_as_uint(v), 1u)), 255u);
+    return min((uint32_t)(int)k + (uint32_t)(((float)(word & 0x7fffu) * t < d) | alone(k, v)), 255u);
 }
 
 // Codes of N elements of a block: im = 127 / (max of |m|), iv = 65025 / (max
@@ -284,25 +288,28 @@ __device__ __forceinline__ void code_group(const float *m, const float *v, float
 
 // New moments of N elements, their largest magnitudes into tm and tv (NaN if
 // one is), and the new weights.
-template <int N, typename Grad, typename Weight>
+template <bool SCALED, int N, typename Grad, typename Weight>
 __device__ __forceinline__ void update_group(Grad grad, Weight weight, const Packed<N> &qm, const Packed<N> &qv, float step_m, float step_v,
                                              float c, float step, float decay, const AdamArgs &A, float *m, float *v, float *w,
                                              float &tm, float &tv) {
 #pragma unroll
     for (int j = 0; j < N; j++) {
         const float g = grad(j) * c;
+        // code times step_m, rounded once: the code's byte plus 128 converts in
+        // one instruction, and the fused product takes the 128 steps off exactly
+        const float cm = (float)(((qm.w[j / 4] ^ 0x80808080u) >> (8 * (j % 4))) & 0xffu);
         const float cv = (float)((qv.w[j / 4] >> (8 * (j % 4))) & 0xffu);
-        m[j] = (float)(int8_t)(qm.w[j / 4] >> (8 * (j % 4))) * step_m + A.omb1 * g;
+        m[j] = __builtin_fmaf(cm, step_m, -128.0f * step_m) + A.omb1 * g;
         v[j] = (cv * cv) * step_v + A.omb2 * (g * g);
         tm = __builtin_elementwise_maximum(tm, fabsf(m[j]));
         tv = __builtin_elementwise_maximum(tv, fabsf(v[j]));
-        w[j] = new_weight(weight(j), m[j], v[j], step, decay, A);
+        w[j] = new_weight<SCALED>(weight(j), m[j], v[j], step, decay, A);
     }
 }
 
 // At most one block.  Elements past its end are zeros: they leave the maxima
 // alone and are not stored.
-template <int GDT, int WDT, bool SR>
+template <int GDT, int WDT, bool SR, bool SCALED>
 __device__ __forceinline__ void task8(const ListTensor &T, int32_t tensor, int64_t e_task, int nvalid, int lane, float c,
                                       const AdamArgs &A) {
     const float step = A.step * T.lr_scale, decay = A.lr * T.lr_scale * T.weight_decay;
@@ -322,7 +329,7 @@ __device__ __forceinline__ void task8(const ListTensor &T, int32_t tensor, int64
     // past the end no scale either: it may be NaN
     const float step_m = n > 0 ? div_const<127>(old_m) * A.b1 : 0.0f, step_v = n > 0 ? div_const<65025>(old_v) * A.b2 : 0.0f;
     float m[4], v[4], w[4], tm = 0.0f, tv = 0.0f;
-    update_group<4>([&](int j) { return unpack<GDT>(rg, j); }, [&](int j) { return unpack<WDT>(rw, j); }, qm, qv, step_m, step_v, c, step, decay,
+    update_group<SCALED, 4>([&](int j) { return unpack<GDT>(rg, j); }, [&](int j) { return unpack<WDT>(rw, j); }, qm, qv, step_m, step_v, c, step, decay,
                     A, m, v, w, tm, tv);
     store_weight<WDT>(T, e, n, w);
     float am = __uint_as_float(wave_max(__float_as_uint(tm))), av = __uint_as_float(wave_max(__float_as_uint(tv)));
@@ -346,7 +353,7 @@ __device__ __forceinline__ void task8(const ListTensor &T, int32_t tensor, int64
 
 template <int WDT> constexpr int kPer8 = 16 / kSizeOf<WDT>;
 
-template <int GDT, int WDT, bool SR>
+template <int GDT, int WDT, bool SR, bool SCALED>
 __device__ __forceinline__ void task8_full(const ListTensor &T, int32_t tensor, int64_t e_task, int lane, float c, const AdamArgs &A) {
     constexpr int N = kPer8<WDT>, H = kListTask / (64 * N);
     PackedOf<GDT, N> rg[H];
@@ -373,7 +380,7 @@ __device__ __forceinline__ void task8_full(const ListTensor &T, int32_t tensor, 
     for (int h = 0; h < H; h++) {
         const uint32_t i = h * 64 * N + lane * N;
         float w[N], tm = 0.0f, tv = 0.0f;
-        update_group<N>([&](int j) { return unpack<GDT>(rg[h], j); }, [&](int j) { return unpack<WDT>(rw[h], j); }, qm[h], qv[h], step_m[h],
+        update_group<SCALED, N>([&](int j) { return unpack<GDT>(rg[h], j); }, [&](int j) { return unpack<WDT>(rw[h], j); }, qm[h], qv[h], step_m[h],
                         step_v[h], c, step, decay, A, m[h], v[h], w, tm, tv);
         top_m[h] = __float_as_uint(tm);
         top_v[h] = __float_as_uint(tv);
@@ -423,7 +430,7 @@ __device__ __forceinline__ void task8_full(const ListTensor &T, int32_t tensor, 
 
 // ------------------------------------------------------------ kernels
 
-template <int BITS, bool SR, int GDT, int WDT>
+template <int BITS, bool SR, bool SCALED, int GDT, int WDT>
 __device__ __forceinline__ void run_task(const ListTensor &T, int32_t tensor, int64_t lt, int lane, float c, const AdamArgs &A) {
     int nvalid;
     const int64_t e_task = task_start(T, lt, nvalid);
@@ -432,12 +439,12 @@ __device__ __forceinline__ void run_task(const ListTensor &T, int32_t tensor, in
         else task32<GDT, WDT>(T, e_task, nvalid, lane, c, A);
     }
     else {
-        if (nvalid == kListTask) task8_full<GDT, WDT, SR>(T, tensor, e_task, lane, c, A);
-        else task8<GDT, WDT, SR>(T, tensor, e_task, nvalid, lane, c, A);
+        if (nvalid == kListTask) task8_full<GDT, WDT, SR, SCALED>(T, tensor, e_task, lane, c, A);
+        else task8<GDT, WDT, SR, SCALED>(T, tensor, e_task, nvalid, lane, c, A);
     }
 }
 
-template <int BITS, bool SR> __global__ __launch_bounds__(kThreads, 6) void adamw_kernel(AdamArgs A) {
+template <int BITS, bool SR, bool SCALED> __global__ __launch_bounds__(kThreads, 6) void adamw_kernel(AdamArgs A) {
     const int lane = threadIdx.x & 63;
     const int task = A.task_lo + __builtin_amdgcn_readfirstlane((int)(blockIdx.x * kWavesPerWG + (threadIdx.x >> 6)));
     if (task >= A.task_hi) return;
@@ -450,15 +457,15 @@ template <int BITS, bool SR> __global__ __launch_bounds__(kThreads, 6) void adam
     const ListTensor T = gmem<const ListTensor>(A.tensors)[ti];
     const int64_t lt = task - T.task_offset;
     switch (T.grad_dtype * 3 + T.weight_dtype) {
-        case QM_F32 * 3 + QM_F32: run_task<BITS, SR, QM_F32, QM_F32>(T, ti, lt, lane, c, A); break;
-        case QM_F32 * 3 + QM_BF16: run_task<BITS, SR, QM_F32, QM_BF16>(T, ti, lt, lane, c, A); break;
-        case QM_F32 * 3 + QM_F16: run_task<BITS, SR, QM_F32, QM_F16>(T, ti, lt, lane, c, A); break;
-        case QM_BF16 * 3 + QM_F32: run_task<BITS, SR, QM_BF16, QM_F32>(T, ti, lt, lane, c, A); break;
-        case QM_BF16 * 3 + QM_BF16: run_task<BITS, SR, QM_BF16, QM_BF16>(T, ti, lt, lane, c, A); break;
-        case QM_BF16 * 3 + QM_F16: run_task<BITS, SR, QM_BF16, QM_F16>(T, ti, lt, lane, c, A); break;
-        case QM_F16 * 3 + QM_F32: run_task<BITS, SR, QM_F16, QM_F32>(T, ti, lt, lane, c, A); break;
-        case QM_F16 * 3 + QM_BF16: run_task<BITS, SR, QM_F16, QM_BF16>(T, ti, lt, lane, c, A); break;
-        default: run_task<BITS, SR, QM_F16, QM_F16>(T, ti, lt, lane, c, A); break;
+        case QM_F32 * 3 + QM_F32: run_task<BITS, SR, SCALED, QM_F32, QM_F32>(T, ti, lt, lane, c, A); break;
+        case QM_F32 * 3 + QM_BF16: run_task<BITS, SR, SCALED, QM_F32, QM_BF16>(T, ti, lt, lane, c, A); break;
+        case QM_F32 * 3 + QM_F16: run_task<BITS, SR, SCALED, QM_F32, QM_F16>(T, ti, lt, lane, c, A); break;
+        case QM_BF16 * 3 + QM_F32: run_task<BITS, SR, SCALED, QM_BF16, QM_F32>(T, ti, lt, lane, c, A); break;
+        case QM_BF16 * 3 + QM_BF16: run_task<BITS, SR, SCALED, QM_BF16, QM_BF16>(T, ti, lt, lane, c, A); break;
+        case QM_BF16 * 3 + QM_F16: run_task<BITS, SR, SCALED, QM_BF16, QM_F16>(T, ti, lt, lane, c, A); break;
+        case QM_F16 * 3 + QM_F32: run_task<BITS, SR, SCALED, QM_F16, QM_F32>(T, ti, lt, lane, c, A); break;
+        case QM_F16 * 3 + QM_BF16: run_task<BITS, SR, SCALED, QM_F16, QM_BF16>(T, ti, lt, lane, c, A); break;
+        default: run_task<BITS, SR, SCALED, QM_F16, QM_F16>(T, ti, lt, lane, c, A); break;
     }
 }
 
@@ -582,15 +589,20 @@ extern "C" qm_status adamw_step(const void *host_plan, const void *dev_plan, con
     if (h->n_tasks32 > 0) {
         A.task_lo = 0;
         A.task_hi = (int32_t)h->n_tasks32;
-        adamw_kernel<32, false><<<grid_for(A.task_hi - A.task_lo), kThreads, 0, s>>>(A);
+        adamw_kernel<32, false, true><<<grid_for(A.task_hi - A.task_lo), kThreads, 0, s>>>(A);
         if (qm_status e = launched("AdamW")) return e;
     }
     if (h->n_tasks > h->n_tasks32) {
         A.task_lo = (int32_t)h->n_tasks32;
         A.task_hi = (int32_t)h->n_tasks;
         const unsigned grid = grid_for(A.task_hi - A.task_lo);
-        if (hp->rounding == QM_ROUND_STOCHASTIC) adamw_kernel<8, true><<<grid, kThreads, 0, s>>>(A);
-        else adamw_kernel<8, false><<<grid, kThreads, 0, s>>>(A);
+        // The 8-bit kernel is held up by its instructions as much as by memory
+        // (VALU busy 80 %): it keeps the root of subnormal moments only where that
+        // root, at most 2^-63, is more than half a step of eps.
+        const bool scaled = A.root * 0x1p-63f > 0x1p-24f * A.eps;
+        const auto kernel = hp->rounding == QM_ROUND_STOCHASTIC ? (scaled ? adamw_kernel<8, true, true> : adamw_kernel<8, true, false>)
+                                                                : (scaled ? adamw_kernel<8, false, true> : adamw_kernel<8, false, false>);
+        kernel<<<grid, kThreads, 0, s>>>(A);
         if (qm_status e = launched("AdamW with 8-bit states")) return e;
     }
     return QM_OK;

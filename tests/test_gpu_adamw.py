@@ -212,6 +212,27 @@ def test_roots_of_subnormal_moments(eps):
     assert np.all(np.abs(got - want) <= 24 * U * np.abs(want) + SUBNORMAL[torch.float32])
 
 
+@pytest.mark.parametrize("rounding", ["nearest", "stochastic"])
+@pytest.mark.parametrize("eps", [1e-30, 1e-12, 1e-8])
+def test_roots_of_subnormal_moments_8_bit(eps, rounding):
+    """The same with 8-bit states, from zero: m and v are the first step's
+    binary32 products."""
+    n = 3000
+    p = Param(n, 8, torch.float32, torch.float32, 16, decay=0.0, zero=True)
+    p.weight.zero_()
+    p.grad.copy_(torch.logspace(-22, -12, n))
+    p.snapshot()
+    plan = q.AdamWPlan([p.tuple()])
+    q.adamw_step(plan, 1, lr=1.0, betas=(0.9, 0.999), eps=eps, rounding=rounding)
+    torch.cuda.synchronize()
+    g = p.h["g"]
+    m, v = np.float32(1 - 0.9) * g, np.float32(1 - 0.999) * (g * g)
+    want = -(m.astype(np.float64) / 0.1) / (np.sqrt(v.astype(np.float64) / 0.001) + eps)
+    got = p.weight.double().cpu().numpy()
+    assert np.any((v > 0) & (v < 2.0 ** -126))
+    assert np.all(np.abs(got - want) <= 24 * U * np.abs(want) + SUBNORMAL[torch.float32])
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_nan_factor_writes_nothing(bits):
     p = Param(5000, bits, torch.bfloat16, torch.float32, 77)
