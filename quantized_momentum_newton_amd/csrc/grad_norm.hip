@@ -5,7 +5,9 @@
 // range long before the norm does, and sums of 10^9 of them lose digits in
 // fp32.  Two launches: every workgroup adds its tasks in order into one
 // partial sum, one workgroup adds the partials in order, so the result does
-// not depend on timing.  Bound by HBM: one read of the gradients.
+// not depend on timing.  Bound by HBM: the norm reads the gradients once (1.3G
+// in bf16: 0.40 ms, 6.6 TB/s), the scaling reads and writes them (0.84 ms, 6.3
+// TB/s; a large copy reaches 6.5).
 #include <hip/hip_runtime.h>
 
 #include <math.h>
@@ -13,6 +15,7 @@
 
 #include "internal.h"
 #include "list_device.h"
+#include "list_host.h"
 #include "list_layout.h"
 #include "qmuon.h"
 
@@ -173,28 +176,9 @@ __global__ __launch_bounds__(kScaleThreads) void grad_scale_kernel(const ListTen
     else task_scale<QM_F16>(T, e_task, nvalid, lane, c);
 }
 
-qm_status launched(const char *what) {
-    const hipError_t e = hipGetLastError();
-    return e == hipSuccess ? QM_OK : fail(QM_E_HIP, "%s launch: %s", what, hipGetErrorString(e));
-}
-
 unsigned parts_of(const ListHeader *h) {
     const int64_t wgs = (h->n_tasks + kWavesPerWG - 1) / kWavesPerWG;
     return (unsigned)(wgs < kMaxParts ? wgs : kMaxParts);
-}
-
-const ListHeader *list_args(const void *host_plan, const void *dev_plan, qm_status *st) {
-    const ListHeader *h = list_header(host_plan, kListGrads, st);
-    if (!h) return nullptr;
-    if (!dev_plan) {
-        *st = fail(QM_E_ARG, "device copy of the list is null");
-        return nullptr;
-    }
-    if (!aligned(dev_plan, 64)) {
-        *st = fail(QM_E_ALIGN, "device copy of the list must be 64-byte aligned");
-        return nullptr;
-    }
-    return h;
 }
 
 }  // namespace
@@ -211,27 +195,24 @@ extern "C" size_t grad_norm_workspace_bytes(const void *host_plan) {
 extern "C" qm_status grad_norm(const void *host_plan, const void *dev_plan, double max_norm, double eps, float *norm_out,
                                float *coef_out, void *ws, size_t ws_bytes, qm_stream_t stream) {
     clear_error();
-    qm_status st;
-    const ListHeader *h = list_args(host_plan, dev_plan, &st);
-    if (!h) return st;
+    const ListArgs list = list_args(host_plan, dev_plan, kListGrads);
+    const ListHeader *h = list.h;
+    if (!h) return list.st;
     if (!(max_norm > 0.0)) return fail(QM_E_ARG, "max_norm must be positive");
     if (!(eps >= 0.0 && eps < (double)INFINITY)) return fail(QM_E_ARG, "eps must be finite and not negative");
     if (!norm_out || !coef_out) return fail(QM_E_ARG, "norm_out and coef_out must not be null");
     if (!aligned(norm_out, 4) || !aligned(coef_out, 4)) return fail(QM_E_ALIGN, "norm_out and coef_out need 4-byte alignment");
     const unsigned parts = parts_of(h);
-    const char *dev = static_cast<const char *>(dev_plan);
-    const ListTensor *tensors = reinterpret_cast<const ListTensor *>(dev + h->off_tensors);
-    const int32_t *owner = reinterpret_cast<const int32_t *>(dev + h->off_task_tensor);
     if (!ws || ws_bytes < (parts + 1) * sizeof(double))
         return fail(QM_E_WORKSPACE, "workspace: need %zu bytes", (size_t)(parts + 1) * sizeof(double));
     if (!aligned(ws, 8)) return fail(QM_E_ALIGN, "workspace needs 8-byte alignment");
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if (h->n_tasks <= kSmallTasks) {
-        grad_norm_small_kernel<<<1, kFinishThreads, 0, s>>>(tensors, owner, (int)h->n_tasks, max_norm, eps, norm_out, coef_out);
+        grad_norm_small_kernel<<<1, kFinishThreads, 0, s>>>(list.tensors, list.owner, (int)h->n_tasks, max_norm, eps, norm_out, coef_out);
         return launched("gradient norm");
     }
     double *part = static_cast<double *>(ws);
-    grad_sumsq_kernel<<<parts, kThreads, 0, s>>>(tensors, owner, (int)h->n_tasks, part);
+    grad_sumsq_kernel<<<parts, kThreads, 0, s>>>(list.tensors, list.owner, (int)h->n_tasks, part);
     if (qm_status e = launched("gradient norm")) return e;
     grad_norm_finish_kernel<<<1, kFinishThreads, 0, s>>>(part, (int)parts, max_norm, eps, norm_out, coef_out);
     return launched("gradient norm");
@@ -239,16 +220,14 @@ extern "C" qm_status grad_norm(const void *host_plan, const void *dev_plan, doub
 
 extern "C" qm_status grad_scale(const void *host_plan, const void *dev_plan, const float *coef, qm_stream_t stream) {
     clear_error();
-    qm_status st;
-    const ListHeader *h = list_args(host_plan, dev_plan, &st);
-    if (!h) return st;
+    const ListArgs list = list_args(host_plan, dev_plan, kListGrads);
+    const ListHeader *h = list.h;
+    if (!h) return list.st;
     if (!coef) return fail(QM_E_ARG, "coef must not be null");
     if (!aligned(coef, 4)) return fail(QM_E_ALIGN, "coef needs 4-byte alignment");
     if (h->n_tasks == 0) return QM_OK;
-    const char *dev = static_cast<const char *>(dev_plan);
     constexpr int waves = kScaleThreads / 64;
     grad_scale_kernel<<<(unsigned)((h->n_tasks + waves - 1) / waves), kScaleThreads, 0, static_cast<hipStream_t>(stream)>>>(
-        reinterpret_cast<const ListTensor *>(dev + h->off_tensors),
-        reinterpret_cast<const int32_t *>(dev + h->off_task_tensor), (int)h->n_tasks, coef);
+        list.tensors, list.owner, (int)h->n_tasks, coef);
     return launched("gradient scale");
 }
