@@ -11,9 +11,9 @@
 //   8-bit states, fp32 weight, bf16 gradient and copy (16.1): 206M in 0.55 ms,
 //     6.0 TB/s;
 //   8-bit states, bf16 weight and gradient (10.1): 218M in 0.37 ms, 5.9 TB/s,
-//     with the VALU busy 80 % of the time; with stochastic codes the VALU
-//     binds: 36M in 0.07 ms, 5 TB/s (two thirds of its instructions over the
-//     nearest codes' are the random numbers').
+//     with the VALU busy 77 % of the time; with stochastic codes the VALU
+//     binds (84 %): 36M in 0.07 ms, 5.2 TB/s (975 instructions a task against
+//     663; half of the difference makes the random numbers).
 //
 // One wave64 owns a task of 1024 consecutive elements of one tensor and issues
 // all of its loads before the arithmetic (half the task a wave: 1.09 ms for the
@@ -590,7 +590,7 @@ extern "C" qm_status adamw_step(const void *host_plan, const void *dev_plan, con
         A.task_hi = (int32_t)h->n_tasks;
         const unsigned grid = grid_for(A.task_hi - A.task_lo);
         // The 8-bit kernel is held up by its instructions as much as by memory
-        // (VALU busy 80 %): it keeps the root of subnormal moments only where that
+        // (VALU busy 77 to 84 %): it keeps the root of subnormal moments only where that
         // root, at most 2^-63, is more than half a step of eps.
         const bool scaled = A.root * 0x1p-63f > 0x1p-24f * A.eps;
         const auto kernel = hp->rounding == QM_ROUND_STOCHASTIC ? (scaled ? adamw_kernel<8, true, true> : adamw_kernel<8, true, false>)
