@@ -109,11 +109,26 @@ __device__ __forceinline__ int64_t task_start(const ListTensor &T, int64_t k, in
     return e;
 }
 
-// Position in its buffer of element e of a strided gradient (numel < 2^32).
-__device__ __forceinline__ int64_t grad_pos(const ListTensor &T, int64_t e) {
-    const uint32_t c = (uint32_t)T.grad_cols, u = (uint32_t)e, r = u / c;
-    return (int64_t)r * T.grad_ld + (int64_t)(u - r * c);
-}
+// Positions in a strided gradient's buffer (numel < 2^32) of element e and,
+// step by step, of the elements after it: one division for a lane's group.
+struct GradPos {
+    int64_t at, jump;
+    uint32_t col, cols;
+    __device__ __forceinline__ GradPos(const ListTensor &T, int64_t e) {
+        cols = (uint32_t)T.grad_cols;
+        const uint32_t u = (uint32_t)e, row = u / cols;
+        col = u - row * cols;
+        at = (int64_t)row * T.grad_ld + col;
+        jump = T.grad_ld - T.grad_cols;
+    }
+    __device__ __forceinline__ void next() {
+        at++;
+        if (++col == cols) {
+            col = 0;
+            at += jump;
+        }
+    }
+};
 
 // Calls access(p, base, off) for a lane's groups of N elements in a whole task
 // of the gradient, group p at element p * 64 N + lane * N: base and byte
@@ -156,25 +171,31 @@ __device__ __forceinline__ void store_grad_task(const ListTensor &T, int64_t e_t
 
 // Elements e .. e + n - 1 of the gradient, n <= 4.
 template <int DT> __device__ __forceinline__ PackedOf<DT, 4> load_grad(const ListTensor &T, int64_t e, int n) {
-    if (T.grad_cols % 4 == 0) return load_edge<DT>(T.grad, T.grad_cols == 0 ? e : grad_pos(T, e), n);   // in one row
+    if (T.grad_cols == 0) return load_edge<DT>(T.grad, e, n);
+    GradPos p(T, e);
+    if (T.grad_cols % 4 == 0) return load_edge<DT>(T.grad, p.at, n);   // in one row
     PackedOf<DT, 4> r = {};
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
+    for (int j = 0; j < 4; j++, p.next()) {
         if (j >= n) continue;
-        const int64_t p = grad_pos(T, e + j);
-        if constexpr (DT == QM_F32) r.w[j] = gmem<const uint32_t>(T.grad)[p];
-        else r.w[j / 2] |= (unsigned)gmem<const uint16_t>(T.grad)[p] << (16 * (j % 2));
+        if constexpr (DT == QM_F32) r.w[j] = gmem<const uint32_t>(T.grad)[p.at];
+        else r.w[j / 2] |= (unsigned)gmem<const uint16_t>(T.grad)[p.at] << (16 * (j % 2));
     }
     return r;
 }
 template <int DT> __device__ __forceinline__ void store_grad(const ListTensor &T, int64_t e, int n, const float *x) {
+    if (T.grad_cols == 0) {
+        store_edge<DT>(T.grad, e, n, x);
+        return;
+    }
+    GradPos p(T, e);
     if (T.grad_cols % 4 == 0) {
-        store_edge<DT>(T.grad, T.grad_cols == 0 ? e : grad_pos(T, e), n, x);
+        store_edge<DT>(T.grad, p.at, n, x);
         return;
     }
 #pragma unroll
-    for (int j = 0; j < 4; j++)
-        if (j < n) store_one<DT>(T.grad, grad_pos(T, e + j), x[j]);
+    for (int j = 0; j < 4; j++, p.next())
+        if (j < n) store_one<DT>(T.grad, p.at, x[j]);
 }
 
 }  // namespace

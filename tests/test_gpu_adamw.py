@@ -304,6 +304,32 @@ def test_repeats_bit_for_bit(bits):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_resume_bit_for_bit(bits):
+    """Ten steps equal five, a host copy of weight and state into fresh
+    buffers, and five more."""
+    def steps(p, plan, lo, hi):
+        for t in range(lo, hi):
+            p.grad.copy_(H.grad((p.n,), torch.bfloat16, DEV, 81, t, std=1e-2))
+            q.adamw_step(plan, t, **HP, rounding="stochastic", seed=6)
+
+    def new():
+        p = Param(12345, bits, torch.float32, torch.bfloat16, 80, zero=True)
+        return p, q.AdamWPlan([p.tuple()])
+
+    a, plan_a = new()
+    steps(a, plan_a, 1, 11)
+    b, plan_b = new()
+    steps(b, plan_b, 1, 6)
+    saved = [t.cpu() for t in [b.weight] + b.state.tensors()]
+    c, plan_c = new()
+    for t, x in zip([c.weight] + c.state.tensors(), saved):
+        t.copy_(x)
+    steps(c, plan_c, 6, 11)
+    for x, y in zip([a.weight] + a.state.tensors(), [c.weight] + c.state.tensors()):
+        assert torch.equal(x, y)
+
+
 def test_training_tracks_32_bit_states():
     """30 steps on noisy gradients: weights by stochastic 8-bit states stay
     within 5 % (Frobenius) of the way that 32-bit states take, block edges
