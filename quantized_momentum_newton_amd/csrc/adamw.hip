@@ -595,7 +595,15 @@ extern "C" qm_status adamw_step(const void *host_plan, const void *dev_plan, con
         const bool scaled = A.root * 0x1p-63f > 0x1p-24f * A.eps;
         const auto kernel = hp->rounding == QM_ROUND_STOCHASTIC ? (scaled ? adamw_kernel<8, true, true> : adamw_kernel<8, true, false>)
                                                                 : (scaled ? adamw_kernel<8, false, true> : adamw_kernel<8, false, false>);
-        kernel<<<grid, kThreads, 0, s>>>(A);
+        // Waves: with 7 per SIMD (what the registers allow), 4, 3 and 2 workgroups of
+        // 4 waves a CU, nearest codes, 218M elements: bf16 weight and gradient 367,
+        // 353, 348, 412 us; fp32 both 584, 587, 574, 549; fp32 weight, bf16 gradient
+        // and copy 587, 590, 587, 562.  17M: 30.6, 30.5, 31.2, 35.6; 45.9, 46.0, 46.6,
+        // 46.3; 47.1, 47.0, 46.6, 48.1; two break even at 33M.  Stochastic codes need
+        // their waves (fp32 weight, 206M: 474, 463, 460, 508).
+        const int64_t n8 = h->n_tasks - h->n_tasks32;
+        const bool two = hp->rounding == QM_ROUND_NEAREST && 2 * h->n_wide8 > n8 && n8 >= 1 << 15;
+        kernel<<<grid, kThreads, two ? 64u << 10 : wgs_per_cu(4), s>>>(A);
         if (qm_status e = launched("AdamW with 8-bit states")) return e;
     }
     return QM_OK;
@@ -610,7 +618,10 @@ extern "C" qm_status adamw_read_state(const void *host_plan, const void *dev_pla
     if (h->n_tasks == 0) return QM_OK;
     if (!m_out || !v_out) return fail(QM_E_ARG, "m_out and v_out must not be null");
     if (!aligned(m_out, 16) || !aligned(v_out, 16)) return fail(QM_E_ALIGN, "m_out and v_out need 16-byte alignment");
-    adamw_read_kernel<<<2 * grid_for(h->n_tasks), kThreads, 0, static_cast<hipStream_t>(stream)>>>(
+    // waves: 8 workgroups a CU as the registers allow, 6 and 3: 218M elements in 8
+    // bits 350, 343 and 531 us; 103M in 32 bits 269, 269 and 253
+    const unsigned lds = 2 * h->n_tasks32 > h->n_tasks ? wgs_per_cu(3) : wgs_per_cu(6);
+    adamw_read_kernel<<<2 * grid_for(h->n_tasks), kThreads, lds, static_cast<hipStream_t>(stream)>>>(
         list.tensors, list.owner, (int)h->n_tasks, m_out, v_out);
     return launched("AdamW state read");
 }

@@ -20,7 +20,7 @@
 namespace qm {
 
 constexpr uint32_t kListMagic = 0x54534c51u;  // "QLST"
-constexpr uint32_t kListVersion = 1;
+constexpr uint32_t kListVersion = 2;
 constexpr int kListTask = 1024;
 enum { kListGrads = 1, kListAdamW = 2 };
 
@@ -30,6 +30,8 @@ struct ListHeader {
     int64_t n_blocks, total_numel;
     int64_t n_tasks;          // of all tensors
     int64_t n_tasks32;        // tasks [0, n_tasks32): 32-bit states (grad lists: all)
+    int64_t n_wide_grad;      // tasks with an fp32 gradient
+    int64_t n_wide8;          // tasks with 8-bit states and an fp32 weight
     int64_t off_tensors;      // ListTensor[n_tensors], list order
     int64_t off_task_tensor;  // int32[n_tasks]
     int64_t total_bytes;
@@ -50,7 +52,7 @@ struct ListTensor {
 constexpr int64_t list_tasks(int64_t n, int64_t full) { return full + (n - full * kListTask + 255) / 256; }
 constexpr int64_t list_task_start(int64_t full, int64_t k) { return k < full ? k * kListTask : full * kListTask + (k - full) * 256; }
 
-static_assert(sizeof(ListHeader) == 72, "list header layout");
+static_assert(sizeof(ListHeader) == 88, "list header layout");
 static_assert(sizeof(ListTensor) == 128, "list tensor layout");
 
 // Reads and checks a host list blob of this kind (0: either); nullptr on

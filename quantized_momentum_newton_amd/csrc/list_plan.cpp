@@ -149,7 +149,10 @@ qm_status encode(const Tensor *tensors, int32_t n, int kind, void *host_blob, si
             int64_t &k = tasks[e.state_bits == 8];
             e.task_offset = k;
             e.full_tasks = e.grad_cols % 8 == 0 ? e.numel / kListTask : 0;
-            k += list_tasks(e.numel, e.full_tasks);
+            const int64_t nt = list_tasks(e.numel, e.full_tasks);
+            k += nt;
+            if (e.grad_dtype == QM_F32) h.n_wide_grad += nt;
+            if (e.state_bits == 8 && e.weight_dtype == QM_F32) h.n_wide8 += nt;
         }
         if (any_overlap(spans)) return fail(QM_E_ARG, "buffers of the list overlap");
         h.magic = kListMagic;
