@@ -8,11 +8,11 @@
 // and HBM binds: a large copy reaches 6.5 TB/s on this part, and of that
 //   32-bit states, fp32 weight, bf16 gradient and copy (28 bytes an element):
 //     218M elements in 1.03 ms, 5.9 TB/s;
-//   8-bit states, fp32 weight, bf16 gradient and copy (16.1): 206M in 0.55 ms,
-//     6.0 TB/s;
-//   8-bit states, bf16 weight and gradient (10.1): 218M in 0.37 ms, 5.9 TB/s,
+//   8-bit states, fp32 weight, bf16 gradient and copy (16.1): 206M in 0.535
+//     ms, 6.2 TB/s;
+//   8-bit states, bf16 weight and gradient (10.1): 218M in 0.35 ms, 6.25 TB/s,
 //     with the VALU busy 77 % of the time; with stochastic codes the VALU
-//     binds (84 %): 36M in 0.07 ms, 5.2 TB/s (975 instructions a task against
+//     binds (84 %): 36M in 0.07 ms, 5.1 TB/s (975 instructions a task against
 //     663; half of the difference makes the random numbers).
 //
 // One wave64 owns a task of 1024 consecutive elements of one tensor and issues

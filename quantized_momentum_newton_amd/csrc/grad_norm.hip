@@ -6,8 +6,8 @@
 // fp32.  Two launches: every workgroup adds its tasks in order into one
 // partial sum, one workgroup adds the partials in order, so the result does
 // not depend on timing.  Bound by HBM: the norm reads the gradients once (1.3G
-// in bf16: 0.40 ms, 6.6 TB/s), the scaling reads and writes them (0.84 ms, 6.3
-// TB/s; a large copy reaches 6.5).
+// in bf16: 0.40 ms, 6.6 TB/s), the scaling reads and writes them (0.81 ms, 6.5
+// TB/s, the rate of a large copy).
 #include <hip/hip_runtime.h>
 
 #include <math.h>
