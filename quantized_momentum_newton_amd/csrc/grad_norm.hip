@@ -30,8 +30,9 @@ constexpr int kFinishThreads = 1024; // two parts a thread: the pass over the pa
 // us for 1 to 64 tasks against 3.5 to 4.1 for the two launches, which cost
 // their caller 7.3 us where one costs 4.6; at 128 tasks 7.4 against 4.1.
 constexpr int kSmallTasks = 64;
-// Workgroups of the scaling pass: 0.84 ms for 1.3G bf16 gradients (6.3 TB/s)
-// with 128 threads, 0.87 with 256 or 64, 0.96 with 1024.
+// Workgroups of the scaling pass: 0.84 ms for 1.3G bf16 gradients with 128
+// threads, 0.87 with 256 or 64, 0.96 with 1024 (as many waves as fit; 0.81
+// with the limit at the launch).
 constexpr int kScaleThreads = 128;
 
 // Sum over the workgroup of WAVES waves, valid in thread 0.
