@@ -307,11 +307,9 @@ __device__ __forceinline__ void update_group(Grad grad, Weight weight, const Pac
 #pragma unroll
     for (int j = 0; j < N; j++) {
         const float g = grad(j) * c;
-        // code times step_m, rounded once: the code's byte plus 128 converts in
-        // one instruction, and the fused product takes the 128 steps off exactly
-        const float cm = (float)(((qm.w[j / 4] ^ 0x80808080u) >> (8 * (j % 4))) & 0xffu);
+        const float cm = (float)(int8_t)(qm.w[j / 4] >> (8 * (j % 4)));   // one instruction, as cv
         const float cv = (float)((qv.w[j / 4] >> (8 * (j % 4))) & 0xffu);
-        m[j] = __builtin_fmaf(cm, step_m, -128.0f * step_m) + A.omb1 * g;
+        m[j] = cm * step_m + A.omb1 * g;
         v[j] = (cv * cv) * step_v + A.omb2 * (g * g);
         tm = __builtin_elementwise_maximum(tm, fabsf(m[j]));
         tv = __builtin_elementwise_maximum(tv, fabsf(v[j]));
