@@ -549,7 +549,9 @@ QM_API qm_status grad_scale(const void *host_plan, const void *dev_plan,
  * key of qm_rounding, the tensor's index in this list), m_code' =
  * floor(x) + 1 if (r >> 16) 2^-16 < x - floor(x), else floor(x); v_code' =
  * k + 1 if y - k^2 > (r mod 2^15) 2^-15 (2k + 1), else k: the mean of the
- * code's square is y.  Clamped to the codes' ranges.
+ * code's square is y.  Clamped to the codes' ranges.  The two sides of every
+ * comparison here and above are exact numbers: x and y are binary32, the
+ * differences and products made from them are not rounded.
  * ---------------------------------------------------------------------- */
 typedef struct {
     void *weight;        /* weight_dtype [numel], in/out                     */

@@ -91,8 +91,8 @@ def coded_states(m_code, v_code, m_absmax, v_absmax, g, beta1, beta2, word=None)
             up = above > k + 0.5
         else:
             r = _blocks(word, np.uint32)
-            cm = np.floor(x)
-            cm = cm + ((r >> np.uint32(16)).astype(F) * F(2.0 ** -16) < x - cm)
+            cm = np.floor(x).astype(np.float64)
+            cm = cm + ((r >> np.uint32(16)).astype(np.float64) * 2.0 ** -16 < x - cm)     # exact
             up = above > (r & np.uint32(0x7FFF)).astype(np.float64) * 2.0 ** -15 * (2 * k + 1)
         cm = np.clip(cm, -127, 127)
         cv = np.where((v > 0) & (ok_v & (top_v > 0))[:, None], np.clip(k + up, 1, 255), 0)

@@ -1,0 +1,53 @@
+"""The coding of 8-bit AdamW states next to its borders, in the oracle: what
+the definition in include/qmuon.h says there, without a GPU."""
+import numpy as np
+import pytest
+
+from oracle import adamw as A
+
+
+def border_gradients(word):
+    """Per element (none of them a block's first) a gradient that lies, by its
+    place modulo 3, one fp32 step below, on or one above the border of its
+    random number u = word >> 16, where floor(x) + u / 2^16 = x, in [0, 1) for
+    u below 2^15 and in (-1, 0) else; a block's first is 127, so that with
+    beta1 = 0 and zero states x is the gradient itself.  Returns (gradients,
+    expected codes of m)."""
+    n = word.size
+    e = np.arange(n)
+    u = (word >> np.uint32(16)).astype(np.float64)
+    down = np.where(u < 32768, 0.0, -1.0)
+    on = (down + u / 65536).astype(np.float32)              # exact: 16 bits
+    side = e % 3 - 1
+    g = np.where(side < 0, np.nextafter(on, np.float32(-np.inf)), np.where(side > 0, np.nextafter(on, np.float32(np.inf)), on))
+    codes = np.where(side > 0, down + 1, down)
+    # one step below a whole number is the interval under it, and its fraction is above any u
+    codes = np.where((side < 0) & (u == 0), down, codes)
+    first = e % 256 == 0
+    return np.where(first, np.float32(127), g).astype(np.float32), np.where(first, 127, codes).astype(np.int8)
+
+
+def zero_state(n):
+    nb = -(-n // 256)
+    return np.zeros(n, np.int8), np.zeros(n, np.uint8), np.zeros(nb, np.float32), np.zeros(nb, np.float32)
+
+
+def test_stochastic_code_of_m_compares_exactly():
+    """floor(x) + 1 if u / 2^16 < x - floor(x): the difference is not rounded.
+    It has more than 24 bits for x in (-1/2, 0)."""
+    z = zero_state(256)
+    for x, u, want in ((-(0.5 - 2.0 ** -25), 32768, 0), (-(2.0 ** -16 - 2.0 ** -40), 65535, 0), (-(2.0 ** -16), 65535, -1),
+                       (-0.5, 32768, -1), (-(2.0 ** -60), 65535, 0), (2.0 ** -60, 0, 1), (0.25, 16384, 0), (0.0, 0, 0)):
+        g = np.zeros(256, np.float32)
+        g[0], g[1] = 127.0, x
+        assert g[1] == x
+        word = np.full(256, u << 16, np.uint32)
+        assert A.coded_states(*z, g, 0.0, 0.9, word)[0][1] == want, (x, u)
+
+
+@pytest.mark.parametrize("seed", [2, 77])
+def test_stochastic_codes_of_m_on_both_sides_of_their_borders(seed):
+    n = 256 * 64
+    word = A.words(n, seed, 3, 0)
+    g, want = border_gradients(word)
+    assert np.array_equal(A.coded_states(*zero_state(n), g, 0.0, 0.9, word)[0], want)

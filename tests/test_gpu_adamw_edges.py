@@ -8,6 +8,8 @@ import torch
 
 import quantized_momentum_newton_amd as q
 from gpu_util import say
+from oracle import adamw as A
+from test_adamw_borders_cpu import border_gradients
 from test_gpu_adamw import DEV, DTYPES, Param
 
 pytestmark = pytest.mark.gpu
@@ -37,3 +39,20 @@ def test_largest_finite_maxima(beta1, wdt, rounding):
         p.check(0, step, rounding=rounding, seed=21, hp=hp)
         assert torch.isfinite(p.state.m_absmax).all()
         p.snapshot()
+
+
+@pytest.mark.parametrize("wdt", ["f32", "bf16"])
+def test_stochastic_codes_of_m_on_both_sides_of_their_borders(wdt):
+    """Every element's m one fp32 step below, on, or one above the border that
+    its random number sets."""
+    n, seed, step = 256 * 4 * 50 + 3 * 256 + 77, (9 << 32) + 5, 3
+    word = A.words(n, seed, step, 0)
+    g, want = border_gradients(word)
+    p = Param(n, 8, DTYPES[wdt], torch.float32, 1300, zero=True)
+    p.grad.copy_(torch.from_numpy(g))
+    plan = q.AdamWPlan([p.tuple()])
+    q.adamw_step(plan, step, lr=1e-3, betas=(0.0, 0.9), eps=1e-8, rounding="stochastic", seed=seed)
+    torch.cuda.synchronize()
+    got = p.state.m.cpu().numpy()
+    bad = np.nonzero(got != want)[0]
+    assert bad.size == 0, (bad[:5], got[bad[:5]], want[bad[:5]], g[bad[:5]])
