@@ -3,8 +3,10 @@
 Muon steps the hidden matrices (int8 momentum, Newton-Schulz), AdamW the rest:
 embedding and head with 8-bit states, norm gains with 32-bit states.  One
 global norm over all gradients gives the clip factor; the Muon gradients are
-scaled by it in place, the AdamW step takes it as an argument, and a step
-whose norm is not finite leaves the AdamW parameters as they are.
+scaled by it in place, the AdamW step takes it as an argument.  A batch whose
+norm is not finite is left out as a whole: the AdamW step would write nothing
+by itself, but the Muon step reads its gradients whatever they hold, so the
+program looks at the factor before it.
 
 The data are synthetic: a fixed random permutation of the vocabulary, each
 token followed by its image, so a model that learns reaches a loss near 0.
@@ -91,12 +93,17 @@ class Optimizer:
         self.adamw_plan = q.AdamWPlan(entries)
 
     def step(self):
-        self.steps += 1
+        """One step; False, with no weight or state written, where the
+        gradients' norm is not finite."""
         q.grad_norm(self.all_grads, self.max_norm, norm=self.norm, coef=self.coef, ws=self.ws)
+        if self.coef.isnan().item():      # the host waits for the norm
+            return False
+        self.steps += 1
         q.grad_scale(self.muon_grads, self.coef)
         q.muon_step(self.muon_plan, None, self.mats, self.steps, self.muon_hp, ws=self.muon_ws)
         q.adamw_step(self.adamw_plan, self.steps, lr=self.lr_adamw, betas=(0.9, 0.99), grad_scale=self.coef,
                      rounding="stochastic", seed=1)
+        return True
 
 
 def main(steps=120, device="cuda", report=print):

@@ -475,7 +475,11 @@ QM_API qm_status grasp_step(const qm_grasp_state *state, int64_t rows,
  *   S = sum of g*g over every element (fp64);  norm = sqrt(S);
  *   coef = min(1, max_norm / (norm + eps)),  NaN if S is not finite.
  * coef stays on the device: adamw_step multiplies it into the gradients it
- * reads, grad_scale into gradients in place (those of the Muon step).
+ * reads, grad_scale into gradients in place (those of the Muon step).  A NaN
+ * coef stops adamw_step and grad_scale, not muon_step, muon_apply or
+ * grasp_step: these read the gradients whatever they hold, and an infinity
+ * or a NaN stays in their momentum.  A program that may meet one copies coef
+ * to the host and leaves the Muon step out where it is NaN.
  * ---------------------------------------------------------------------- */
 typedef struct {
     void *grad;         /* dtype, aligned to its element                     */

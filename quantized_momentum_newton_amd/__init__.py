@@ -554,7 +554,8 @@ def grad_norm(plan, max_norm=float("inf"), eps=1e-6, norm=None, coef=None, ws=No
 
 def grad_scale(plan, coef, stream=None):
     """Every gradient of the plan times coef (device fp32 [1]) in place; a NaN
-    coef leaves them as they are."""
+    coef leaves them as they are (and muon_step would read them as they are:
+    test coef before it)."""
     _require(coef, "coef", torch.float32, plan.device, numel=1)
     _check(_LIB.grad_scale(plan.hptr, plan.dptr, coef.data_ptr(), _queue(stream, plan)))
 
