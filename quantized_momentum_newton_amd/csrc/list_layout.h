@@ -22,6 +22,9 @@ namespace qm {
 constexpr uint32_t kListMagic = 0x54534c51u;  // "QLST"
 constexpr uint32_t kListVersion = 2;
 constexpr int kListTask = 1024;
+// A launch takes fewer than 2^32 threads: two workgroups of 256 for every four
+// tasks in a state read, the largest of the launches.
+constexpr int64_t kListMaxTasks = (((int64_t)1 << 32) / (2 * 256) - 1) * 4;
 enum { kListGrads = 1, kListAdamW = 2 };
 
 struct ListHeader {

@@ -161,8 +161,7 @@ qm_status encode(const Tensor *tensors, int32_t n, int kind, void *host_blob, si
         h.n_tensors = n;
         h.n_tasks32 = tasks[0];
         h.n_tasks = tasks[0] + tasks[1];
-        // a launch takes fewer than 2^32 threads, 64 a task, twice for a state read
-        if (h.n_tasks > 1 << 25) return fail(QM_E_UNSUPPORTED, "list too large");
+        if (h.n_tasks > kListMaxTasks) return fail(QM_E_UNSUPPORTED, "list too large");
         h.off_tensors = align_up(sizeof(ListHeader), 128);
         h.off_task_tensor = h.off_tensors + (int64_t)n * (int64_t)sizeof(ListTensor);
         h.total_bytes = align_up(h.off_task_tensor + h.n_tasks * 4, 64);
