@@ -472,6 +472,18 @@ def _grad_view(t, name):
     return t.shape[1], t.stride(0)
 
 
+def _plan_device(device, home):
+    """The device of a list whose tensors are on `home`: that one; a device that
+    is given has to name it."""
+    if device is not None:
+        given = torch.device(device)
+        if given.type == "cuda" and given.index is None:
+            given = torch.device("cuda", torch.cuda.current_device())
+        if given != home:
+            raise ValueError(f"a list is kept where its tensors are: on {home}, not on {given}")
+    return home
+
+
 class _ListPlan:
     """A tensor list encoded once and copied to the device once."""
 
@@ -492,20 +504,21 @@ class GradPlan(_ListPlan):
     """The gradients of a model, for their global norm.
 
     grads: list of fp32 / bf16 / f16 device tensors, each contiguous or a 2-D
-           view with unit column stride; none overlaps another."""
+           view with unit column stride; none overlaps another.
+    device: the tensors' device, if given."""
 
     def __init__(self, grads, device=None):
         if not grads:
             raise ValueError("no grads")
-        dev = device if device is not None else grads[0].device
+        home = _plan_device(device, grads[0].device)
         arr = (L.GradTensor * len(grads))()
         for i, g in enumerate(grads):
             cols, ld = _grad_view(g, f"grad {i}")
-            if g.device != grads[0].device:
-                raise ValueError(f"grad {i} is on {g.device}, expected {grads[0].device}")
+            if g.device != home:
+                raise ValueError(f"grad {i} is on {g.device}, expected {home}")
             arr[i] = L.GradTensor(g.data_ptr(), g.numel(), cols, ld, _dtype(g), 0)
         self._keep = list(grads)
-        self._finish(_encode_list(_LIB.qm_grad_plan_encode, arr, len(grads)), dev, [g.numel() for g in grads])
+        self._finish(_encode_list(_LIB.qm_grad_plan_encode, arr, len(grads)), home, [g.numel() for g in grads])
 
     def workspace_bytes(self):
         return _LIB.grad_norm_workspace_bytes(self.hptr)
@@ -600,12 +613,13 @@ class AdamWPlan(_ListPlan):
              weight fp32 / bf16 / f16, contiguous; grad of any of these types,
              contiguous or a 2-D view with unit column stride; state an
              AdamWState; copy None, or a bf16 / f16 tensor that receives the
-             new weight too; lr_scale a factor on the step's lr."""
+             new weight too; lr_scale a factor on the step's lr.
+    device: the tensors' device, if given."""
 
     def __init__(self, tensors, device=None):
         if not tensors:
             raise ValueError("no tensors")
-        home = tensors[0][0].device
+        home = _plan_device(device, tensors[0][0].device)
         arr = (L.AdamWTensor * len(tensors))()
         keep, numels = [], []
         for i, (weight, grad, state, copy, lr_scale, weight_decay) in enumerate(tensors):
@@ -625,8 +639,7 @@ class AdamWPlan(_ListPlan):
             keep += [weight, grad, copy, state]
             numels.append(n)
         self._keep = keep
-        self._finish(_encode_list(_LIB.qm_adamw_plan_encode, arr, len(tensors)),
-                     device if device is not None else home, numels)
+        self._finish(_encode_list(_LIB.qm_adamw_plan_encode, arr, len(tensors)), home, numels)
 
     def view(self, flat, i):
         """Tensor i's elements of a [256 * n_blocks] buffer (adamw_read_state)."""
