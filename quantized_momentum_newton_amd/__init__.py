@@ -527,13 +527,24 @@ class GradPlan(_ListPlan):
         return torch.empty(self.workspace_bytes(), dtype=torch.uint8, device=self.device)
 
 
-def _queue(stream, plan):
-    """The given stream, or torch's current one on the plan's device, as the
-    raw handle (torch.cuda.current_stream() builds a Stream object, which
-    costs as much as a launch)."""
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(plan.device.index)
+def _launch(plan, stream, entry, *args):
+    """entry(*args, queue) with the plan's device current (a launch on the
+    default queue goes to the device that is).  queue: that of the given
+    stream, or of torch's current one on the plan's device, as the raw handle
+    (torch.cuda.current_stream() builds a Stream object, which costs as much
+    as a launch)."""
+    index = plan.device.index
+    if stream is None:
+        queue = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        if stream.device != plan.device:
+            raise ValueError(f"the stream is on {stream.device}, the list on {plan.device}")
+        queue = stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        _check(entry(*args, queue))
+    else:
+        with torch.cuda.device(index):
+            _check(entry(*args, queue))
 
 
 def _new(count, dtype, plan, stream):
@@ -560,8 +571,8 @@ def grad_norm(plan, max_norm=float("inf"), eps=1e-6, norm=None, coef=None, ws=No
     norm, coef = _out(norm, "norm", 1, plan, stream), _out(coef, "coef", 1, plan, stream)
     if ws is None:
         ws = _new(plan.workspace_bytes(), torch.uint8, plan, stream)
-    _check(_LIB.grad_norm(plan.hptr, plan.dptr, max_norm, eps, norm.data_ptr(), coef.data_ptr(), ws.data_ptr(),
-                          ws.numel(), _queue(stream, plan)))
+    _launch(plan, stream, _LIB.grad_norm, plan.hptr, plan.dptr, max_norm, eps, norm.data_ptr(), coef.data_ptr(),
+            ws.data_ptr(), ws.numel())
     return norm, coef
 
 
@@ -570,7 +581,7 @@ def grad_scale(plan, coef, stream=None):
     coef leaves them as they are (and muon_step would read them as they are:
     test coef before it)."""
     _require(coef, "coef", torch.float32, plan.device, numel=1)
-    _check(_LIB.grad_scale(plan.hptr, plan.dptr, coef.data_ptr(), _queue(stream, plan)))
+    _launch(plan, stream, _LIB.grad_scale, plan.hptr, plan.dptr, coef.data_ptr())
 
 
 class AdamWState:
@@ -658,8 +669,8 @@ def adamw_step(plan, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, grad_scale=Non
         _require(grad_scale, "grad_scale", torch.float32, plan.device, numel=1)
     hp = L.AdamWHparams(lr, betas[0], betas[1], eps, step, ROUNDING[rounding],
                         (step if offset is None else offset) & 0xFFFFFFFF, seed)
-    _check(_LIB.adamw_step(plan.hptr, plan.dptr, ctypes.byref(hp),
-                           grad_scale.data_ptr() if grad_scale is not None else None, _queue(stream, plan)))
+    _launch(plan, stream, _LIB.adamw_step, plan.hptr, plan.dptr, ctypes.byref(hp),
+            grad_scale.data_ptr() if grad_scale is not None else None)
 
 
 def adamw_read_state(plan, m=None, v=None, stream=None):
@@ -667,5 +678,5 @@ def adamw_read_state(plan, m=None, v=None, stream=None):
     (given or new); plan.view(m, i) is tensor i's part.  Returns (m, v)."""
     n = plan.n_blocks * BLOCK
     m, v = _out(m, "m", n, plan, stream), _out(v, "v", n, plan, stream)
-    _check(_LIB.adamw_read_state(plan.hptr, plan.dptr, m.data_ptr(), v.data_ptr(), _queue(stream, plan)))
+    _launch(plan, stream, _LIB.adamw_read_state, plan.hptr, plan.dptr, m.data_ptr(), v.data_ptr())
     return m, v
