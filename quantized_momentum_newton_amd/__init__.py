@@ -571,8 +571,12 @@ def grad_norm(plan, max_norm=float("inf"), eps=1e-6, norm=None, coef=None, ws=No
     norm, coef = _out(norm, "norm", 1, plan, stream), _out(coef, "coef", 1, plan, stream)
     if ws is None:
         ws = _new(plan.workspace_bytes(), torch.uint8, plan, stream)
+    elif not isinstance(ws, torch.Tensor):
+        raise TypeError("ws must be a tensor")
+    else:
+        _require(ws, "ws", ws.dtype, plan.device)
     _launch(plan, stream, _LIB.grad_norm, plan.hptr, plan.dptr, max_norm, eps, norm.data_ptr(), coef.data_ptr(),
-            ws.data_ptr(), ws.numel())
+            ws.data_ptr(), ws.numel() * ws.element_size())
     return norm, coef
 
 
