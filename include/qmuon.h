@@ -503,8 +503,8 @@ QM_API qm_status qm_grad_plan_encode(const qm_grad_tensor *grads, int32_t n_grad
 QM_API size_t grad_norm_workspace_bytes(const void *host_plan);
 
 /* norm_out[0], coef_out[0]: device fp32 out, as defined above (max_norm > 0,
- * infinity allowed: coef is then 1; eps >= 0).  Fixed summation order, no
- * atomics.  ws: >= grad_norm_workspace_bytes, 8-byte aligned.
+ * infinity allowed: coef is then 1; eps >= 0), two different numbers.  Fixed
+ * summation order, no atomics.  ws: >= grad_norm_workspace_bytes, 8-byte aligned.
  * Errors: QM_E_ARG, QM_E_PLAN, QM_E_ALIGN, QM_E_WORKSPACE, QM_E_HIP. */
 QM_API qm_status grad_norm(const void *host_plan, const void *dev_plan,
                            double max_norm, double eps, float *norm_out,
@@ -603,7 +603,7 @@ QM_API qm_status adamw_step(const void *host_plan, const void *dev_plan,
 /* The values the states stand for, e.g. for a checkpoint that does not
  * depend on the state's form: element e of tensor t goes to m_out and v_out
  * [256 * (t's first block) + e] (fp32 [256 * qm_list_blocks], 16-byte
- * aligned); what lies between two tensors is set to 0.
+ * aligned, not overlapping); what lies between two tensors is set to 0.
  * Errors: QM_E_ARG, QM_E_ALIGN, QM_E_PLAN, QM_E_HIP. */
 QM_API qm_status adamw_read_state(const void *host_plan, const void *dev_plan,
                                   float *m_out, float *v_out, qm_stream_t stream);

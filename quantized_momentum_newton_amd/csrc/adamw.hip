@@ -616,6 +616,8 @@ extern "C" qm_status adamw_read_state(const void *host_plan, const void *dev_pla
     if (h->n_tasks == 0) return QM_OK;
     if (!m_out || !v_out) return fail(QM_E_ARG, "m_out and v_out must not be null");
     if (!aligned(m_out, 16) || !aligned(v_out, 16)) return fail(QM_E_ALIGN, "m_out and v_out need 16-byte alignment");
+    const uintptr_t m_at = (uintptr_t)m_out, v_at = (uintptr_t)v_out, bytes = (uintptr_t)h->n_blocks * kBlock * 4;
+    if (m_at < v_at + bytes && v_at < m_at + bytes) return fail(QM_E_ARG, "m_out and v_out overlap");
     // waves: 8 workgroups a CU as the registers allow, 6 and 3: 218M elements in 8
     // bits 350, 343 and 531 us; 103M in 32 bits 269, 269 and 253
     const unsigned lds = 2 * h->n_tasks32 > h->n_tasks ? wgs_per_cu(3) : wgs_per_cu(6);

@@ -207,6 +207,7 @@ extern "C" qm_status grad_norm(const void *host_plan, const void *dev_plan, doub
     if (!ws || ws_bytes < (parts + 1) * sizeof(double))
         return fail(QM_E_WORKSPACE, "workspace: need %zu bytes", (size_t)(parts + 1) * sizeof(double));
     if (!aligned(ws, 8)) return fail(QM_E_ALIGN, "workspace needs 8-byte alignment");
+    if (norm_out == coef_out) return fail(QM_E_ARG, "norm_out and coef_out must not share memory");
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if (h->n_tasks <= kSmallTasks) {
         grad_norm_small_kernel<<<1, kFinishThreads, 0, s>>>(list.tensors, list.owner, (int)h->n_tasks, max_norm, eps, norm_out, coef_out);
