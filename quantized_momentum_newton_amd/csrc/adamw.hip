@@ -572,6 +572,7 @@ extern "C" qm_status adamw_step(const void *host_plan, const void *dev_plan, con
     A.omb2 = (float)(1.0 - hp->beta2);
     A.step = (float)(hp->lr / (1.0 - pow(hp->beta1, (double)hp->step)));
     A.lr = (float)hp->lr;
+    if (!isfinite(A.step) || !isfinite(A.lr)) return fail(QM_E_ARG, "lr, or lr / (1 - beta1^step), is too large for fp32");
     A.root = (float)(1.0 / sqrt(1.0 - pow(hp->beta2, (double)hp->step)));
     A.eps = (float)hp->eps;
     A.seed = hp->seed;
