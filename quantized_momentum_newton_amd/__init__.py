@@ -472,6 +472,19 @@ def _grad_view(t, name):
     return t.shape[1], t.stride(0)
 
 
+def _same_order(a, b):
+    """Whether two shapes of one size number their elements alike: one merges
+    dimensions of the other (a flat view, a matrix for a stack of matrices)."""
+    def ends(shape):
+        below, n = {1}, 1
+        for d in reversed(shape):
+            n *= d
+            below.add(n)
+        return below
+
+    return ends(a) <= ends(b) or ends(b) <= ends(a)
+
+
 def _plan_device(device, home):
     """The device of a list whose tensors are on `home`: that one; a device that
     is given has to name it."""
@@ -628,7 +641,9 @@ class AdamWPlan(_ListPlan):
              weight fp32 / bf16 / f16, contiguous; grad of any of these types,
              contiguous or a 2-D view with unit column stride; state an
              AdamWState; copy None, or a bf16 / f16 tensor that receives the
-             new weight too; lr_scale a factor on the step's lr.
+             new weight too; lr_scale a factor on the step's lr.  The shapes
+             of weight, grad and copy are equal, or one merges dimensions of
+             the other (a flat view).
     device: the tensors' device, if given."""
 
     def __init__(self, tensors, device=None):
@@ -647,6 +662,9 @@ class AdamWPlan(_ListPlan):
                 raise ValueError(f"tensor {i}: grad and state must be on {home}")
             if copy is not None:
                 _require(copy, f"copy {i}", copy.dtype, home, numel=n)
+            for t, name in ((grad, "grad"), (copy, "copy")):
+                if t is not None and not _same_order(t.shape, weight.shape):
+                    raise ValueError(f"{name} {i} has shape {tuple(t.shape)}, the weight {tuple(weight.shape)}")
             p = [t.data_ptr() if t is not None else None
                  for t in (weight, grad, state.m, state.v, state.m_absmax, state.v_absmax, copy)]
             arr[i] = L.AdamWTensor(*p, n, cols, ld, _dtype(weight), _dtype(grad),
