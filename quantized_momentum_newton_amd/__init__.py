@@ -663,7 +663,7 @@ class AdamWPlan(_ListPlan):
             if copy is not None:
                 _require(copy, f"copy {i}", copy.dtype, home, numel=n)
             for t, name in ((grad, "grad"), (copy, "copy")):
-                if t is not None and not _same_order(t.shape, weight.shape):
+                if t is not None and t.shape != weight.shape and not _same_order(t.shape, weight.shape):
                     raise ValueError(f"{name} {i} has shape {tuple(t.shape)}, the weight {tuple(weight.shape)}")
             p = [t.data_ptr() if t is not None else None
                  for t in (weight, grad, state.m, state.v, state.m_absmax, state.v_absmax, copy)]
