@@ -493,8 +493,9 @@ typedef struct {
 
 /* Build a grad-list blob (host only; touches no GPU), used like a norm plan:
  * the caller copies it verbatim to the device once (64-byte aligned) and
- * passes both copies.  host_blob == NULL asks for the size, as in
- * qm_plan_encode.  Errors: QM_E_ARG (null, counts, overlapping buffers),
+ * passes both copies.  The blob holds the buffers' addresses: a buffer that
+ * moves (a gradient allocated anew each step) needs a new blob.
+ * host_blob == NULL asks for the size, as in qm_plan_encode.  Errors: QM_E_ARG (null, counts, overlapping buffers),
  * QM_E_ALIGN, QM_E_DTYPE, QM_E_SHAPE, QM_E_UNSUPPORTED. */
 QM_API qm_status qm_grad_plan_encode(const qm_grad_tensor *grads, int32_t n_grads,
                                      void *host_blob, size_t *inout_blob_bytes);

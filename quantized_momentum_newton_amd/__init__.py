@@ -498,7 +498,9 @@ def _plan_device(device, home):
 
 
 class _ListPlan:
-    """A tensor list encoded once and copied to the device once."""
+    """A tensor list encoded once and copied to the device once.  It holds the
+    tensors' addresses (and keeps the tensors alive): a call works on the
+    buffers that were there when the list was made."""
 
     def _finish(self, host, device, numels):
         self.host, self.device = host, device
@@ -518,6 +520,11 @@ class GradPlan(_ListPlan):
 
     grads: list of fp32 / bf16 / f16 device tensors, each contiguous or a 2-D
            view with unit column stride; none overlaps another.
+           The list keeps their addresses, so they have to stay the buffers
+           that backward writes: a gradient that is set to None (the default
+           of torch's zero_grad) comes back elsewhere, and the list would go
+           on with the old one.  Clear them in place
+           (zero_grad(set_to_none=False)), or make a new list.
     device: the tensors' device, if given."""
 
     def __init__(self, grads, device=None):
@@ -644,6 +651,8 @@ class AdamWPlan(_ListPlan):
              new weight too; lr_scale a factor on the step's lr.  The shapes
              of weight, grad and copy are equal, or one merges dimensions of
              the other (a flat view).
+             All of them, the state's buffers too, have to stay where they
+             are, as the gradients of a GradPlan.
     device: the tensors' device, if given."""
 
     def __init__(self, tensors, device=None):
