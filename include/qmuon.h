@@ -554,7 +554,10 @@ QM_API qm_status grad_scale(const void *host_plan, const void *dev_plan,
  * key of qm_rounding, the tensor's index in this list), m_code' =
  * floor(x) + 1 if (r >> 16) 2^-16 < x - floor(x), else floor(x); v_code' =
  * k + 1 if y - k^2 > (r mod 2^15) 2^-15 (2k + 1), else k: the mean of the
- * code's square is y.  Clamped to the codes' ranges.  The two sides of every
+ * code's square is y for y >= 1.  For 0 < y < 1 the code is 1 always (as with
+ * nearest rounding, no smaller one is kept where v > 0), so v reads too large
+ * there, by the factor 1 / y, until it passes its block's smallest code or
+ * its block's maximum falls.  Clamped to the codes' ranges.  The two sides of every
  * comparison here and above are exact numbers: x and y are binary32, the
  * differences and products made from them are not rounded.
  * ---------------------------------------------------------------------- */

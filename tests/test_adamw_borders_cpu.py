@@ -51,3 +51,25 @@ def test_stochastic_codes_of_m_on_both_sides_of_their_borders(seed):
     word = A.words(n, seed, 3, 0)
     g, want = border_gradients(word)
     assert np.array_equal(A.coded_states(*zero_state(n), g, 0.0, 0.9, word)[0], want)
+
+
+@pytest.mark.parametrize("y", [1e-6, 0.1, 0.5, 0.99, 1.0, 1.01, 1.5, 2.5, 3.99, 4.0, 50.3, 1000.7, 64000.0])
+def test_mean_of_the_square_of_stochastic_codes_of_v(y):
+    """E[code^2] = y from y = 1 on (within 6 standard errors); below, the code
+    is 1 always, so a decoded v is at least one code of its block: more than v
+    by the factor 1 / y."""
+    n = 256 * 1000
+    g = np.full(n, np.sqrt(np.float32(y)), np.float32)
+    g[::256] = 255.0                      # every block's maximum: 65025, so that y = v = g * g
+    code = A.coded_states(*zero_state(n), g, 0.9, 0.0, A.words(n, 13, 1, 0))[1].astype(np.float64)
+    assert np.all(code[::256] == 255)
+    body = code[np.arange(n) % 256 != 0]
+    exact = float(g[1]) ** 2
+    if y < 1:
+        assert np.all(body == 1)
+    else:
+        k = np.floor(np.sqrt(exact))
+        assert np.all((body == k) | (body == k + 1))
+        spread = np.sqrt(max((exact - k * k) * ((k + 1) ** 2 - exact), 0.0) / body.size)
+        # the random number has 15 bits: its mean threshold is half a step (2k + 1) 2^-16 low
+        assert abs((body ** 2).mean() - exact) <= 6 * spread + (2 * k + 1) * 2.0 ** -16 + 2.0 ** -22 * exact
