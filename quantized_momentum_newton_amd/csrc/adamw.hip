@@ -63,7 +63,7 @@ __device__ __forceinline__ float new_weight(float w, float m, float v, float ste
     const bool tiny = SCALED && v < 0x1p-96f;
     const float r = __builtin_amdgcn_sqrtf(tiny ? v * 0x1p64f : v);
     const float denom = __builtin_fmaf(r, tiny ? A.root * 0x1p-32f : A.root, A.eps);
-    return __builtin_fmaf(-step, m * __builtin_amdgcn_rcpf(denom), __builtin_fmaf(-decay, w, w));
+    return in_fp32(__builtin_fmaf(-step, m * __builtin_amdgcn_rcpf(denom), __builtin_fmaf(-decay, w, w)));
 }
 
 template <int DT> __device__ __forceinline__ void store_weight(const ListTensor &T, int64_t e, int n, const float *w) {

@@ -147,7 +147,7 @@ template <int DT> __device__ __forceinline__ void task_scale(const ListTensor &T
         for (int p = 0; p < P; p++) {
             float x[N];
 #pragma unroll
-            for (int j = 0; j < N; j++) x[j] = unpack<DT>(r[p], j) * c;
+            for (int j = 0; j < N; j++) x[j] = in_fp32(unpack<DT>(r[p], j) * c);
             r[p] = pack<DT, N>(x);
         }
         store_grad_task<DT, N, P>(T, e_task, lane, r);
@@ -157,7 +157,7 @@ template <int DT> __device__ __forceinline__ void task_scale(const ListTensor &T
     const PackedOf<DT, 4> r = load_grad<DT>(T, e_task + lane * 4, n);
     float x[4];
 #pragma unroll
-    for (int j = 0; j < 4; j++) x[j] = unpack<DT>(r, j) * c;
+    for (int j = 0; j < 4; j++) x[j] = in_fp32(unpack<DT>(r, j) * c);
     store_grad<DT>(T, e_task + lane * 4, n, x);
 }
 

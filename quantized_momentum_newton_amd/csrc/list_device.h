@@ -61,6 +61,14 @@ template <int DT, int BYTES> __device__ __forceinline__ float unpack(const Packe
         return DT == QM_BF16 ? bf16_val(h) : f16_val(h);
     }
 }
+// x as the fp32 number it is.  The empty asm keeps a conversion to f16 apart
+// from the product or sum that made x: fused into one instruction
+// (v_fma_mixlo_f16) they round once, and a result next to a border of f16
+// depends on whether the compiler fused.
+__device__ __forceinline__ float in_fp32(float x) {
+    asm("" : "+v"(x));
+    return x;
+}
 template <int DT, int N> __device__ __forceinline__ PackedOf<DT, N> pack(const float *x) {
     PackedOf<DT, N> r;
 #pragma unroll
