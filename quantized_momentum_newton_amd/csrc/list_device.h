@@ -117,54 +117,26 @@ __device__ __forceinline__ int64_t task_start(const ListTensor &T, int64_t k, in
     return e;
 }
 
-// Positions in a strided gradient's buffer (numel < 2^32) of element e and,
-// step by step, of the elements after it: one division for a lane's group.
-struct GradPos {
-    int64_t at, jump;
-    uint32_t col, cols;
-    __device__ __forceinline__ GradPos(const ListTensor &T, int64_t e) {
-        cols = (uint32_t)T.grad_cols;
-        const uint32_t u = (uint32_t)e, row = u / cols;
-        col = u - row * cols;
-        at = (int64_t)row * T.grad_ld + col;
-        jump = T.grad_ld - T.grad_cols;
-    }
-    __device__ __forceinline__ void next() {
-        at++;
-        if (++col == cols) {
-            col = 0;
-            at += jump;
-        }
-    }
-};
-
 // Calls access(p, base, off) for a lane's groups of N elements in a whole task
 // of the gradient, group p at element p * 64 N + lane * N: base and byte
-// offset of its first element (a group lies in one row).  Rows of a task's
-// length or more: a task meets at most one row end, so one scalar division
-// serves the wave (the other branch divides per group).
+// offset of its first element (a group lies in one row).  Where a task meets
+// at most one row end, one scalar division serves the wave; the last branch
+// divides per group.
 template <int DT, int N, int PARTS, typename Access>
 __device__ __forceinline__ void grad_task(const ListTensor &T, int64_t e_task, int lane, Access access) {
     constexpr int S = kSizeOf<DT>;
-    const uint32_t cols = (uint32_t)T.grad_cols, at = (uint32_t)e_task;
-    const int64_t jump = T.grad_ld - T.grad_cols;
     if (T.grad_cols == 0) {
 #pragma unroll
         for (int p = 0; p < PARTS; p++) access(p, T.grad + (uint64_t)e_task * S, (uint32_t)(p * 64 + lane) * N * S);
-    } else if (T.grad_cols >= kListTask && jump < 1 << 28) {
-        const uint32_t row = at / cols, col = at - row * cols;
-        const uint64_t base = T.grad + (uint64_t)((int64_t)row * T.grad_ld + col) * S;
+        return;
+    }
+    const GradPos first(T, (uint32_t)e_task);
+    if (first.near_all()) {
 #pragma unroll
-        for (int p = 0; p < PARTS; p++) {
-            const uint32_t i = (p * 64 + lane) * N;
-            access(p, base, (i + (col + i >= cols ? (uint32_t)jump : 0u)) * S);
-        }
+        for (int p = 0; p < PARTS; p++) access(p, T.grad + (uint64_t)first.at * S, first.offset((p * 64 + lane) * N) * S);
     } else {
 #pragma unroll
-        for (int p = 0; p < PARTS; p++) {
-            const uint32_t u = at + (p * 64 + lane) * N, row = u / cols;
-            access(p, T.grad + (uint64_t)((int64_t)row * T.grad_ld + (int64_t)(u - row * cols)) * S, 0);
-        }
+        for (int p = 0; p < PARTS; p++) access(p, T.grad + (uint64_t)GradPos(T, (uint32_t)e_task + (p * 64 + lane) * N).at * S, 0);
     }
 }
 
@@ -180,7 +152,7 @@ __device__ __forceinline__ void store_grad_task(const ListTensor &T, int64_t e_t
 // Elements e .. e + n - 1 of the gradient, n <= 4.
 template <int DT> __device__ __forceinline__ PackedOf<DT, 4> load_grad(const ListTensor &T, int64_t e, int n) {
     if (T.grad_cols == 0) return load_edge<DT>(T.grad, e, n);
-    GradPos p(T, e);
+    GradPos p(T, (uint32_t)e);
     if (T.grad_cols % 4 == 0) return load_edge<DT>(T.grad, p.at, n);   // in one row
     PackedOf<DT, 4> r = {};
 #pragma unroll
@@ -196,7 +168,7 @@ template <int DT> __device__ __forceinline__ void store_grad(const ListTensor &T
         store_edge<DT>(T.grad, e, n, x);
         return;
     }
-    GradPos p(T, e);
+    GradPos p(T, (uint32_t)e);
     if (T.grad_cols % 4 == 0) {
         store_edge<DT>(T.grad, p.at, n, x);
         return;

@@ -55,6 +55,33 @@ struct ListTensor {
 constexpr int64_t list_tasks(int64_t n, int64_t full) { return full + (n - full * kListTask + 255) / 256; }
 constexpr int64_t list_task_start(int64_t full, int64_t k) { return k < full ? k * kListTask : full * kListTask + (k - full) * 256; }
 
+// Position, in elements, in a strided gradient's buffer (numel < 2^32) of
+// element e, by one division, and, step by step, of the elements after it.
+struct GradPos {
+    int64_t at = 0, jump = 0;
+    uint32_t col = 0, cols = 0;
+    constexpr GradPos(const ListTensor &T, uint32_t e) {
+        cols = (uint32_t)T.grad_cols;
+        const uint32_t row = e / cols;
+        col = e - row * cols;
+        at = (int64_t)row * T.grad_ld + col;
+        jump = T.grad_ld - T.grad_cols;
+    }
+    constexpr void next() {
+        at++;
+        if (++col == cols) {
+            col = 0;
+            at += jump;
+        }
+    }
+    // Whether a whole task's positions are 32-bit byte offsets from its first
+    // element's (this one): rows of a task's length or more, so that it meets
+    // at most one row end, and a jump there that fits.
+    constexpr bool near_all() const { return cols >= kListTask && jump < 1 << 28; }
+    // Then: from the first element to element i of the task.
+    constexpr uint32_t offset(uint32_t i) const { return i + (col + i >= cols ? (uint32_t)jump : 0u); }
+};
+
 static_assert(sizeof(ListHeader) == 88, "list header layout");
 static_assert(sizeof(ListTensor) == 128, "list tensor layout");
 
