@@ -47,11 +47,12 @@ def weight(w0, m, v, step, lr, beta1, beta2, eps, weight_decay):
     return w0 - lr * weight_decay * w0 - lr * hat
 
 
-def words(numel, seed, offset, tensor):
-    """32-bit random word of every element: Philox4x32-10, counter (element / 4
-    as two words, offset, tensor), key seed."""
+def words(numel, seed, offset, tensor, first=0):
+    """32-bit random word of every element from `first` (a multiple of 4) on:
+    Philox4x32-10, counter (element / 4 as two words, offset, tensor), key
+    seed."""
     mask, n4 = np.uint64(0xFFFFFFFF), -(-numel // 4)
-    q = np.arange(n4, dtype=np.uint64)
+    q = np.arange(first // 4, first // 4 + n4, dtype=np.uint64)
     sh = np.uint64(32)
     c = [q & mask, q >> sh, np.full(n4, offset, np.uint64), np.full(n4, tensor, np.uint64)]
     k0, k1 = seed & 0xFFFFFFFF, seed >> 32

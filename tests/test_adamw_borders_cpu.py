@@ -3,6 +3,7 @@ the definition in include/qmuon.h says there, without a GPU."""
 import numpy as np
 import pytest
 
+import oracle
 from oracle import adamw as A
 
 
@@ -73,3 +74,14 @@ def test_mean_of_the_square_of_stochastic_codes_of_v(y):
         spread = np.sqrt(max((exact - k * k) * ((k + 1) ** 2 - exact), 0.0) / body.size)
         # the random number has 15 bits: its mean threshold is half a step (2k + 1) 2^-16 low
         assert abs((body ** 2).mean() - exact) <= 6 * spread + (2 * k + 1) * 2.0 ** -16 + 2.0 ** -22 * exact
+
+
+def test_words_from_an_element_on():
+    """The counter's second word is used from element 2^34 on."""
+    assert np.array_equal(A.words(100, 5, 6, 7)[40:], A.words(60, 5, 6, 7, first=40))
+    for first in (1 << 32, (1 << 34) - 4, 1 << 34):
+        w = A.words(8, (3 << 32) + 9, 77, 5, first=first)
+        for e in range(8):
+            group = (first + e) // 4
+            ref = oracle.philox4x32_10([group & 0xFFFFFFFF, group >> 32, 77, 5], [9, 3])
+            assert w[e] == ref[e % 4]
