@@ -594,14 +594,14 @@ extern "C" qm_status adamw_step(const void *host_plan, const void *dev_plan, con
         const bool scaled = A.root * 0x1p-63f > 0x1p-24f * A.eps;
         const auto kernel = hp->rounding == QM_ROUND_STOCHASTIC ? (scaled ? adamw_kernel<8, true, true> : adamw_kernel<8, true, false>)
                                                                 : (scaled ? adamw_kernel<8, false, true> : adamw_kernel<8, false, false>);
-        // Waves: with 7 per SIMD (what the registers allow), 4, 3 and 2 workgroups of
-        // 4 waves a CU, nearest codes, 218M elements: bf16 weight and gradient 367,
-        // 353, 348, 412 us; fp32 both 584, 587, 574, 549; fp32 weight, bf16 gradient
-        // and copy 587, 590, 587, 562.  17M: 30.6, 30.5, 31.2, 35.6; 45.9, 46.0, 46.6,
-        // 46.3; 47.1, 47.0, 46.6, 48.1; two break even at 33M.  Stochastic codes need
-        // their waves (fp32 weight, 206M: 474, 463, 460, 508).
+        // Workgroups a CU: as many as fit (7), 4, 2.  Nearest codes, bf16 weight and
+        // gradient: 17M elements 30.3, 30.9, 35.1 us, 216M 356, 351, 408; fp32 both:
+        // 33M 87.8, 87.9, 88.1, 67M 174, 175, 172, 216M 582, 584, 550; fp32 weight,
+        // bf16 gradient: 33M 77.2, 77.7, 78.7, 67M 153, 154, 154, 216M 499, 497, 486;
+        // a tenth of it bf16 weights: 108M 239, 241, 241, a quarter: 230, 231, 234.
+        // Stochastic codes need their waves (fp32 weight, 216M: 493, 484, 540).
         const int64_t n8 = h->n_tasks - h->n_tasks32;
-        const bool two = hp->rounding == QM_ROUND_NEAREST && 2 * h->n_wide8 > n8 && n8 >= 1 << 15;
+        const bool two = hp->rounding == QM_ROUND_NEAREST && 10 * h->n_wide8 >= 9 * n8 && n8 >= 1 << 16;
         kernel<<<grid, kThreads, two ? 64u << 10 : wgs_per_cu(4), s>>>(A);
         if (qm_status e = launched("AdamW with 8-bit states")) return e;
     }
@@ -619,9 +619,11 @@ extern "C" qm_status adamw_read_state(const void *host_plan, const void *dev_pla
     if (!aligned(m_out, 16) || !aligned(v_out, 16)) return fail(QM_E_ALIGN, "m_out and v_out need 16-byte alignment");
     const uintptr_t m_at = (uintptr_t)m_out, v_at = (uintptr_t)v_out, bytes = (uintptr_t)h->n_blocks * kBlock * 4;
     if (m_at < v_at + bytes && v_at < m_at + bytes) return fail(QM_E_ARG, "m_out and v_out overlap");
-    // waves: 8 workgroups a CU as the registers allow, 6 and 3: 218M elements in 8
-    // bits 350, 343 and 531 us; 103M in 32 bits 269, 269 and 253
-    const unsigned lds = 2 * h->n_tasks32 > h->n_tasks ? wgs_per_cu(3) : wgs_per_cu(6);
+    // Workgroups a CU: as many as fit (8), 6, 3.  States in 8 bits: 4M elements 8.1,
+    // 7.8, 9.5 us, 216M 350, 338, 519; in 32 bits: 4M 12.1, 13.5, 13.2, 6M 18.8,
+    // 18.1, 17.7, 108M 279, 281, 264; three quarters of the tasks 32 bits: 4M 10.2,
+    // 10.7, 11.7, 6M 17.8, 16.6, 16.7, 108M 250, 250, 239; 55 %: 108M 232, 234, 265.
+    const unsigned lds = 4 * h->n_tasks32 < 3 * h->n_tasks ? wgs_per_cu(6) : h->n_tasks < 6 << 10 ? 0u : wgs_per_cu(3);
     adamw_read_kernel<<<2 * grid_for(h->n_tasks), kThreads, lds, static_cast<hipStream_t>(stream)>>>(
         list.tensors, list.owner, (int)h->n_tasks, m_out, v_out);
     return launched("AdamW state read");

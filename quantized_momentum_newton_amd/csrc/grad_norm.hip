@@ -229,9 +229,11 @@ extern "C" qm_status grad_scale(const void *host_plan, const void *dev_plan, con
     if (!aligned(coef, 4)) return fail(QM_E_ALIGN, "coef needs 4-byte alignment");
     if (h->n_tasks == 0) return QM_OK;
     constexpr int waves = kScaleThreads / 64;
-    // waves: 16 workgroups a CU as fit, 11 and 4: 1.3G bf16 gradients 825, 805 and
-    // 1098 us; 206M in fp32 288, 278 and 263
-    const unsigned lds = 2 * h->n_wide_grad > h->n_tasks ? wgs_per_cu(4) : wgs_per_cu(11);
+    // Workgroups a CU: as many as fit (16), 11, 4.  fp32: 17M elements 23.0, 22.5,
+    // 22.5 us, 108M 149, 143, 137; nine tenths of the tasks fp32: 22.2, 22.1, 22.0
+    // and 141, 136, 132; three quarters: 20.3, 20.1, 20.7 and 130, 124, 124; bf16:
+    // 12.2, 12.2, 15.3 and 69, 68, 87.
+    const unsigned lds = 10 * h->n_wide_grad >= 9 * h->n_tasks ? wgs_per_cu(4) : wgs_per_cu(11);
     grad_scale_kernel<<<(unsigned)((h->n_tasks + waves - 1) / waves), kScaleThreads, lds, static_cast<hipStream_t>(stream)>>>(
         list.tensors, list.owner, (int)h->n_tasks, coef);
     return launched("gradient scale");
