@@ -505,6 +505,9 @@ class _ListPlan:
     def _finish(self, host, device, numels):
         self.host, self.device = host, device
         self.dev = host.to(device)
+        # the queues that its memory is known to be used on (torch's allocator orders the one it was made on)
+        self.queues = {torch._C._cuda_getCurrentRawStream(device.index)} if device.type == "cuda" else None
+        self.only_device = device.type == "cuda" and torch.cuda.device_count() == 1
         self.hptr, self.dptr = ctypes.c_void_p(host.data_ptr()), ctypes.c_void_p(self.dev.data_ptr())
         self.numels = numels
         self.n_blocks = _LIB.qm_list_blocks(self.hptr)
@@ -560,11 +563,17 @@ def _launch(plan, stream, entry, *args):
         if stream.device != plan.device:
             raise ValueError(f"the stream is on {stream.device}, the list on {plan.device}")
         queue = stream.cuda_stream
-    if torch._C._cuda_getDevice() == index:
-        _check(entry(*args, queue))
+    if plan.queues is not None and queue not in plan.queues:
+        # freed while the call is pending, the list's device copy must not be given out again
+        plan.dev.record_stream(stream if stream is not None else torch.cuda.current_stream(index))
+        plan.queues.add(queue)
+    if plan.only_device or torch._C._cuda_getDevice() == index:
+        status = entry(*args, queue)
     else:
         with torch.cuda.device(index):
-            _check(entry(*args, queue))
+            status = entry(*args, queue)
+    if status:
+        raise QmuonError(status)
 
 
 def _new(count, dtype, plan, stream):
@@ -591,12 +600,10 @@ def grad_norm(plan, max_norm=float("inf"), eps=1e-6, norm=None, coef=None, ws=No
     norm, coef = _out(norm, "norm", 1, plan, stream), _out(coef, "coef", 1, plan, stream)
     if ws is None:
         ws = _new(plan.workspace_bytes(), torch.uint8, plan, stream)
-    elif not isinstance(ws, torch.Tensor):
-        raise TypeError("ws must be a tensor")
-    else:
-        _require(ws, "ws", ws.dtype, plan.device)
+    elif not isinstance(ws, torch.Tensor) or ws.device != plan.device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {plan.device}")
     _launch(plan, stream, _LIB.grad_norm, plan.hptr, plan.dptr, max_norm, eps, norm.data_ptr(), coef.data_ptr(),
-            ws.data_ptr(), ws.numel() * ws.element_size())
+            ws.data_ptr(), ws.nbytes)
     return norm, coef
 
 
