@@ -7,13 +7,13 @@
 // gives the step.  Every byte of gradient, weight and state is touched once,
 // and HBM binds: a large copy reaches 6.5 TB/s on this part, and of that
 //   32-bit states, fp32 weight, bf16 gradient and copy (28 bytes an element):
-//     218M elements in 1.03 ms, 5.9 TB/s;
-//   8-bit states, fp32 weight, bf16 gradient and copy (16.1): 206M in 0.535
+//     218M elements in 1.04 ms, 5.9 TB/s;
+//   8-bit states, fp32 weight, bf16 gradient and copy (16.1): 206M in 0.53
 //     ms, 6.2 TB/s;
-//   8-bit states, bf16 weight and gradient (10.1): 218M in 0.35 ms, 6.25 TB/s,
-//     with the VALU busy 77 % of the time; with stochastic codes the VALU
-//     binds (84 %): 36M in 0.07 ms, 5.1 TB/s (975 instructions a task against
-//     663; half of the difference makes the random numbers).
+//   8-bit states, bf16 weight and gradient (10.1): 218M in 0.35 ms, 6.2 TB/s,
+//     with the VALU busy 76 % of the time; with stochastic codes the VALU
+//     binds (82 %): 36M in 0.072 ms, 5.0 TB/s (979 instructions a task against
+//     669; half of the difference makes the random numbers).
 //
 // One wave64 owns a task of 1024 consecutive elements of one tensor and issues
 // all of its loads before the arithmetic (half the task a wave: 1.09 ms for the
@@ -307,7 +307,10 @@ __device__ __forceinline__ void update_group(Grad grad, Weight weight, const Pac
 #pragma unroll
     for (int j = 0; j < N; j++) {
         const float g = grad(j) * c;
-        const float cm = (float)(int8_t)(qm.w[j / 4] >> (8 * (j % 4)));   // one instruction, as cv
+        // Signed, one instruction as cv.  (The byte plus 128, with 128 steps taken
+        // off in a fused product, is 1 % faster on 218M bf16 elements, 352 us for
+        // 357, but 128 steps leave fp32's range next to its end.)
+        const float cm = (float)(int8_t)(qm.w[j / 4] >> (8 * (j % 4)));
         const float cv = (float)((qv.w[j / 4] >> (8 * (j % 4))) & 0xffu);
         m[j] = cm * step_m + A.omb1 * g;
         v[j] = (cv * cv) * step_v + A.omb2 * (g * g);
@@ -482,7 +485,7 @@ template <int BITS, bool SR, bool SCALED> __global__ __launch_bounds__(kThreads,
 
 // The values the states stand for.  Even workgroups read m, odd ones v, of
 // the same four tasks: a workgroup with one stream in and one out runs 218M
-// elements in 8 bits in 0.345 ms (6.3 TB/s, near the rate of a large copy), one
+// elements in 8 bits in 0.34 ms (6.4 TB/s, near the rate of a large copy), one
 // with both took 0.40.  Codes are loaded through the caches (what a step has
 // just written may still be there), values stored past them.
 __global__ __launch_bounds__(kThreads) void adamw_read_kernel(const ListTensor *tensors, const int32_t *owner, int n_tasks,
@@ -589,7 +592,7 @@ extern "C" qm_status adamw_step(const void *host_plan, const void *dev_plan, con
         A.task_hi = (int32_t)h->n_tasks;
         const unsigned grid = grid_for(A.task_hi - A.task_lo);
         // The 8-bit kernel is held up by its instructions as much as by memory
-        // (VALU busy 77 to 84 %): it keeps the root of subnormal moments only where that
+        // (VALU busy 76 to 82 %): it keeps the root of subnormal moments only where that
         // root, at most 2^-63, is more than half a step of eps.
         const bool scaled = A.root * 0x1p-63f > 0x1p-24f * A.eps;
         const auto kernel = hp->rounding == QM_ROUND_STOCHASTIC ? (scaled ? adamw_kernel<8, true, true> : adamw_kernel<8, true, false>)
