@@ -580,7 +580,8 @@ typedef struct {
 } qm_adamw_tensor;
 
 typedef struct {
-    double lr, beta1, beta2, eps;  /* 0 <= beta < 1, eps >= 2^-126           */
+    double lr, beta1, beta2, eps;  /* 0 <= beta < 1, eps >= 2^-126; lr and
+                                      lr / (1 - beta1^t) finite in fp32      */
     int64_t step;        /* t, 1-based                                       */
     int32_t rounding;    /* qm_rounding of 8-bit states                      */
     uint32_t offset;     /* counter word 2 of stochastic rounding            */
@@ -588,7 +589,10 @@ typedef struct {
 } qm_adamw_hparams;
 
 /* Build an AdamW list blob (host only); use as qm_grad_plan_encode's.  All
- * buffers aligned to their elements, none overlapping another. */
+ * buffers aligned to their elements, none overlapping another.  A list has
+ * at most 2^25 - 4 tasks of 1024 elements (256 at a tensor's end, and
+ * throughout a tensor whose grad's rows are strided and no multiple of 8),
+ * else QM_E_UNSUPPORTED; so has a grad list. */
 QM_API qm_status qm_adamw_plan_encode(const qm_adamw_tensor *tensors, int32_t n_tensors,
                                       void *host_blob, size_t *inout_blob_bytes);
 
