@@ -20,6 +20,8 @@ def test_a_list_dropped_while_a_side_stream_uses_it(given):
     weights = [torch.ones(n, device=DEV) for _ in range(count)]
     states = [q.AdamWState(n, 32) for _ in range(count)]
     side = torch.cuda.Stream()
+    q.grad_norm(q.GradPlan(grads))                # loads the kernels, which takes longer than a sleep
+    q.adamw_step(q.AdamWPlan([(torch.ones(n, device=DEV), grads[0], q.AdamWState(n, 32), None, 1.0, 0.0)]), 1)
     torch.cuda.synchronize()
     side.wait_stream(torch.cuda.current_stream())
     plans = [q.GradPlan(grads), q.AdamWPlan([(w, g, s, None, 1.0, 0.0) for w, g, s in zip(weights, grads, states)])]
@@ -27,7 +29,7 @@ def test_a_list_dropped_while_a_side_stream_uses_it(given):
     at = [p.dev.data_ptr() for p in plans]
     torch.cuda.synchronize()
     with torch.cuda.stream(side):
-        torch.cuda._sleep(20_000_000)
+        torch.cuda._sleep(100_000_000)
         if not given:
             norm, coef = q.grad_norm(plans[0], 1.0)
             q.adamw_step(plans[1], 1, lr=0.1)
