@@ -2,7 +2,8 @@
  * qmuon.h -- C ABI of libqmuon.so: one Muon optimizer step on an AMD MI355X
  * (gfx950), as a blockwise-int8 momentum update followed by quintic
  * Newton-Schulz orthogonalisation; next to it the AdamW step of the
- * parameters Muon does not fit and the global gradient norm.
+ * parameters Muon does not fit, the global gradient norm, and the operators
+ * that make the gradients from activations kept in 8 bits.
  *
  * Conventions shared by every entry point
  *   - Pointers are device pointers unless a parameter says "host".
@@ -615,6 +616,120 @@ QM_API qm_status adamw_step(const void *host_plan, const void *dev_plan,
  * Errors: QM_E_ARG, QM_E_ALIGN, QM_E_PLAN, QM_E_HIP. */
 QM_API qm_status adamw_read_state(const void *host_plan, const void *dev_plan,
                                   float *m_out, float *v_out, qm_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * What makes the gradients: activations kept in 8 bits from the forward to
+ * the backward pass, the weight gradient that is formed from them, the gated
+ * activation between two products, the embedding and its gradient.  Results go
+ * to the gradient buffers that the steps above read, whole or added to what
+ * they hold (accumulate = 1: several batches a step, a tied table).
+ *
+ * Matrices are rows x cols with a row pitch ld in elements (cols <= ld <=
+ * 2^24 - 16) and aligned to their elements; a matrix without elements may be
+ * null.  Fastest are rows of a multiple of 8 elements at 16-byte addresses.
+ * An output shares no memory with another buffer of its call (columns of one
+ * wider buffer are separate buffers).
+ * ---------------------------------------------------------------------- */
+
+/* A rows x cols matrix in 8 bits: one E4M3 byte an element (format of
+ * qmuon_update_mxfp8_carrier) and one scale byte for 32 consecutive rows of a
+ * column (the last group takes the remainder):
+ *   value(r, c) = E4M3(data[r * ld + c]) * 2^(scale[(r / 32) * ld + c] - 127).
+ * Coding: scale - 127 = e, the smallest integer with max|x| <= 448 * 2^e over
+ * the group, between -95 and 119; data = E4M3(x * 2^-e), rounded to nearest
+ * even, at most 448.  A value is off by at most 1/16 of itself, or by 2^-10 *
+ * 2^e where it is below 2^-6 * 2^e, and exact in fp32 and bf16.  A group that
+ * holds an infinity or a NaN decodes to NaN as a whole.  Rows share a scale,
+ * not columns: an activation's outliers keep to their columns, and a weight
+ * gradient contracts over the rows. */
+typedef struct {
+    uint8_t *data;       /* [rows * ld], 16-byte aligned                     */
+    uint8_t *scale;      /* [ceil(rows / 32) * ld], 16-byte aligned          */
+    int64_t rows, cols;
+    int64_t ld;          /* multiple of 16, cols <= ld <= 2^24 - 16; bytes
+                            past cols may be written                         */
+} qm_act8;
+
+/* kept = x in 8 bits.  Errors: QM_E_ARG, QM_E_ALIGN, QM_E_DTYPE, QM_E_SHAPE,
+ * QM_E_UNSUPPORTED (more than 2^25 patches of 32 x 128), QM_E_HIP. */
+QM_API qm_status act_pack(const void *x, int32_t dtype, int64_t ld,
+                          const qm_act8 *kept, qm_stream_t stream);
+
+/* out = the values kept stands for, rounded to nearest even into its dtype.
+ * Errors: as act_pack. */
+QM_API qm_status act_read(const qm_act8 *kept, void *out, int32_t dtype,
+                          int64_t ld, qm_stream_t stream);
+
+/* Gradient of a linear layer's weight (n x k) over rows tokens:
+ *   out[i][j] (= or +=) sum over t of dy[t][i] * x[t][j]
+ * dy: rows x n, bf16 or f16.  x: rows x k of the same type, or null with
+ * `kept` in its place (its values, in f16 rounded to f16).  Products exact,
+ * sums in fp32 in an order that the sizes determine; the result is rounded
+ * once.  out: any dtype.  rows = 0: zeros, or nothing to add.
+ *   ws: >= weight_grad_workspace_bytes(rows, n, k) bytes (0: none needed),
+ *   16-byte aligned.
+ * Errors: QM_E_ARG, QM_E_ALIGN, QM_E_DTYPE, QM_E_SHAPE, QM_E_WORKSPACE,
+ * QM_E_UNSUPPORTED (more than 2^22 tiles of 128 or 256 squared), QM_E_HIP. */
+QM_API size_t weight_grad_workspace_bytes(int64_t rows, int64_t n, int64_t k);
+QM_API qm_status weight_grad(const void *dy, int32_t dtype, int64_t ld_dy,
+                             const void *x, int64_t ld_x, const qm_act8 *kept,
+                             int64_t rows, int64_t n, int64_t k, void *out,
+                             int32_t out_dtype, int64_t ld_out,
+                             int32_t accumulate, void *ws, size_t ws_bytes,
+                             qm_stream_t stream);
+
+/* Gated activation of a feed-forward block: h = act(gate) * up, in fp32,
+ * rounded once.  QM_ACT_SILU: act(g) = g / (1 + exp(-g)); QM_ACT_GELU:
+ * act(g) = g / 2 * (1 + tanh(sqrt(2 / pi) * (g + 0.044715 g^3))).
+ *   gate8, up8: both null, or what receives gate and up in 8 bits (as
+ *   act_pack codes them) for the backward pass.
+ * gate, up and h: rows x cols, one dtype.  Errors: as act_pack. */
+typedef enum { QM_ACT_SILU = 0, QM_ACT_GELU = 1 } qm_act;
+QM_API qm_status gated_act_forward(const void *gate, int64_t ld_gate,
+                                   const void *up, int64_t ld_up, int32_t dtype,
+                                   int64_t rows, int64_t cols, int32_t act,
+                                   void *h, int64_t ld_h, const qm_act8 *gate8,
+                                   const qm_act8 *up8, qm_stream_t stream);
+
+/* Its backward pass at the kept values g, u of gate and up:
+ *   dgate = dh * u * act'(g);   dup = dh * act(g);
+ *   h (nullable): act(g) * u, for the weight gradient of the product that
+ *   follows.
+ * dh, dgate, dup and h: one dtype.  Errors: as act_pack. */
+QM_API qm_status gated_act_backward(const qm_act8 *gate8, const qm_act8 *up8,
+                                    const void *dh, int64_t ld_dh, int32_t dtype,
+                                    int32_t act, void *dgate, int64_t ld_dgate,
+                                    void *dup, int64_t ld_dup, void *h,
+                                    int64_t ld_h, qm_stream_t stream);
+
+/* out[i] = scale * table[tokens[i]], rounded once; a token outside [0, vocab)
+ * (padding) gives a row of zeros.  tokens: contiguous int32 or int64
+ * (token_bits); fewer than 2^30 tokens and values.  Errors: QM_E_ARG, QM_E_ALIGN, QM_E_DTYPE,
+ * QM_E_SHAPE, QM_E_UNSUPPORTED (more than 2^34 pieces of 8 columns),
+ * QM_E_HIP. */
+QM_API qm_status embedding_lookup(const void *tokens, int32_t token_bits,
+                                  int64_t n_tokens, const void *table,
+                                  int32_t table_dtype, int64_t ld_table,
+                                  int64_t vocab, int64_t cols, float scale,
+                                  void *out, int32_t out_dtype, int64_t ld_out,
+                                  qm_stream_t stream);
+
+/* Its gradient: grad[v] (= or +=) scale * sum of dy[i] over tokens[i] = v, in
+ * fp32, in an order that the tokens determine, rounded once.  With accumulate
+ * only rows that have tokens are touched.  A token outside [0, vocab) has no
+ * part in it.
+ *   ws: >= embedding_grad_workspace_bytes(n_tokens, vocab, cols) bytes,
+ *   16-byte aligned.
+ * Errors: as embedding_lookup, and QM_E_WORKSPACE. */
+QM_API size_t embedding_grad_workspace_bytes(int64_t n_tokens, int64_t vocab,
+                                             int64_t cols);
+QM_API qm_status embedding_grad(const void *tokens, int32_t token_bits,
+                                int64_t n_tokens, const void *dy,
+                                int32_t dy_dtype, int64_t ld_dy, void *grad,
+                                int32_t grad_dtype, int64_t ld_grad,
+                                int64_t vocab, int64_t cols, float scale,
+                                int32_t accumulate, void *ws, size_t ws_bytes,
+                                qm_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Launch timing (measurement aid, off by default).

@@ -23,6 +23,12 @@ Entry points (same names as the C ABI in include/qmuon.h):
   GradPlan, grad_norm, grad_scale  global gradient norm, clip factor, clipping in place
   AdamWState, AdamWPlan, adamw_step, adamw_read_state
                                    AdamW over many tensors, states in 32 or 8 bits
+  ActCheckpoint, act_pack, act_read
+                                   activations kept in 8 bits for the backward pass
+  weight_grad                      weight gradient from the output's gradient and the input (kept or not)
+  gated_act_forward, gated_act_backward
+                                   act(gate) * up, writing and reading what is kept of them
+  embedding_lookup, embedding_grad scaled rows of a table, and the table's gradient
   timing_enable, timing_read       per-kernel-class launch timing (HIP events)
 """
 import ctypes
@@ -718,3 +724,265 @@ def adamw_read_state(plan, m=None, v=None, stream=None):
     m, v = _out(m, "m", n, plan, stream), _out(v, "v", n, plan, stream)
     _launch(plan, stream, _LIB.adamw_read_state, plan.hptr, plan.dptr, m.data_ptr(), v.data_ptr())
     return m, v
+
+
+# ---------------------------------------------------------------- gradients
+
+ACTIVATIONS = {"silu": L.QM_ACT_SILU, "gelu": L.QM_ACT_GELU}
+GROUP_ROWS = 32      # rows of a column that share a scale in an ActCheckpoint
+
+
+def _call(device, stream, entry, *args):
+    """entry(*args, queue) with `device` current, as _launch."""
+    if device.type != "cuda":
+        raise ValueError(f"the tensors are on {device}, not on a GPU")
+    index = device.index
+    if stream is None:
+        queue = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        queue = stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        status = entry(*args, queue)
+    else:
+        with torch.cuda.device(index):
+            status = entry(*args, queue)
+    if status:
+        raise QmuonError(status)
+
+
+def _alloc(shape, dtype, device, stream):
+    """As _new: a tensor in the pool of the stream that will use it."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _matrix(t, name, device=None, shape=None, dtype=None):
+    """(address, qm_dtype, row pitch) of a 2-D tensor with unit column stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, not {t.dim()}")
+    rows, cols = t.shape
+    code = _DTYPES.get(t.dtype)
+    if code is None or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name} is {t.dtype}" + (f", expected {dtype}" if dtype is not None else ", which is not supported"))
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if shape is not None and (rows, cols) != shape:
+        raise ValueError(f"{name} has shape {(rows, cols)}, expected {shape}")
+    ld = t.stride(0) if rows > 1 else cols
+    if (cols > 1 and t.stride(1) != 1) or ld < cols:
+        raise ValueError(f"{name} needs unit column stride and rows that do not overlap")
+    return t.data_ptr(), code, ld
+
+
+def _space(ws, nbytes, device, stream):
+    """(address, bytes) of a workspace: the given one, or a new one, which is
+    returned with them so that it lives through the call."""
+    if ws is None:
+        ws = _alloc(nbytes, torch.uint8, device, stream) if nbytes else None
+    elif not isinstance(ws, torch.Tensor) or ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {device}")
+    return (None, 0, ws) if ws is None else (ws.data_ptr(), ws.nbytes, ws)
+
+
+class ActCheckpoint:
+    """A rows x cols activation in 8 bits (the layout of qm_act8): data uint8
+    (E4M3) [rows, ld], scale uint8 (E8M0) [ceil(rows / 32), ld], ld the columns
+    rounded up to a multiple of 16.  Buffers that are given are used as they
+    are, their row length being ld."""
+
+    def __init__(self, rows, cols, device="cuda", data=None, scale=None):
+        if rows < 0 or cols < 0:
+            raise ValueError(f"bad size {rows} x {cols}")
+        given = data if data is not None else scale
+        home = given.device if given is not None else torch.device(device)
+        ld = given.shape[-1] if given is not None else -(-cols // 16) * 16
+        groups = -(-rows // GROUP_ROWS)
+        if data is None:
+            data = torch.empty((rows, ld), dtype=torch.uint8, device=home)
+        if scale is None:
+            scale = torch.empty((groups, ld), dtype=torch.uint8, device=home)
+        _require(data, "data", torch.uint8, home, shape=(rows, ld))
+        _require(scale, "scale", torch.uint8, home, shape=(groups, ld))
+        if ld % 16 or ld < cols:
+            raise ValueError(f"rows of {ld} bytes: a multiple of 16 that holds {cols} columns is needed")
+        self.rows, self.cols, self.data, self.scale, self.device = rows, cols, data, scale, data.device
+        self.shape = (rows, cols)
+        self.c = L.Act8(data.data_ptr(), scale.data_ptr(), rows, cols, ld)
+
+    @property
+    def nbytes(self):
+        return self.data.nbytes + self.scale.nbytes
+
+
+def _kept(ckpt, name, shape, device, stream):
+    """ckpt, checked, or a new one for None."""
+    if ckpt is None:
+        ld = -(-shape[1] // 16) * 16
+        return ActCheckpoint(*shape, data=_alloc((shape[0], ld), torch.uint8, device, stream),
+                             scale=_alloc((-(-shape[0] // GROUP_ROWS), ld), torch.uint8, device, stream))
+    if not isinstance(ckpt, ActCheckpoint):
+        raise TypeError(f"{name} must be an ActCheckpoint")
+    if ckpt.shape != shape:
+        raise ValueError(f"{name} is {ckpt.rows} x {ckpt.cols}, expected {shape[0]} x {shape[1]}")
+    if ckpt.device != device:
+        raise ValueError(f"{name} is on {ckpt.device}, expected {device}")
+    return ckpt
+
+
+def act_pack(x, ckpt=None, stream=None):
+    """x (rows x cols, unit column stride) in 8 bits: an ActCheckpoint, given
+    or new."""
+    p, dt, ld = _matrix(x, "x")
+    ckpt = _kept(ckpt, "ckpt", tuple(x.shape), x.device, stream)
+    _call(x.device, stream, _LIB.act_pack, p, dt, ld, ckpt.c)
+    return ckpt
+
+
+def act_read(ckpt, out=None, dtype=torch.bfloat16, stream=None):
+    """The values an ActCheckpoint stands for (exact in fp32 and bf16), in
+    `out` or a new tensor of `dtype`."""
+    if not isinstance(ckpt, ActCheckpoint):
+        raise TypeError("ckpt must be an ActCheckpoint")
+    if out is None:
+        out = _alloc(ckpt.shape, dtype, ckpt.device, stream)
+    p, dt, ld = _matrix(out, "out", ckpt.device, ckpt.shape)
+    _call(ckpt.device, stream, _LIB.act_read, ckpt.c, p, dt, ld)
+    return out
+
+
+def weight_grad_workspace_bytes(rows, n, k):
+    return _LIB.weight_grad_workspace_bytes(rows, n, k)
+
+
+def weight_grad_workspace(dy, x, out):
+    """A workspace for weight_grad on tensors of these sizes."""
+    return torch.empty(weight_grad_workspace_bytes(dy.shape[0], *out.shape), dtype=torch.uint8, device=out.device)
+
+
+def weight_grad(dy, x, out, accumulate=False, ws=None, stream=None):
+    """out (n x k, any dtype) = dy^T x, or out + dy^T x: the gradient of a
+    linear layer's weight from dy (rows x n, bf16 / f16), the gradient of its
+    output, and its input x, a rows x k tensor of dy's type or an
+    ActCheckpoint.  All with unit column stride.  Returns out."""
+    pd, dt, ldd = _matrix(dy, "dy")
+    if dt == L.QM_F32:
+        raise TypeError("dy must be bf16 or f16")
+    rows, n = dy.shape
+    device = dy.device
+    if isinstance(x, ActCheckpoint):
+        k = x.cols
+        if x.rows != rows or x.device != device:
+            raise ValueError(f"x is {x.rows} x {x.cols} on {x.device}, dy {rows} x {n} on {device}")
+        px, ldx, kept = None, 0, x.c
+    else:
+        px, _, ldx = _matrix(x, "x", device, dtype=dy.dtype)
+        if x.shape[0] != rows:
+            raise ValueError(f"x has {x.shape[0]} rows, dy {rows}")
+        k, kept = x.shape[1], None
+    po, ot, ldo = _matrix(out, "out", device, (n, k))
+    pw, nw, ws = _space(ws, _LIB.weight_grad_workspace_bytes(rows, n, k) if ws is None else 0, device, stream)
+    _call(device, stream, _LIB.weight_grad, pd, dt, ldd, px, ldx, kept, rows, n, k, po, ot, ldo, bool(accumulate), pw, nw)
+    return out
+
+
+def gated_act_forward(gate, up, gate_ckpt=None, up_ckpt=None, out=None, act="silu", keep=True, stream=None):
+    """act(gate) * up (act: "silu" or "gelu", the tanh form) and, with keep,
+    gate and up in 8 bits for the backward pass: (h, gate_ckpt, up_ckpt), given
+    or new; the checkpoints are None without keep.  gate and up: rows x cols
+    with unit column stride, e.g. the two halves of one product."""
+    pg, dt, ldg = _matrix(gate, "gate")
+    shape, device = tuple(gate.shape), gate.device
+    pu, _, ldu = _matrix(up, "up", device, shape, gate.dtype)
+    if out is None:
+        out = _alloc(shape, gate.dtype, device, stream)
+    ph, _, ldh = _matrix(out, "out", device, shape, gate.dtype)
+    if keep:
+        gate_ckpt = _kept(gate_ckpt, "gate_ckpt", shape, device, stream)
+        up_ckpt = _kept(up_ckpt, "up_ckpt", shape, device, stream)
+    elif gate_ckpt is not None or up_ckpt is not None:
+        raise ValueError("checkpoints are given, but not to be kept")
+    _call(device, stream, _LIB.gated_act_forward, pg, ldg, pu, ldu, dt, *shape, ACTIVATIONS[act], ph, ldh,
+          gate_ckpt.c if keep else None, up_ckpt.c if keep else None)
+    return out, gate_ckpt, up_ckpt
+
+
+def gated_act_backward(gate_ckpt, up_ckpt, dh, dgate=None, dup=None, h=None, recompute=False, act="silu", stream=None):
+    """Gradients of gate and up from dh, the gradient of act(gate) * up, at the
+    kept values; with recompute (or h given) the activation again, for the
+    weight gradient of the product after it.  Returns (dgate, dup, h), given or
+    new, h None without recompute."""
+    pd, dt, ldd = _matrix(dh, "dh")
+    shape, device = tuple(dh.shape), dh.device
+    for ckpt, name in ((gate_ckpt, "gate_ckpt"), (up_ckpt, "up_ckpt")):
+        if ckpt is None:
+            raise TypeError(f"{name} must be an ActCheckpoint")
+        _kept(ckpt, name, shape, device, stream)
+    if dgate is None:
+        dgate = _alloc(shape, dh.dtype, device, stream)
+    if dup is None:
+        dup = _alloc(shape, dh.dtype, device, stream)
+    if h is None and recompute:
+        h = _alloc(shape, dh.dtype, device, stream)
+    pg, _, ldg = _matrix(dgate, "dgate", device, shape, dh.dtype)
+    pu, _, ldu = _matrix(dup, "dup", device, shape, dh.dtype)
+    ph, _, ldh = _matrix(h, "h", device, shape, dh.dtype) if h is not None else (None, 0, 0)
+    _call(device, stream, _LIB.gated_act_backward, gate_ckpt.c, up_ckpt.c, pd, ldd, dt, ACTIVATIONS[act], pg, ldg, pu,
+          ldu, ph, ldh)
+    return dgate, dup, h
+
+
+def _tokens(tokens, device):
+    """(address, bits) of contiguous int32 or int64 tokens."""
+    if not isinstance(tokens, torch.Tensor) or tokens.dtype not in (torch.int32, torch.int64):
+        raise TypeError("tokens must be an int32 or int64 tensor")
+    if not tokens.is_contiguous():
+        raise ValueError("tokens must be contiguous")
+    if tokens.device != device:
+        raise ValueError(f"tokens are on {tokens.device}, expected {device}")
+    return tokens.data_ptr(), 64 if tokens.dtype == torch.int64 else 32
+
+
+def embedding_lookup(tokens, table, scale=1.0, out=None, dtype=None, stream=None):
+    """scale * table[tokens] as a [number of tokens, cols] tensor of `dtype`
+    (the table's if not given) or in `out`; zeros for a token outside the
+    table (padding).  tokens: contiguous int32 / int64 of any shape."""
+    pt, tt, ldt = _matrix(table, "table")
+    device, (vocab, cols) = table.device, table.shape
+    pk, bits = _tokens(tokens, device)
+    n = tokens.numel()
+    if out is None:
+        out = _alloc((n, cols), dtype if dtype is not None else table.dtype, device, stream)
+    po, ot, ldo = _matrix(out, "out", device, (n, cols))
+    _call(device, stream, _LIB.embedding_lookup, pk, bits, n, pt, tt, ldt, vocab, cols, scale, po, ot, ldo)
+    return out
+
+
+def embedding_grad_workspace_bytes(n_tokens, vocab, cols):
+    return _LIB.embedding_grad_workspace_bytes(n_tokens, vocab, cols)
+
+
+def embedding_grad_workspace(tokens, dy, grad):
+    """A workspace for embedding_grad on tensors of these sizes."""
+    return torch.empty(embedding_grad_workspace_bytes(tokens.numel(), *grad.shape), dtype=torch.uint8, device=grad.device)
+
+
+def embedding_grad(tokens, dy, grad, scale=1.0, accumulate=False, ws=None, stream=None):
+    """Gradient of embedding_lookup's table from dy ([number of tokens, cols]):
+    grad ([vocab, cols]) is written whole, or added to in the rows that have
+    tokens.  Sums have an order that the tokens determine: the same call gives
+    the same bits.  Returns grad."""
+    pg, gt, ldg = _matrix(grad, "grad")
+    device, (vocab, cols) = grad.device, grad.shape
+    pk, bits = _tokens(tokens, device)
+    n = tokens.numel()
+    pd, dt, ldd = _matrix(dy, "dy", device, (n, cols))
+    pw, nw, ws = _space(ws, _LIB.embedding_grad_workspace_bytes(n, vocab, cols) if ws is None else 0, device, stream)
+    _call(device, stream, _LIB.embedding_grad, pk, bits, n, pd, dt, ldd, pg, gt, ldg, vocab, cols, scale,
+          bool(accumulate), pw, nw)
+    return grad

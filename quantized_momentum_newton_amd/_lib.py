@@ -14,6 +14,7 @@ STATUS_NAMES = {0: "QM_OK", 1: "QM_E_ARG", 2: "QM_E_ALIGN", 3: "QM_E_DTYPE",
                 4: "QM_E_SHAPE", 5: "QM_E_WORKSPACE", 6: "QM_E_HIP",
                 7: "QM_E_UNSUPPORTED", 8: "QM_E_PLAN"}
 QM_F32, QM_BF16, QM_F16 = 0, 1, 2
+QM_ACT_SILU, QM_ACT_GELU = 0, 1
 QM_NS_BF16, QM_NS_F32, QM_NS_BF16X3 = 0, 1, 2
 QM_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -77,6 +78,10 @@ class AdamWHparams(ctypes.Structure):
                 ("rounding", c_i32), ("offset", ctypes.c_uint32), ("seed", ctypes.c_uint64)]
 
 
+class Act8(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("scale", c_void_p), ("rows", c_i64), ("cols", c_i64), ("ld", c_i64)]
+
+
 # name -> (restype, argtypes); every symbol include/qmuon.h declares.
 SIGNATURES = {
     "qm_plan_encode": (c_i32, [ctypes.POINTER(Q8Tensor), c_i32, ctypes.POINTER(NormSegment),
@@ -127,6 +132,20 @@ SIGNATURES = {
     "qm_list_blocks": (c_i64, [c_void_p]),
     "adamw_step": (c_i32, [c_void_p, c_void_p, ctypes.POINTER(AdamWHparams), c_void_p, c_void_p]),
     "adamw_read_state": (c_i32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "act_pack": (c_i32, [c_void_p, c_i32, c_i64, ctypes.POINTER(Act8), c_void_p]),
+    "act_read": (c_i32, [ctypes.POINTER(Act8), c_void_p, c_i32, c_i64, c_void_p]),
+    "weight_grad_workspace_bytes": (c_size, [c_i64, c_i64, c_i64]),
+    "weight_grad": (c_i32, [c_void_p, c_i32, c_i64, c_void_p, c_i64, ctypes.POINTER(Act8), c_i64, c_i64, c_i64,
+                            c_void_p, c_i32, c_i64, c_i32, c_void_p, c_size, c_void_p]),
+    "gated_act_forward": (c_i32, [c_void_p, c_i64, c_void_p, c_i64, c_i32, c_i64, c_i64, c_i32, c_void_p, c_i64,
+                                  ctypes.POINTER(Act8), ctypes.POINTER(Act8), c_void_p]),
+    "gated_act_backward": (c_i32, [ctypes.POINTER(Act8), ctypes.POINTER(Act8), c_void_p, c_i64, c_i32, c_i32, c_void_p,
+                                   c_i64, c_void_p, c_i64, c_void_p, c_i64, c_void_p]),
+    "embedding_lookup": (c_i32, [c_void_p, c_i32, c_i64, c_void_p, c_i32, c_i64, c_i64, c_i64, c_f32, c_void_p, c_i32,
+                                 c_i64, c_void_p]),
+    "embedding_grad_workspace_bytes": (c_size, [c_i64, c_i64, c_i64]),
+    "embedding_grad": (c_i32, [c_void_p, c_i32, c_i64, c_void_p, c_i32, c_i64, c_void_p, c_i32, c_i64, c_i64, c_i64,
+                               c_f32, c_i32, c_void_p, c_size, c_void_p]),
     "qm_timing_enable": (c_i32, [c_i32]),
     "qm_timing_read": (c_i32, [c_i32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(c_i64)]),
     "qm_hbm_stream_copy": (c_i32, [c_void_p, c_void_p, c_size, c_void_p]),

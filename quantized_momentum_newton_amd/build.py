@@ -31,6 +31,9 @@ UNITS = [
     ("hbm_stream.hip", []),
     ("adamw.hip", ["-ffp-contract=off"]),
     ("grad_norm.hip", []),
+    ("act8.hip", []),
+    ("weight_grad.hip", []),
+    ("embedding.hip", []),
     ("plan.cpp", []),
     ("list_plan.cpp", []),
     ("timing.cpp", ["-D__HIP_PLATFORM_AMD__", "-I", "/opt/rocm/include"]),

@@ -1,0 +1,305 @@
+// Activations kept in 8 bits between the forward and the backward pass, and
+// the gated activation that writes and reads them.
+//
+//   e      = the smallest integer with max|x| <= 448 * 2^e over 32 rows of a
+//            column, between -95 and 119
+//   data   = E4M3(x * 2^-e), rounded to nearest even;  scale = e + 127
+//   value  = data * 2^e: exact in fp32 and in bf16
+//
+//   h  = act(g) u;    dg = dh u act'(g),  du = dh act(g)
+//   silu: act = g s, act' = s (1 + g (1 - s)), s = 1 / (1 + exp(-g))
+//   gelu (tanh form): act = g s, act' = s + g s (1 - s) z', s = 1 / (1 + exp(-z)),
+//         z = 2 sqrt(2 / pi) (g + 0.044715 g^3)      (1 + tanh(z / 2) = 2 s)
+//
+// Every kernel passes once over its elements.  The forward of the gated
+// activation codes g and u from the registers that h is formed from; the
+// backward reads 2 bytes of g and u an element instead of 4.
+#include <algorithm>
+#include <type_traits>
+
+#include "act8_device.h"
+#include "act_host.h"
+
+namespace qm {
+namespace {
+
+constexpr int kWaves = 4;
+
+__device__ __forceinline__ int64_t wave_patch() {
+    return __builtin_amdgcn_readfirstlane((int)(blockIdx.x * kWaves + threadIdx.x / 64));
+}
+
+// ------------------------------------------------------------ pack and read
+
+struct PackArgs {
+    uint64_t x, data, scale;
+    int64_t rows, cols, ld, ld8;
+    int patches, across;
+};
+
+template <int DT> __global__ __launch_bounds__(kWaves * 64) void act_pack_kernel(PackArgs a) {
+    const int patch = wave_patch();
+    if (patch >= a.patches) return;
+    const Patch p(a.rows, a.cols, patch, a.across, threadIdx.x % 64);
+    PackedOf<DT, 8> r[kLaneRows];
+#pragma unroll
+    for (int i = 0; i < kLaneRows; i++) r[i] = patch_load<DT>(a.x, a.ld, p, i);
+    encode(p, [&](int i, int j) { return unpack<DT>(r[i], j); }, a.data, a.scale, a.ld8);
+}
+
+template <int DT> __global__ __launch_bounds__(kWaves * 64) void act_read_kernel(PackArgs a) {
+    const int patch = wave_patch();
+    if (patch >= a.patches) return;
+    const Patch p(a.rows, a.cols, patch, a.across, threadIdx.x % 64);
+    Packed<8> w[kLaneRows];
+#pragma unroll
+    for (int i = 0; i < kLaneRows; i++) w[i] = load_codes(p, a.data, a.ld8, i);
+    float unit[8];
+    load_scales(p, a.scale, a.ld8, unit);
+#pragma unroll
+    for (int i = 0; i < kLaneRows; i++) {
+        float x[8];
+        decode(w[i], unit, x);
+        patch_store<DT>(a.x, a.ld, p, i, x);
+    }
+}
+
+// --------------------------------------------------------- gated activation
+
+enum { kSilu = QM_ACT_SILU, kGelu = QM_ACT_GELU };
+
+// 1 / (1 + exp(-z)).  16-bit results: the hardware's exponential and
+// reciprocal, each within an ulp of fp32 (2^-23; a bf16 half step is 2^-9, an
+// f16 one 2^-12).
+template <bool FAST> __device__ __forceinline__ float sigmoid(float z) {
+    if constexpr (FAST) return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * z));
+    else return 1.0f / (1.0f + expf(-z));
+}
+
+constexpr float kGeluA = 1.5957691216057308f;             // 2 sqrt(2 / pi)
+constexpr float kGeluB = 3.0f * 0.044715f;
+
+template <int ACT, bool FAST> __device__ __forceinline__ float act_value(float g) {
+    if constexpr (ACT == kSilu) return g * sigmoid<FAST>(g);
+    else return g * sigmoid<FAST>(kGeluA * (g + 0.044715f * g * g * g));
+}
+// The value and the slope.  s is 0 or 1 in fp32 long before |g| = 32; from
+// there on the slope's second term is left at its limit 0, where g^2 would
+// overflow for the largest g.
+template <int ACT, bool FAST> __device__ __forceinline__ float act_slope(float g, float &value) {
+    if constexpr (ACT == kSilu) {
+        const float s = sigmoid<FAST>(g);
+        value = g * s;
+        return s * (1.0f + g * (1.0f - s));
+    } else {
+        const float b = fminf(fmaxf(g, -32.0f), 32.0f);
+        const float s = sigmoid<FAST>(kGeluA * (b + 0.044715f * b * b * b));
+        value = g * s;
+        return s + b * (s * (1.0f - s)) * (kGeluA * (1.0f + kGeluB * b * b));
+    }
+}
+
+struct GatedArgs {
+    uint64_t gate, up, h;                      // forward in: g, u; backward out: dg, du
+    uint64_t dh;
+    uint64_t gate_data, gate_scale, up_data, up_scale;
+    int64_t rows, cols, ld_gate, ld_up, ld_h, ld_dh, ld_gate8, ld_up8;
+    int patches, across;
+};
+
+template <int DT, int ACT> __global__ __launch_bounds__(kWaves * 64) void gated_forward_kernel(GatedArgs a) {
+    const int patch = wave_patch();
+    if (patch >= a.patches) return;
+    const Patch p(a.rows, a.cols, patch, a.across, threadIdx.x % 64);
+    PackedOf<DT, 8> g[kLaneRows], u[kLaneRows];
+#pragma unroll
+    for (int i = 0; i < kLaneRows; i++) {
+        g[i] = patch_load<DT>(a.gate, a.ld_gate, p, i);
+        u[i] = patch_load<DT>(a.up, a.ld_up, p, i);
+    }
+#pragma unroll
+    for (int i = 0; i < kLaneRows; i++) {
+        float h[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) h[j] = in_fp32(act_value<ACT, DT != QM_F32>(unpack<DT>(g[i], j)) * unpack<DT>(u[i], j));
+        patch_store<DT>(a.h, a.ld_h, p, i, h);
+    }
+    if (a.gate_data) {
+        encode(p, [&](int i, int j) { return unpack<DT>(g[i], j); }, a.gate_data, a.gate_scale, a.ld_gate8);
+        encode(p, [&](int i, int j) { return unpack<DT>(u[i], j); }, a.up_data, a.up_scale, a.ld_up8);
+    }
+}
+
+template <int DT, int ACT> __global__ __launch_bounds__(kWaves * 64) void gated_backward_kernel(GatedArgs a) {
+    const int patch = wave_patch();
+    if (patch >= a.patches) return;
+    const Patch p(a.rows, a.cols, patch, a.across, threadIdx.x % 64);
+    Packed<8> g8[kLaneRows], u8[kLaneRows];
+    PackedOf<DT, 8> d[kLaneRows];
+    float gs[8], us[8];
+#pragma unroll
+    for (int i = 0; i < kLaneRows; i++) {
+        g8[i] = load_codes(p, a.gate_data, a.ld_gate8, i);
+        u8[i] = load_codes(p, a.up_data, a.ld_up8, i);
+        d[i] = patch_load<DT>(a.dh, a.ld_dh, p, i);
+    }
+    load_scales(p, a.gate_scale, a.ld_gate8, gs);
+    load_scales(p, a.up_scale, a.ld_up8, us);
+#pragma unroll
+    for (int i = 0; i < kLaneRows; i++) {
+        float g[8], u[8], dg[8], du[8], h[8];
+        decode(g8[i], gs, g);
+        decode(u8[i], us, u);
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            float v;
+            const float slope = act_slope<ACT, DT != QM_F32>(g[j], v), dh = unpack<DT>(d[i], j);
+            dg[j] = in_fp32(dh * u[j] * slope);
+            du[j] = in_fp32(dh * v);
+            h[j] = in_fp32(v * u[j]);
+        }
+        patch_store<DT>(a.gate, a.ld_gate, p, i, dg);
+        patch_store<DT>(a.up, a.ld_up, p, i, du);
+        if (a.h) patch_store<DT>(a.h, a.ld_h, p, i, h);
+    }
+}
+
+// ------------------------------------------------------------------- host
+
+// Patches of a rows x cols matrix, one a wave; a launch has less than 2^32
+// threads.
+qm_status patch_grid(int64_t rows, int64_t cols, int &patches, int &across) {
+    const int64_t a = (cols + kPatchCols - 1) / kPatchCols, n = a * ((rows + kGroupRows - 1) / kGroupRows);
+    if (n > (int64_t)1 << 25) return fail(QM_E_UNSUPPORTED, "more than 2^25 patches of 32 x 128 elements");
+    patches = (int)n;
+    across = (int)a;
+    return QM_OK;
+}
+unsigned wgs(int patches) { return (unsigned)((patches + kWaves - 1) / kWaves); }
+uint64_t addr(const void *p) { return (uint64_t)(uintptr_t)p; }
+
+// Calls f with the type as a constant.
+template <typename F> void with_dtype(int32_t dtype, F f) {
+    if (dtype == QM_F32) f(std::integral_constant<int, QM_F32>());
+    else if (dtype == QM_BF16) f(std::integral_constant<int, QM_BF16>());
+    else f(std::integral_constant<int, QM_F16>());
+}
+
+}  // namespace
+}  // namespace qm
+
+using namespace qm;
+
+extern "C" qm_status act_pack(const void *x, int32_t dtype, int64_t ld, const qm_act8 *kept, qm_stream_t stream) {
+    clear_error();
+    if (!kept) return fail(QM_E_ARG, "kept is null");
+    const int64_t rows = kept->rows, cols = kept->cols;
+    if (qm_status e = check_kept("kept", kept, rows, cols)) return e;
+    if (qm_status e = check_matrix("x", x, dtype, rows, cols, ld)) return e;
+    if (rows == 0 || cols == 0) return QM_OK;
+    Spans s;
+    s.matrix(x, dtype, rows, cols, ld, false);
+    s.kept(kept, true);
+    if (s.clash()) return fail(QM_E_ARG, "x and kept overlap");
+    PackArgs a{addr(x), addr(kept->data), addr(kept->scale), rows, cols, ld, kept->ld, 0, 0};
+    if (qm_status e = patch_grid(rows, cols, a.patches, a.across)) return e;
+    with_dtype(dtype, [&](auto dt) {
+        act_pack_kernel<decltype(dt)::value><<<wgs(a.patches), kWaves * 64, 0, static_cast<hipStream_t>(stream)>>>(a);
+    });
+    return launch_status("act_pack");
+}
+
+extern "C" qm_status act_read(const qm_act8 *kept, void *out, int32_t dtype, int64_t ld, qm_stream_t stream) {
+    clear_error();
+    if (!kept) return fail(QM_E_ARG, "kept is null");
+    const int64_t rows = kept->rows, cols = kept->cols;
+    if (qm_status e = check_kept("kept", kept, rows, cols)) return e;
+    if (qm_status e = check_matrix("out", out, dtype, rows, cols, ld)) return e;
+    if (rows == 0 || cols == 0) return QM_OK;
+    Spans s;
+    s.matrix(out, dtype, rows, cols, ld, true);
+    s.kept(kept, false);
+    if (s.clash()) return fail(QM_E_ARG, "out and kept overlap");
+    PackArgs a{addr(out), addr(kept->data), addr(kept->scale), rows, cols, ld, kept->ld, 0, 0};
+    if (qm_status e = patch_grid(rows, cols, a.patches, a.across)) return e;
+    with_dtype(dtype, [&](auto dt) {
+        act_read_kernel<decltype(dt)::value><<<wgs(a.patches), kWaves * 64, 0, static_cast<hipStream_t>(stream)>>>(a);
+    });
+    return launch_status("act_read");
+}
+
+extern "C" qm_status gated_act_forward(const void *gate, int64_t ld_gate, const void *up, int64_t ld_up, int32_t dtype,
+                                       int64_t rows, int64_t cols, int32_t act, void *h, int64_t ld_h,
+                                       const qm_act8 *gate8, const qm_act8 *up8, qm_stream_t stream) {
+    clear_error();
+    if (act != kSilu && act != kGelu) return fail(QM_E_ARG, "unknown activation %d", act);
+    if (!gate8 != !up8) return fail(QM_E_ARG, "gate8 and up8: both or neither");
+    if (qm_status e = check_matrix("gate", gate, dtype, rows, cols, ld_gate)) return e;
+    if (qm_status e = check_matrix("up", up, dtype, rows, cols, ld_up)) return e;
+    if (qm_status e = check_matrix("h", h, dtype, rows, cols, ld_h)) return e;
+    if (gate8) {
+        if (qm_status e = check_kept("gate8", gate8, rows, cols)) return e;
+        if (qm_status e = check_kept("up8", up8, rows, cols)) return e;
+    }
+    if (rows == 0 || cols == 0) return QM_OK;
+    Spans s;
+    s.matrix(gate, dtype, rows, cols, ld_gate, false);
+    s.matrix(up, dtype, rows, cols, ld_up, false);
+    s.matrix(h, dtype, rows, cols, ld_h, true);
+    s.kept(gate8, true);
+    s.kept(up8, true);
+    if (s.clash()) return fail(QM_E_ARG, "an output overlaps another buffer");
+    GatedArgs a{};
+    a.gate = addr(gate), a.up = addr(up), a.h = addr(h);
+    a.rows = rows, a.cols = cols, a.ld_gate = ld_gate, a.ld_up = ld_up, a.ld_h = ld_h;
+    if (gate8) {
+        a.gate_data = addr(gate8->data), a.gate_scale = addr(gate8->scale), a.ld_gate8 = gate8->ld;
+        a.up_data = addr(up8->data), a.up_scale = addr(up8->scale), a.ld_up8 = up8->ld;
+    }
+    if (qm_status e = patch_grid(rows, cols, a.patches, a.across)) return e;
+    const hipStream_t q = static_cast<hipStream_t>(stream);
+    with_dtype(dtype, [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        if (act == kSilu) gated_forward_kernel<DT, kSilu><<<wgs(a.patches), kWaves * 64, 0, q>>>(a);
+        else gated_forward_kernel<DT, kGelu><<<wgs(a.patches), kWaves * 64, 0, q>>>(a);
+    });
+    return launch_status("gated_act_forward");
+}
+
+extern "C" qm_status gated_act_backward(const qm_act8 *gate8, const qm_act8 *up8, const void *dh, int64_t ld_dh,
+                                        int32_t dtype, int32_t act, void *dgate, int64_t ld_dgate, void *dup,
+                                        int64_t ld_dup, void *h, int64_t ld_h, qm_stream_t stream) {
+    clear_error();
+    if (act != kSilu && act != kGelu) return fail(QM_E_ARG, "unknown activation %d", act);
+    if (!gate8) return fail(QM_E_ARG, "gate8 is null");
+    const int64_t rows = gate8->rows, cols = gate8->cols;
+    if (qm_status e = check_kept("gate8", gate8, rows, cols)) return e;
+    if (qm_status e = check_kept("up8", up8, rows, cols)) return e;
+    if (qm_status e = check_matrix("dh", dh, dtype, rows, cols, ld_dh)) return e;
+    if (qm_status e = check_matrix("dgate", dgate, dtype, rows, cols, ld_dgate)) return e;
+    if (qm_status e = check_matrix("dup", dup, dtype, rows, cols, ld_dup)) return e;
+    if (h)
+        if (qm_status e = check_matrix("h", h, dtype, rows, cols, ld_h)) return e;
+    if (rows == 0 || cols == 0) return QM_OK;
+    Spans s;
+    s.kept(gate8, false);
+    s.kept(up8, false);
+    s.matrix(dh, dtype, rows, cols, ld_dh, false);
+    s.matrix(dgate, dtype, rows, cols, ld_dgate, true);
+    s.matrix(dup, dtype, rows, cols, ld_dup, true);
+    s.matrix(h, dtype, rows, cols, ld_h, true);
+    if (s.clash()) return fail(QM_E_ARG, "an output overlaps another buffer");
+    GatedArgs a{};
+    a.gate = addr(dgate), a.up = addr(dup), a.h = addr(h), a.dh = addr(dh);
+    a.gate_data = addr(gate8->data), a.gate_scale = addr(gate8->scale), a.ld_gate8 = gate8->ld;
+    a.up_data = addr(up8->data), a.up_scale = addr(up8->scale), a.ld_up8 = up8->ld;
+    a.rows = rows, a.cols = cols, a.ld_gate = ld_dgate, a.ld_up = ld_dup, a.ld_h = ld_h, a.ld_dh = ld_dh;
+    if (qm_status e = patch_grid(rows, cols, a.patches, a.across)) return e;
+    const hipStream_t q = static_cast<hipStream_t>(stream);
+    with_dtype(dtype, [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        if (act == kSilu) gated_backward_kernel<DT, kSilu><<<wgs(a.patches), kWaves * 64, 0, q>>>(a);
+        else gated_backward_kernel<DT, kGelu><<<wgs(a.patches), kWaves * 64, 0, q>>>(a);
+    });
+    return launch_status("gated_act_backward");
+}

@@ -1,0 +1,161 @@
+// Device side of activations kept in 8 bits: where a wave's elements lie, the
+// scale of 32 rows of a column, coding and decoding.
+//
+// value(r, c) = E4M3(data[r * ld + c]) * 2^(scale[(r / 32) * ld + c] - 127)
+//
+// A wave takes a patch of 32 rows x 128 columns: lane l holds columns
+// 8 (l % 16) .. + 7 of rows l / 16, l / 16 + 4, ..., l / 16 + 28, so that each
+// of its eight loads covers four rows of 256 bytes (16-bit elements) and the
+// 32 rows that share a scale meet in one wave: maxima over a lane's rows, then
+// over lanes 16, 32 and 48 away.
+#pragma once
+#include "device_util.h"
+#include "list_device.h"
+
+namespace qm {
+namespace {
+
+constexpr int kGroupRows = 32;               // rows of a column that share a scale
+constexpr int kPatchCols = 128, kLaneCols = 8, kLaneRows = 8;
+constexpr int kScaleLow = 32, kScaleHigh = 246;   // scale bytes: exponents -95 .. 119
+
+// One wave's patch and a lane's place in it.
+struct Patch {
+    int64_t row, col;    // the lane's first row and column
+    bool whole;          // every element of the patch exists (uniform)
+    int rows, cols;      // rows (of 8, four apart) and columns (of 8) the lane has
+
+    __device__ __forceinline__ Patch(int64_t n_rows, int64_t n_cols, int64_t patch, int64_t patches_across, int lane) {
+        const int64_t r0 = patch / patches_across * kGroupRows, c0 = patch % patches_across * kPatchCols;
+        whole = r0 + kGroupRows <= n_rows && c0 + kPatchCols <= n_cols;
+        row = r0 + lane / 16;
+        col = c0 + lane % 16 * kLaneCols;
+        rows = row >= n_rows ? 0 : (int)min((int64_t)kLaneRows, (n_rows - row + 3) / 4);
+        cols = (int)max((int64_t)0, min((int64_t)kLaneCols, n_cols - col));
+    }
+};
+
+// Eight elements of row i of the lane (zeros where there are none).
+template <int DT> __device__ __forceinline__ PackedOf<DT, 8> patch_load(uint64_t base, int64_t ld, const Patch &p, int i) {
+    const uint64_t at = base + (uint64_t)((p.row + 4 * i) * ld + p.col) * kSizeOf<DT>;
+    if (p.whole || (i < p.rows && p.cols == 8)) return load_bytes<8 * kSizeOf<DT>>(at, 0);
+    PackedOf<DT, 8> r = {};
+    if (i < p.rows) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            if (j >= p.cols) continue;
+            if constexpr (DT == QM_F32) r.w[j] = gmem<const uint32_t>(at)[j];
+            else r.w[j / 2] |= (unsigned)gmem<const uint16_t>(at)[j] << (16 * (j % 2));
+        }
+    }
+    return r;
+}
+template <int DT> __device__ __forceinline__ void patch_store(uint64_t base, int64_t ld, const Patch &p, int i, const float *x) {
+    const uint64_t at = base + (uint64_t)((p.row + 4 * i) * ld + p.col) * kSizeOf<DT>;
+    if (p.whole || (i < p.rows && p.cols == 8)) {
+        store_bytes(at, 0, qm::pack<DT, 8>(x));
+        return;
+    }
+    if (i < p.rows) {
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            if (j < p.cols) store_one<DT>(at, j, x[j]);
+    }
+}
+
+// The kept bytes and scales: rows of a multiple of 16 bytes, so a lane's eight
+// are there (what lies past the last column included) wherever its first is.
+__device__ __forceinline__ bool has_bytes(const Patch &p, int i) { return p.whole || (i < p.rows && p.cols > 0); }
+
+typedef float f32x2_v __attribute__((ext_vector_type(2)));
+
+// Bits of the largest magnitude a lane's column j has seen, taken over the
+// four lanes that hold the column: as unsigned numbers magnitudes of floats
+// order as the floats do, infinities and NaN above them.
+__device__ __forceinline__ void column_max(uint32_t *top) {
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        top[j] = max(top[j], (uint32_t)xor_lanes((int)top[j], 16));
+        top[j] = max(top[j], (uint32_t)xor_lanes((int)top[j], 32));
+    }
+}
+
+// Scale byte of a column whose largest magnitude has these bits: the smallest
+// power of two with top <= 448 = 1.75 * 2^8 times it.  Past 1.75 the fraction
+// carries into the exponent.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
+    const int b = (int)((top + 0x1fffffu) >> 23) - 8;
+    return (uint32_t)min(max(b, kScaleLow), kScaleHigh);
+}
+
+// Codes of the lane's eight rows and the scale bytes of its columns.  x(i, j):
+// the element in row i, column j as fp32.
+template <typename X>
+__device__ __forceinline__ void encode(const Patch &p, X x, uint64_t data, uint64_t scale, int64_t ld) {
+    uint32_t top[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        top[j] = 0;
+#pragma unroll
+        for (int i = 0; i < kLaneRows; i++) top[j] = max(top[j], __float_as_uint(x(i, j)) & 0x7fffffffu);
+    }
+    column_max(top);
+    float inv[8];
+    uint32_t sb[8], bad[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        sb[j] = scale_byte(top[j]);
+        inv[j] = __uint_as_float((254u - sb[j]) << 23);
+        // a column that holds an infinity or a NaN: every code a NaN
+        if (top[j] >= 0x7f800000u) bad[j / 4] |= 0x7fu << (8 * (j % 4));
+    }
+#pragma unroll
+    for (int i = 0; i < kLaneRows; i++) {
+        float c[8];
+        // past 448 only where the exponent met its upper limit
+#pragma unroll
+        for (int j = 0; j < 8; j++) c[j] = __builtin_amdgcn_fmed3f(x(i, j) * inv[j], -448.0f, 448.0f);
+        Packed<8> w;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(c[4 * h], c[4 * h + 1], 0, false);
+            w.w[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[4 * h + 2], c[4 * h + 3], lo, true) | bad[h];
+        }
+        if (has_bytes(p, i)) store_bytes(data + (uint64_t)((p.row + 4 * i) * ld + p.col), 0, w);
+    }
+    // lanes 0 .. 15 hold the group's first row
+    if (threadIdx.x % 64 < 16 && has_bytes(p, 0)) {
+        Packed<8> w;
+        w.w[0] = sb[0] | sb[1] << 8 | sb[2] << 16 | sb[3] << 24;
+        w.w[1] = sb[4] | sb[5] << 8 | sb[6] << 16 | sb[7] << 24;
+        store_bytes(scale + (uint64_t)(p.row / kGroupRows * ld + p.col), 0, w);
+    }
+}
+
+// The lane's eight scales as fp32 numbers, and its codes of row i (zeros where
+// there are none).
+__device__ __forceinline__ void load_scales(const Patch &p, uint64_t scale, int64_t ld, float *unit) {
+    Packed<8> w = {};
+    if (has_bytes(p, 0)) w = load_bytes<8>(scale + (uint64_t)(p.row / kGroupRows * ld + p.col), 0);
+#pragma unroll
+    for (int j = 0; j < 8; j++) unit[j] = __uint_as_float((w.w[j / 4] >> (8 * (j % 4)) & 0xffu) << 23);
+}
+__device__ __forceinline__ Packed<8> load_codes(const Patch &p, uint64_t data, int64_t ld, int i) {
+    Packed<8> w = {};
+    if (has_bytes(p, i)) w = load_bytes<8>(data + (uint64_t)((p.row + 4 * i) * ld + p.col), 0);
+    return w;
+}
+__device__ __forceinline__ void decode(const Packed<8> &w, const float *unit, float *x) {
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        const f32x2_v a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.w[h], false);
+        const f32x2_v b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.w[h], true);
+        x[4 * h] = a.x * unit[4 * h];
+        x[4 * h + 1] = a.y * unit[4 * h + 1];
+        x[4 * h + 2] = b.x * unit[4 * h + 2];
+        x[4 * h + 3] = b.y * unit[4 * h + 3];
+    }
+}
+
+}  // namespace
+}  // namespace qm

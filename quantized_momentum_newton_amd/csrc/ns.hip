@@ -52,6 +52,7 @@
 #include "plan_layout.h"
 #include "q8_internal.h"
 #include "qmuon.h"
+#include "reserve_lds.h"
 
 namespace qm {
 namespace {
@@ -1551,7 +1552,6 @@ struct CfgF32Small {
 // Per-device caches below are indexed by device ordinal; they are atomics
 // because entry points may run on several host threads at once (the values
 // written are the same whichever thread writes first).
-constexpr int kMaxDevices = 64;
 
 // Compute units of the current device (cached per device).
 int64_t cu_count() {
@@ -1564,20 +1564,6 @@ int64_t cu_count() {
         cached[dev].store(v, std::memory_order_relaxed);
     }
     return v;
-}
-
-// Raises a kernel's dynamic LDS limit to `bytes` on the current device, once
-// per device (done[] indexed by device; devices beyond the table are set on
-// every call).
-qm_status reserve_lds(const void *kern, size_t bytes, std::atomic<bool> *done) {
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess) return fail(QM_E_HIP, "no current device");
-    const bool cached = dev >= 0 && dev < kMaxDevices;
-    if (cached && done[dev].load(std::memory_order_acquire)) return QM_OK;
-    if (hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != hipSuccess)
-        return fail(QM_E_HIP, "cannot reserve %zu bytes of LDS", bytes);
-    if (cached) done[dev].store(true, std::memory_order_release);
-    return QM_OK;
 }
 
 // Whether a symmetric launch deals its tiles by xcd_tile: only when it has

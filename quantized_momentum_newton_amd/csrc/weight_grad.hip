@@ -1,0 +1,510 @@
+// The weight gradient of a linear layer, from the gradient of its output and
+// its input, the latter in 16 bits or as kept in 8 (act8.hip):
+//
+//   out[n][k] (= or +=) sum over rows t of dy[t][n] x[t][k]
+//
+// Both operands hold the contraction index t along their slow axis, which is
+// what a training step has in hand, while a matrix instruction wants a lane's
+// eight t of one column.  The transposition is done by the LDS reads
+// (ds_read_b64_tr_b16 / _b8), so no transposed copy is made.
+//
+// A kept operand stays in its bytes up to the registers: a fragment is one
+// 8-byte read of eight t of a column, and its group of 32 t shares one scale,
+// so four conversions with that scale make the bf16 fragment (exact: an E4M3
+// number times a power of two).  That is why groups run along the rows.
+//
+// Tiles of 256 x 256 (eight waves of 128 x 64, fp32 accumulators) or 128 x 128
+// (four waves of 64 x 64), 64 rows a step, two LDS buffers; the next step's
+// rows are in registers while this one is multiplied.  Rows and columns past
+// the ends read as zeros (buffer descriptors with their extents), so the loop
+// has no edge cases.  Tiles that do not fill a round of the GPU are split over
+// t; their parts go to the workspace and are added in order by a second
+// kernel.
+#include <algorithm>
+#include <type_traits>
+
+#include "act_host.h"
+#include "list_device.h"
+#include "reserve_lds.h"
+
+namespace qm {
+namespace {
+
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
+typedef __attribute__((ext_vector_type(8))) _Float16 f16x8_t;
+typedef __attribute__((ext_vector_type(4))) short s16x4_t;
+typedef __attribute__((ext_vector_type(2))) int s32x2_t;
+typedef __attribute__((ext_vector_type(16))) float f32x16_t;
+typedef __attribute__((ext_vector_type(4))) unsigned int u32x4_t;
+typedef __attribute__((ext_vector_type(2))) unsigned int u32x2_t;
+typedef __attribute__((ext_vector_type(2))) _Float16 f16x2_t;
+
+constexpr int kStep = 64;         // rows t of a step
+constexpr int kCus = 256;         // workgroups of a round are counted in these
+
+struct ProductArgs {
+    uint64_t dy, x, scale;        // x: 16-bit elements, or bytes with their scales
+    uint64_t out, part;
+    int64_t ld_dy, ld_x, ld_out;
+    int rows, n, k;
+    int tiles_n, tiles_k;
+    int whole, rest, splits, split_steps;   // whole tiles, tiles in parts, parts of each, steps of a part
+    int out_dtype, accumulate;
+};
+
+// Workgroup barrier that completes this wave's LDS accesses and leaves its
+// global loads in flight (the fence of __syncthreads would wait for them).
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// Tile order: bands of four tile rows, walked column by column; consecutive
+// workgroups go to the 8 XCDs in turn, and each XCD's share of a round covers
+// neighbouring tiles, whose operand panels its L2 then holds once.
+__device__ __forceinline__ void tile_at(int p, int tiles_n, int tiles_k, int &bn, int &bk) {
+    const int band = p / (4 * tiles_k), r0 = band * 4, h = min(4, tiles_n - r0), q = p - r0 * tiles_k;
+    bn = r0 + q % h;
+    bk = q / h;
+}
+// Position i of `count` workgroups, XCD i % 8 taking a contiguous share.
+__device__ __forceinline__ int spread(int i, int count) {
+    const int x = i & 7, l = i >> 3;
+    return x * (count >> 3) + min(x, count & 7) + l;
+}
+
+template <int DT> __device__ __forceinline__ void mfma(const u32x4_t &a, const u32x4_t &b, f32x16_t &c) {
+    if constexpr (DT == QM_BF16)
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+    else
+        c = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+}
+
+// Eight kept bytes times their scale, in the product's type.
+template <int DT> __device__ __forceinline__ u32x4_t widen(u32x2_t w, float unit) {
+    u32x4_t r;
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        if constexpr (DT == QM_BF16) {
+            r[2 * h] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[h], unit, false));
+            r[2 * h + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[h], unit, true));
+        } else {
+            r[2 * h] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[h], unit, false));
+            r[2 * h + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[h], unit, true));
+        }
+    }
+    return r;
+}
+
+// One operand's 64 x B panel of a step: PIECES 16-byte pieces a thread, kept
+// in registers between their loads and the LDS writes.
+//
+// LDS row t holds the panel's B elements; its 16-byte pieces lie at
+// p ^ swizzle(t), so that what one transposing read takes together (four rows
+// of 64 bytes, or eight of 32) comes from all banks.
+template <int DT, int B, int NT, bool BYTES, bool FAST> struct Panel {
+    static constexpr int kSize = BYTES ? 1 : 2, kRow = B * kSize, kPer = 16 / kSize;
+    static constexpr int kAcross = kRow / 16, kRowsPass = NT / kAcross, kPieces = kStep / kRowsPass;
+    static_assert(kPieces * kRowsPass == kStep && kRowsPass % 8 == 0, "panel split");
+    static constexpr int kBytes = kStep * kRow;
+
+    u32x4_t r[kPieces];
+    uint64_t base;           // of the panel's first column, row 0
+    int64_t pitch;           // bytes
+    int limit;               // columns from the panel's first to the matrix's last
+    uint32_t voff, at;       // this thread's first piece: byte offset in the panel, in LDS
+    int row, piece;
+
+    static __device__ __forceinline__ int swizzle(int t) {
+        if constexpr (!BYTES) return (t & 3) << 2;
+        else return kRow == 256 ? (t & 7) << 1 : (t >> 1 & 3) << 1;
+    }
+    __device__ __forceinline__ Panel(uint64_t p, int64_t ld, int col, int cols) {
+        base = p + (uint64_t)col * kSize;
+        pitch = ld * kSize;
+        limit = cols - col;
+        row = threadIdx.x / kAcross;
+        piece = threadIdx.x % kAcross;
+        voff = piece * kPer < limit ? (uint32_t)(row * pitch + piece * 16) : 0x80000000u;
+        at = row * kRow + ((piece ^ swizzle(row)) << 4);
+    }
+    // rows t .. t + 63 below `end`; past it, and past the last column: zeros
+    __device__ __forceinline__ void load(int64_t t, int64_t end) {
+        const int64_t rows = max((int64_t)0, min((int64_t)kStep, end - t));
+        const uint64_t p = base + (uint64_t)(t * pitch);
+        if constexpr (FAST) {
+            // extent: the rows' bytes from the panel's first column on (kept rows
+            // are there up to a multiple of 16).  The whole offset is in the
+            // vector operand: the scalar one is not part of the bounds check.
+            const int last = BYTES ? (limit + 15) / 16 * 16 : limit * kSize;
+            const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, rows ? (int)((rows - 1) * pitch) + last : 0, 0x00027000);
+#pragma unroll
+            for (int i = 0; i < kPieces; i++)
+                r[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                       rsrc, (int)(voff + (uint32_t)(i * kRowsPass) * (uint32_t)pitch), 0, 0));
+        } else {
+            static_assert(FAST || !BYTES, "kept bytes are aligned");
+#pragma unroll
+            for (int i = 0; i < kPieces; i++) {
+                const int n = row + i * kRowsPass < rows ? min(8, limit - piece * 8) : 0;
+                const uint64_t q = p + (uint64_t)((row + i * kRowsPass) * pitch) + piece * 16;
+                Packed<16> w = {};
+                if (n == 8) w = load_bytes<16>(q, 0);
+                else {
+#pragma unroll
+                    for (int j = 0; j < 8; j++)
+                        if (j < n) w.w[j / 2] |= (unsigned)gmem<const uint16_t>(q)[j] << (16 * (j % 2));
+                }
+                r[i] = u32x4_t{w.w[0], w.w[1], w.w[2], w.w[3]};
+            }
+        }
+    }
+    __device__ __forceinline__ void store(char *lds) const {
+#pragma unroll
+        for (int i = 0; i < kPieces; i++)
+            *reinterpret_cast<u32x4_t *>(lds + at + i * kRowsPass * kRow) = r[i];
+    }
+
+    // A lane's part of a fragment read: 32 columns from c0 on, rows 16 s + 8
+    // (lane / 32) .. + 7.  16-bit elements: if lane i of 16 points at four
+    // elements, lane i receives element i % 4 of lanes i / 4, + 4, + 8, + 12,
+    // so with lane i at row i / 4, column 4 (i % 4) it gets column i of four
+    // rows.  Bytes: likewise eight rows by 16 columns, lane i at row i / 2,
+    // column 8 (i % 2).
+    static __device__ __forceinline__ int lane_at(int lane, int c0) {
+        const int i = lane & 15;
+        const int t = 8 * (lane >> 5) + (BYTES ? i >> 1 : i >> 2);
+        const int b = (c0 + 16 * (lane >> 4 & 1)) * kSize + (BYTES ? 8 * (i & 1) : 8 * (i & 3));
+        return t * kRow + (((b >> 4) ^ swizzle(t)) << 4) + (b & 15);
+    }
+    static __device__ __forceinline__ s16x4_t read_b16(const char *p) {
+        return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t *)p);
+    }
+    static __device__ __forceinline__ u32x4_t fragment(const char *lds, int lane_off, int s) {
+        const char *p = lds + lane_off + 16 * s * kRow;
+        const u32x2_t lo = __builtin_bit_cast(u32x2_t, read_b16(p)), hi = __builtin_bit_cast(u32x2_t, read_b16(p + 4 * kRow));
+        return u32x4_t{lo.x, lo.y, hi.x, hi.y};
+    }
+    static __device__ __forceinline__ u32x2_t byte_fragment(const char *lds, int lane_off, int s) {
+        const char *p = lds + lane_off + 16 * s * kRow;
+        return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) s32x2_t *)p));
+    }
+};
+
+template <int DT, bool KEPT, bool FAST, int B, int WAVES_N, int WAVES_K>
+__global__ __launch_bounds__(WAVES_N *WAVES_K * 64, B == 256 ? 2 : 2) void weight_grad_kernel(ProductArgs a) {
+    constexpr int NT = WAVES_N * WAVES_K * 64;
+    constexpr int FN = B / WAVES_N / 32, FK = B / WAVES_K / 32, STEPS = kStep / 16;
+    using PanelA = Panel<DT, B, NT, false, FAST>;
+    using PanelB = Panel<DT, B, NT, KEPT, FAST || KEPT>;
+    constexpr int BUF = PanelA::kBytes + PanelB::kBytes;
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int wn = wave / WAVES_K, wk = wave % WAVES_K;
+    int tile, t0 = 0, t1 = a.rows;
+    uint64_t part = 0;
+    if ((int)blockIdx.x < a.whole) {
+        const int w = blockIdx.x;
+        // whole: a multiple of 256
+        tile = (w >> 8) * 256 + spread(w & 255, 256);
+    } else {
+        const int p = spread((int)blockIdx.x - a.whole, a.rest * a.splits);
+        const int split = p / a.rest, i = p % a.rest;
+        tile = a.whole + i;
+        t0 = min(a.rows, split * a.split_steps * kStep);
+        t1 = min(a.rows, t0 + a.split_steps * kStep);
+        if (a.splits > 1) part = a.part + ((uint64_t)i * a.splits + split) * (B * B * 4);
+    }
+    int bn, bk;
+    tile_at(tile, a.tiles_n, a.tiles_k, bn, bk);
+
+    PanelA pa(a.dy, a.ld_dy, bn * B, a.n);
+    PanelB pb(a.x, a.ld_x, bk * B, a.k);
+    int off_a[FN], off_b[FK];
+#pragma unroll
+    for (int i = 0; i < FN; i++) off_a[i] = PanelA::lane_at(lane, wn * FN * 32 + i * 32);
+#pragma unroll
+    for (int j = 0; j < FK; j++) off_b[j] = PanelA::kBytes + PanelB::lane_at(lane, wk * FK * 32 + j * 32);
+
+    // scale bytes of the lane's columns, for the step's two groups of 32 rows
+    uint32_t sc[2][FK] = {}, sc_next[2][FK] = {};
+    auto load_scales = [&](int64_t t) {
+        if constexpr (KEPT) {
+            const int64_t groups = max((int64_t)0, min((int64_t)2, (t1 - t + 31) / 32));
+            const int limit = a.k - bk * B;
+            const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)(a.scale + (uint64_t)(t / 32 * a.ld_x + bk * B)), 0,
+                                                                groups ? (int)((groups - 1) * a.ld_x) + limit : 0, 0x00027000);
+#pragma unroll
+            for (int g = 0; g < 2; g++)
+#pragma unroll
+                for (int j = 0; j < FK; j++) {
+                    const int c = wk * FK * 32 + j * 32 + (lane & 31);
+                    sc_next[g][j] = __builtin_amdgcn_raw_buffer_load_b8(rsrc, c < limit ? c + g * (int)a.ld_x : (int)0x80000000u, 0, 0);
+                }
+        }
+    };
+
+    f32x16_t acc[FN][FK];
+#pragma unroll
+    for (int i = 0; i < FN; i++)
+#pragma unroll
+        for (int j = 0; j < FK; j++)
+#pragma unroll
+            for (int r = 0; r < 16; r++) acc[i][j][r] = 0.0f;
+
+    const int steps = (t1 - t0 + kStep - 1) / kStep;
+    pa.load(t0, t1);
+    pb.load(t0, t1);
+    load_scales(t0);
+    pa.store(lds);
+    pb.store(lds + PanelA::kBytes);
+#pragma unroll
+    for (int g = 0; g < 2; g++)
+#pragma unroll
+        for (int j = 0; j < FK; j++) sc[g][j] = sc_next[g][j];
+    pa.load((int64_t)t0 + kStep, t1);
+    pb.load((int64_t)t0 + kStep, t1);
+    load_scales((int64_t)t0 + kStep);
+    lds_barrier();
+    for (int it = 0; it < steps; it++) {
+        const char *cur = lds + (it & 1) * BUF;
+        char *next = lds + (~it & 1) * BUF;
+        u32x4_t fa[2][FN], fb[2][FK];
+        auto read = [&](int s, u32x4_t *x, u32x4_t *y) {
+#pragma unroll
+            for (int j = 0; j < FK; j++) {
+                if constexpr (KEPT) y[j] = widen<DT>(PanelB::byte_fragment(cur, off_b[j], s), __uint_as_float(sc[s / 2][j] << 23));
+                else y[j] = PanelB::fragment(cur, off_b[j], s);
+            }
+#pragma unroll
+            for (int i = 0; i < FN; i++) x[i] = PanelA::fragment(cur, off_a[i], s);
+        };
+        read(0, fa[0], fb[0]);
+#pragma unroll
+        for (int s = 0; s < STEPS; s++) {
+            if (s + 1 < STEPS) read(s + 1, fa[(s + 1) & 1], fb[(s + 1) & 1]);
+            if (s == 1) {
+                // the buffer's last readers passed the previous barrier
+                pa.store(next);
+                pb.store(next + PanelA::kBytes);
+            }
+#pragma unroll
+            for (int i = 0; i < FN; i++)
+#pragma unroll
+                for (int j = 0; j < FK; j++) mfma<DT>(fa[s & 1][i], fb[s & 1][j], acc[i][j]);
+        }
+#pragma unroll
+        for (int g = 0; g < 2; g++)
+#pragma unroll
+            for (int j = 0; j < FK; j++) sc[g][j] = sc_next[g][j];
+        const int64_t t = t0 + (int64_t)(it + 2) * kStep;
+        pa.load(t, t1);
+        pb.load(t, t1);
+        load_scales(t);
+        lds_barrier();
+    }
+
+    // Element r of a 32 x 32 block: row 8 (r / 4) + 4 (lane / 32) + r % 4,
+    // column lane % 32: each store of a wave is two runs of 32 columns.
+    const int row0 = wn * FN * 32 + 4 * (lane >> 5), col0 = wk * FK * 32 + (lane & 31);
+    if (part) {
+#pragma unroll
+        for (int i = 0; i < FN; i++)
+#pragma unroll
+            for (int j = 0; j < FK; j++)
+#pragma unroll
+                for (int r = 0; r < 16; r++)
+                    gmem<float>(part)[(row0 + i * 32 + 8 * (r / 4) + r % 4) * B + col0 + j * 32] = acc[i][j][r];
+        return;
+    }
+    auto leave = [&](auto dt) {
+        constexpr int OT = decltype(dt)::value;
+#pragma unroll
+        for (int i = 0; i < FN; i++)
+#pragma unroll
+            for (int j = 0; j < FK; j++) {
+                const int64_t c = (int64_t)bk * B + col0 + j * 32, n0 = (int64_t)bn * B + row0 + i * 32;
+                float old[16];
+#pragma unroll
+                for (int r = 0; r < 16; r++) {
+                    const int64_t n = n0 + 8 * (r / 4) + r % 4;
+                    old[r] = 0.0f;
+                    if (a.accumulate && n < a.n && c < a.k) {
+                        if constexpr (OT == QM_F32) old[r] = gmem<float>(a.out)[n * a.ld_out + c];
+                        else {
+                            const uint16_t h = gmem<uint16_t>(a.out)[n * a.ld_out + c];
+                            old[r] = OT == QM_BF16 ? bf16_val(h) : f16_val(h);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < 16; r++) {
+                    const int64_t n = n0 + 8 * (r / 4) + r % 4;
+                    if (n < a.n && c < a.k) store_one<OT>(a.out, n * a.ld_out + c, in_fp32(old[r] + acc[i][j][r]));
+                }
+            }
+    };
+    if (a.out_dtype == QM_F32) leave(std::integral_constant<int, QM_F32>());
+    else if (a.out_dtype == QM_BF16) leave(std::integral_constant<int, QM_BF16>());
+    else leave(std::integral_constant<int, QM_F16>());
+}
+
+// The parts of the split tiles, added in order: a thread takes eight columns
+// of a row.
+template <int OT, int B> __global__ __launch_bounds__(256) void weight_grad_join_kernel(ProductArgs a) {
+    constexpr int kPerTile = B * B / 8 / 256;
+    const int i = blockIdx.x / kPerTile, e = (blockIdx.x % kPerTile) * 256 + threadIdx.x;
+    int bn, bk;
+    tile_at(a.whole + i, a.tiles_n, a.tiles_k, bn, bk);
+    const int row = e / (B / 8), col = e % (B / 8) * 8;
+    const int64_t n = (int64_t)bn * B + row, c = (int64_t)bk * B + col;
+    const int cols = (int)min((int64_t)8, a.k - c);
+    if (n >= a.n || cols <= 0) return;
+    float y[8] = {};
+    const uint64_t at = a.out + (uint64_t)(n * a.ld_out + c) * kSizeOf<OT>;
+    if (a.accumulate) {
+        PackedOf<OT, 8> w = {};
+        if (cols == 8) w = load_bytes<8 * kSizeOf<OT>>(at, 0);
+        else {
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                if (j >= cols) continue;
+                if constexpr (OT == QM_F32) w.w[j] = gmem<const uint32_t>(at)[j];
+                else w.w[j / 2] |= (unsigned)gmem<const uint16_t>(at)[j] << (16 * (j % 2));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j++) y[j] = unpack<OT>(w, j);
+    }
+    float acc[8] = {};
+    const uint64_t p = a.part + (uint64_t)i * a.splits * (B * B * 4) + (uint64_t)(row * B + col) * 4;
+#pragma unroll 4
+    for (int s = 0; s < a.splits; s++) {
+        const Packed<32> w = load_bytes<32>(p + (uint64_t)s * (B * B * 4), 0);
+#pragma unroll
+        for (int j = 0; j < 8; j++) acc[j] += __uint_as_float(w.w[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j++) y[j] = in_fp32(y[j] + acc[j]);
+    if (cols == 8) store_bytes(at, 0, qm::pack<OT, 8>(y));
+    else {
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            if (j < cols) store_one<OT>(at, j, y[j]);
+    }
+}
+
+// -------------------------------------------------------------------- host
+
+// How a product is cut.
+struct Cut {
+    int b;                       // tile side
+    int tiles_n, tiles_k, whole, rest, splits, split_steps;
+    size_t bytes;                // of the parts
+};
+
+Cut cut_for(int b, int64_t rows, int64_t n, int64_t k) {
+    Cut c{};
+    c.b = b;
+    c.tiles_n = (int)((n + b - 1) / b);
+    c.tiles_k = (int)((k + b - 1) / b);
+    const int64_t tiles = (int64_t)c.tiles_n * c.tiles_k, slots = b == 256 ? kCus : 2 * kCus;
+    const int steps = (int)((rows + kStep - 1) / kStep);
+    c.whole = (int)(tiles / slots * slots);
+    c.rest = (int)(tiles - c.whole);
+    c.splits = 1;
+    if (c.rest) c.splits = (int)std::max<int64_t>(1, std::min<int64_t>(slots / c.rest, steps / 4));
+    c.split_steps = (steps + c.splits - 1) / c.splits;
+    if (c.split_steps) c.splits = std::max(1, (steps + c.split_steps - 1) / c.split_steps);
+    c.bytes = c.splits > 1 ? (size_t)c.rest * c.splits * b * b * 4 : 0;
+    return c;
+}
+
+Cut choose_cut(int64_t rows, int64_t n, int64_t k) {
+    const int64_t tiles = ((n + 255) / 256) * ((k + 255) / 256);
+    const int64_t steps = (rows + kStep - 1) / kStep;
+    return cut_for(tiles * steps >= 4 * kCus ? 256 : 128, rows, n, k);
+}
+
+uint64_t addr(const void *p) { return (uint64_t)(uintptr_t)p; }
+
+template <int DT, bool KEPT, bool FAST, int B, int WAVES_N, int WAVES_K>
+qm_status launch_product(const ProductArgs &a, hipStream_t q) {
+    constexpr size_t lds = 2 * (kStep * B * 2 + kStep * B * (KEPT ? 1 : 2));
+    auto kern = weight_grad_kernel<DT, KEPT, FAST, B, WAVES_N, WAVES_K>;
+    static std::atomic<bool> set[kMaxDevices] = {};
+    if (qm_status e = reserve_lds(reinterpret_cast<const void *>(kern), lds, set)) return e;
+    kern<<<(unsigned)(a.whole + a.rest * a.splits), WAVES_N * WAVES_K * 64, lds, q>>>(a);
+    return launch_status("weight_grad");
+}
+template <int DT, bool KEPT, bool FAST> qm_status launch_cut(const ProductArgs &a, int b, hipStream_t q) {
+    if (b == 256) return launch_product<DT, KEPT, FAST, 256, 2, 4>(a, q);
+    return launch_product<DT, KEPT, FAST, 128, 2, 2>(a, q);
+}
+template <int DT> qm_status launch_type(const ProductArgs &a, bool kept, bool fast, int b, hipStream_t q) {
+    if (kept) return fast ? launch_cut<DT, true, true>(a, b, q) : launch_cut<DT, true, false>(a, b, q);
+    return fast ? launch_cut<DT, false, true>(a, b, q) : launch_cut<DT, false, false>(a, b, q);
+}
+template <int OT> void launch_join(const ProductArgs &a, int b, hipStream_t q) {
+    if (b == 256) weight_grad_join_kernel<OT, 256><<<(unsigned)a.rest * 32, 256, 0, q>>>(a);
+    else weight_grad_join_kernel<OT, 128><<<(unsigned)a.rest * 8, 256, 0, q>>>(a);
+}
+
+bool bad_side(int64_t v) { return v < 0 || v >= (int64_t)1 << 30; }
+
+}  // namespace
+}  // namespace qm
+
+using namespace qm;
+
+extern "C" size_t weight_grad_workspace_bytes(int64_t rows, int64_t n, int64_t k) {
+    if (bad_side(rows) || bad_side(n) || bad_side(k)) return 0;
+    return choose_cut(rows, n, k).bytes;
+}
+
+extern "C" qm_status weight_grad(const void *dy, int32_t dtype, int64_t ld_dy, const void *x, int64_t ld_x,
+                                 const qm_act8 *kept, int64_t rows, int64_t n, int64_t k, void *out, int32_t out_dtype,
+                                 int64_t ld_out, int32_t accumulate, void *ws, size_t ws_bytes, qm_stream_t stream) {
+    clear_error();
+    if (dtype != QM_BF16 && dtype != QM_F16) return fail(QM_E_DTYPE, "dy must be bf16 or f16");
+    if (accumulate != 0 && accumulate != 1) return fail(QM_E_ARG, "accumulate must be 0 or 1");
+    if (bad_side(rows) || bad_side(n) || bad_side(k)) return fail(QM_E_SHAPE, "rows, n and k are 0 to 2^30 - 1");
+    if (!x == !kept && rows && k) return fail(QM_E_ARG, "either x or kept");
+    if (qm_status e = check_matrix("dy", dy, dtype, rows, n, ld_dy)) return e;
+    if (kept) {
+        if (qm_status e = check_kept("kept", kept, rows, k)) return e;
+    } else if (qm_status e = check_matrix("x", x, dtype, rows, k, ld_x)) return e;
+    if (qm_status e = check_matrix("out", out, out_dtype, n, k, ld_out)) return e;
+    if (n == 0 || k == 0 || (rows == 0 && accumulate)) return QM_OK;
+    const Cut c = choose_cut(rows, n, k);
+    if ((int64_t)c.tiles_n * c.tiles_k >= (int64_t)1 << 22) return fail(QM_E_UNSUPPORTED, "more than 2^22 tiles");
+    if (c.bytes) {
+        if (!ws || ws_bytes < c.bytes) return fail(QM_E_WORKSPACE, "workspace: need %zu bytes", c.bytes);
+        if (!aligned(ws, 16)) return fail(QM_E_ALIGN, "workspace needs 16-byte alignment");
+    }
+    Spans s;
+    s.matrix(dy, dtype, rows, n, ld_dy, false);
+    if (kept) s.kept(kept, false);
+    else s.matrix(x, dtype, rows, k, ld_x, false);
+    s.matrix(out, out_dtype, n, k, ld_out, true);
+    if (c.bytes) s.bytes(ws, (int64_t)c.bytes, true);
+    if (s.clash()) return fail(QM_E_ARG, "out or workspace overlaps another buffer");
+    ProductArgs a{};
+    a.dy = addr(dy), a.ld_dy = ld_dy;
+    a.x = kept ? addr(kept->data) : addr(x), a.ld_x = kept ? kept->ld : ld_x;
+    a.scale = kept ? addr(kept->scale) : 0;
+    a.out = addr(out), a.ld_out = ld_out, a.part = addr(ws);
+    a.rows = (int)rows, a.n = (int)n, a.k = (int)k;
+    a.tiles_n = c.tiles_n, a.tiles_k = c.tiles_k, a.whole = c.whole, a.rest = c.rest;
+    a.splits = c.splits, a.split_steps = c.split_steps;
+    a.out_dtype = out_dtype, a.accumulate = accumulate;
+    auto wide = [](const void *p, int64_t ld, int64_t cols) { return aligned(p, 16) && ld % 8 == 0 && cols % 8 == 0; };
+    const bool fast = wide(dy, ld_dy, n) && (kept || wide(x, ld_x, k));
+    const hipStream_t q = static_cast<hipStream_t>(stream);
+    if (qm_status e = dtype == QM_BF16 ? launch_type<QM_BF16>(a, kept != nullptr, fast, c.b, q)
+                                       : launch_type<QM_F16>(a, kept != nullptr, fast, c.b, q))
+        return e;
+    if (c.splits == 1) return QM_OK;
+    if (out_dtype == QM_F32) launch_join<QM_F32>(a, c.b, q);
+    else if (out_dtype == QM_BF16) launch_join<QM_BF16>(a, c.b, q);
+    else launch_join<QM_F16>(a, c.b, q);
+    return launch_status("weight_grad");
+}
