@@ -805,6 +805,7 @@ class ActCheckpoint:
         groups = -(-rows // GROUP_ROWS)
         if data is None:
             data = torch.empty((rows, ld), dtype=torch.uint8, device=home)
+            home = data.device      # with its index
         if scale is None:
             scale = torch.empty((groups, ld), dtype=torch.uint8, device=home)
         _require(data, "data", torch.uint8, home, shape=(rows, ld))
