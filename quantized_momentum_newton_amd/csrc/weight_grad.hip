@@ -14,8 +14,8 @@
 // number times a power of two).  That is why groups run along the rows.
 //
 // Tiles of 256 x 256 (eight waves of 128 x 64, fp32 accumulators) or 128 x 128
-// (four waves of 64 x 64), 64 rows a step, two LDS buffers; the next step's
-// rows are in registers while this one is multiplied.  Rows and columns past
+// (four waves of 64 x 64), 64 rows a step, two LDS buffers; the rows of the step
+// after the next are in flight to registers while this one is multiplied.  Rows and columns past
 // the ends read as zeros (buffer descriptors with their extents), so the loop
 // has no edge cases.  Tiles that do not fill a round of the GPU are split over
 // t; their parts go to the workspace and are added in order by a second
@@ -41,6 +41,7 @@ typedef __attribute__((ext_vector_type(2))) _Float16 f16x2_t;
 
 constexpr int kStep = 64;         // rows t of a step
 constexpr int kCus = 256;         // workgroups of a round are counted in these
+template <int B> constexpr int kBufStride = 256 * B;      // both operands of a step in 16 bits
 
 struct ProductArgs {
     uint64_t dy, x, scale;        // x: 16-bit elements, or bytes with their scales
@@ -104,36 +105,46 @@ template <int DT, int B, int NT, bool BYTES, bool FAST> struct Panel {
     static constexpr int kAcross = kRow / 16, kRowsPass = NT / kAcross, kPieces = kStep / kRowsPass;
     static_assert(kPieces * kRowsPass == kStep && kRowsPass % 8 == 0, "panel split");
     static constexpr int kBytes = kStep * kRow;
+    using Raw = std::conditional_t<BYTES, u32x2_t, u32x4_t>;      // a lane's eight t of a column, as they lie in LDS
 
     u32x4_t r[kPieces];
-    uint64_t base;           // of the panel's first column, row 0
+    uint64_t base;           // row 0 of the matrix, from the panel's first column on
     int64_t pitch;           // bytes
-    int limit;               // columns from the panel's first to the matrix's last
+    int col, cols;           // the panel's first column, the matrix's columns
     uint32_t voff, at;       // this thread's first piece: byte offset in the panel, in LDS
-    int row, piece;
+    int row, shift, rows;    // unaligned: elements the piece was moved back by, rows of the last load
 
     static __device__ __forceinline__ int swizzle(int t) {
         if constexpr (!BYTES) return (t & 3) << 2;
         else return kRow == 256 ? (t & 7) << 1 : (t >> 1 & 3) << 1;
     }
-    __device__ __forceinline__ Panel(uint64_t p, int64_t ld, int col, int cols) {
-        base = p + (uint64_t)col * kSize;
+    __device__ __forceinline__ Panel(uint64_t p, int64_t ld, int first, int n) {
+        base = p + (uint64_t)first * kSize;
         pitch = ld * kSize;
-        limit = cols - col;
+        col = first;
+        cols = n;
         row = threadIdx.x / kAcross;
-        piece = threadIdx.x % kAcross;
-        voff = piece * kPer < limit ? (uint32_t)(row * pitch + piece * 16) : 0x80000000u;
+        const int piece = threadIdx.x % kAcross, limit = cols - col;
         at = row * kRow + ((piece ^ swizzle(row)) << 4);
+        if constexpr (FAST) voff = piece * kPer < limit ? (uint32_t)(row * pitch + piece * 16) : 0x80000000u;
+        else {
+            // the last eight columns of the row where the piece would pass its
+            // end; from 8 on nothing of the piece exists
+            shift = min(8, max(0, piece * 8 + 8 - limit));
+            voff = (uint32_t)max(0, min(col + piece * 8, cols - 8)) * kSize;
+            base = p;
+        }
     }
     // rows t .. t + 63 below `end`; past it, and past the last column: zeros
+    // (of an unaligned panel made by store)
     __device__ __forceinline__ void load(int64_t t, int64_t end) {
-        const int64_t rows = max((int64_t)0, min((int64_t)kStep, end - t));
-        const uint64_t p = base + (uint64_t)(t * pitch);
+        rows = (int)max((int64_t)0, min((int64_t)kStep, end - t));
         if constexpr (FAST) {
             // extent: the rows' bytes from the panel's first column on (kept rows
             // are there up to a multiple of 16).  The whole offset is in the
             // vector operand: the scalar one is not part of the bounds check.
-            const int last = BYTES ? (limit + 15) / 16 * 16 : limit * kSize;
+            const uint64_t p = base + (uint64_t)(t * pitch);
+            const int last = BYTES ? (cols - col + 15) / 16 * 16 : (cols - col) * kSize;
             const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, rows ? (int)((rows - 1) * pitch) + last : 0, 0x00027000);
 #pragma unroll
             for (int i = 0; i < kPieces; i++)
@@ -141,22 +152,36 @@ template <int DT, int B, int NT, bool BYTES, bool FAST> struct Panel {
                                                        rsrc, (int)(voff + (uint32_t)(i * kRowsPass) * (uint32_t)pitch), 0, 0));
         } else {
             static_assert(FAST || !BYTES, "kept bytes are aligned");
+            if (rows == 0) return;
+            const uint64_t p = base + (uint64_t)(t * pitch);
 #pragma unroll
             for (int i = 0; i < kPieces; i++) {
-                const int n = row + i * kRowsPass < rows ? min(8, limit - piece * 8) : 0;
-                const uint64_t q = p + (uint64_t)((row + i * kRowsPass) * pitch) + piece * 16;
+                const uint32_t off = (uint32_t)min(row + i * kRowsPass, rows - 1) * (uint32_t)pitch + voff;
                 Packed<16> w = {};
-                if (n == 8) w = load_bytes<16>(q, 0);
+                if (cols >= 8) w = load_bytes<16>(p, off);
                 else {
 #pragma unroll
                     for (int j = 0; j < 8; j++)
-                        if (j < n) w.w[j / 2] |= (unsigned)gmem<const uint16_t>(q)[j] << (16 * (j % 2));
+                        if (j + shift < 8) w.w[j / 2] |= (unsigned)gmem<const uint16_t>(p + off)[j] << (16 * (j % 2));
                 }
                 r[i] = u32x4_t{w.w[0], w.w[1], w.w[2], w.w[3]};
             }
         }
     }
-    __device__ __forceinline__ void store(char *lds) const {
+    __device__ __forceinline__ void store(char *lds) {
+        if constexpr (!FAST) {
+            if (rows < kStep || cols - col < B) {
+#pragma unroll
+                for (int i = 0; i < kPieces; i++) {
+                    u32x4_t &v = r[i];
+                    const int s = cols >= 8 ? shift : shift & 8;
+                    if (s & 1) v = u32x4_t{v.x >> 16 | v.y << 16, v.y >> 16 | v.z << 16, v.z >> 16 | v.w << 16, v.w >> 16};
+                    if (s & 2) v = u32x4_t{v.y, v.z, v.w, 0};
+                    if (s & 4) v = u32x4_t{v.z, v.w, 0, 0};
+                    if ((s & 8) || row + i * kRowsPass >= rows) v = u32x4_t{0, 0, 0, 0};
+                }
+            }
+        }
 #pragma unroll
         for (int i = 0; i < kPieces; i++)
             *reinterpret_cast<u32x4_t *>(lds + at + i * kRowsPass * kRow) = r[i];
@@ -174,17 +199,17 @@ template <int DT, int B, int NT, bool BYTES, bool FAST> struct Panel {
         const int b = (c0 + 16 * (lane >> 4 & 1)) * kSize + (BYTES ? 8 * (i & 1) : 8 * (i & 3));
         return t * kRow + (((b >> 4) ^ swizzle(t)) << 4) + (b & 15);
     }
-    static __device__ __forceinline__ s16x4_t read_b16(const char *p) {
-        return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t *)p);
+    static __device__ __forceinline__ u32x2_t read_b16(const char *p) {
+        return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t *)p));
     }
-    static __device__ __forceinline__ u32x4_t fragment(const char *lds, int lane_off, int s) {
-        const char *p = lds + lane_off + 16 * s * kRow;
-        const u32x2_t lo = __builtin_bit_cast(u32x2_t, read_b16(p)), hi = __builtin_bit_cast(u32x2_t, read_b16(p + 4 * kRow));
-        return u32x4_t{lo.x, lo.y, hi.x, hi.y};
-    }
-    static __device__ __forceinline__ u32x2_t byte_fragment(const char *lds, int lane_off, int s) {
-        const char *p = lds + lane_off + 16 * s * kRow;
-        return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) s32x2_t *)p));
+    static __device__ __forceinline__ void read(const char *p, int s, Raw &f) {
+        p += 16 * s * kRow;
+        if constexpr (BYTES)
+            f = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) s32x2_t *)p));
+        else {
+            const u32x2_t lo = read_b16(p), hi = read_b16(p + 4 * kRow);
+            f = u32x4_t{lo.x, lo.y, hi.x, hi.y};
+        }
     }
 };
 
@@ -194,7 +219,8 @@ __global__ __launch_bounds__(WAVES_N *WAVES_K * 64, B == 256 ? 2 : 2) void weigh
     constexpr int FN = B / WAVES_N / 32, FK = B / WAVES_K / 32, STEPS = kStep / 16;
     using PanelA = Panel<DT, B, NT, false, FAST>;
     using PanelB = Panel<DT, B, NT, KEPT, FAST || KEPT>;
-    constexpr int BUF = PanelA::kBytes + PanelB::kBytes;
+    constexpr int BUF = kBufStride<B>;      // a power of two: the buffers are told apart by one address bit
+    static_assert(PanelA::kBytes + PanelB::kBytes <= BUF, "LDS buffers");
     extern __shared__ __attribute__((aligned(16))) char lds[];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -218,14 +244,15 @@ __global__ __launch_bounds__(WAVES_N *WAVES_K * 64, B == 256 ? 2 : 2) void weigh
 
     PanelA pa(a.dy, a.ld_dy, bn * B, a.n);
     PanelB pb(a.x, a.ld_x, bk * B, a.k);
-    int off_a[FN], off_b[FK];
+    uint32_t off_a[FN], off_b[FK], off_next = 0;      // of the buffer to be read, of the one to be written
 #pragma unroll
     for (int i = 0; i < FN; i++) off_a[i] = PanelA::lane_at(lane, wn * FN * 32 + i * 32);
 #pragma unroll
     for (int j = 0; j < FK; j++) off_b[j] = PanelA::kBytes + PanelB::lane_at(lane, wk * FK * 32 + j * 32);
 
     // scale bytes of the lane's columns, for the step's two groups of 32 rows
-    uint32_t sc[2][FK] = {}, sc_next[2][FK] = {};
+    // of the step multiplied, of the one in LDS, of the one in flight
+    uint32_t sc[2][FK] = {}, sc_put[2][FK] = {}, sc_next[2][FK] = {};
     auto load_scales = [&](int64_t t) {
         if constexpr (KEPT) {
             const int64_t groups = max((int64_t)0, min((int64_t)2, (t1 - t + 31) / 32));
@@ -251,55 +278,83 @@ __global__ __launch_bounds__(WAVES_N *WAVES_K * 64, B == 256 ? 2 : 2) void weigh
             for (int r = 0; r < 16; r++) acc[i][j][r] = 0.0f;
 
     const int steps = (t1 - t0 + kStep - 1) / kStep;
-    pa.load(t0, t1);
-    pb.load(t0, t1);
-    load_scales(t0);
-    pa.store(lds);
-    pb.store(lds + PanelA::kBytes);
+    u32x4_t fa[2][FN];
+    typename PanelB::Raw fb[2][FK];
+    auto read = [&](int s, u32x4_t *x, typename PanelB::Raw *y) {
 #pragma unroll
-    for (int g = 0; g < 2; g++)
+        for (int j = 0; j < FK; j++) PanelB::read(lds + off_b[j], s, y[j]);
 #pragma unroll
-        for (int j = 0; j < FK; j++) sc[g][j] = sc_next[g][j];
-    pa.load((int64_t)t0 + kStep, t1);
-    pb.load((int64_t)t0 + kStep, t1);
-    load_scales((int64_t)t0 + kStep);
-    lds_barrier();
-    for (int it = 0; it < steps; it++) {
-        const char *cur = lds + (it & 1) * BUF;
-        char *next = lds + (~it & 1) * BUF;
-        u32x4_t fa[2][FN], fb[2][FK];
-        auto read = [&](int s, u32x4_t *x, u32x4_t *y) {
+        for (int i = 0; i < FN; i++) PanelA::read(lds + off_a[i], s, x[i]);
+    };
+    auto fetch = [&](int64_t t) {
+        pa.load(t, t1);
+        pb.load(t, t1);
+        load_scales(t);
+    };
+    auto put = [&]() {
+        pa.store(lds + off_next);
+        pb.store(lds + off_next + PanelA::kBytes);
+        off_next ^= BUF;
 #pragma unroll
-            for (int j = 0; j < FK; j++) {
-                if constexpr (KEPT) y[j] = widen<DT>(PanelB::byte_fragment(cur, off_b[j], s), __uint_as_float(sc[s / 2][j] << 23));
-                else y[j] = PanelB::fragment(cur, off_b[j], s);
-            }
+        for (int g = 0; g < 2; g++)
 #pragma unroll
-            for (int i = 0; i < FN; i++) x[i] = PanelA::fragment(cur, off_a[i], s);
-        };
+            for (int j = 0; j < FK; j++) sc_put[g][j] = sc_next[g][j];
+    };
+    auto take_scales = [&]() {
+#pragma unroll
+        for (int g = 0; g < 2; g++)
+#pragma unroll
+            for (int j = 0; j < FK; j++) sc[g][j] = sc_put[g][j];
+    };
+    // A step's four slices of 16 rows.  While a slice is multiplied, the next
+    // one's fragments are read into the other register set; the barrier between
+    // two steps stands before the last slice's products, so that those cover
+    // the first reads of the next step.  The scheduling barriers keep the reads
+    // ahead of the products they overlap: left alone the compiler moves each
+    // read down to its use, which saves registers that nothing else needs.
+    if (steps > 0) {
+        fetch(t0);
+        put();
+        take_scales();
+        fetch((int64_t)t0 + kStep);
+        lds_barrier();
         read(0, fa[0], fb[0]);
+    }
+    for (int it = 0; it < steps; it++) {
 #pragma unroll
         for (int s = 0; s < STEPS; s++) {
-            if (s + 1 < STEPS) read(s + 1, fa[(s + 1) & 1], fb[(s + 1) & 1]);
-            if (s == 1) {
-                // the buffer's last readers passed the previous barrier
-                pa.store(next);
-                pb.store(next + PanelA::kBytes);
+            const int now = s & 1, then = now ^ 1;
+            // the scales of this slice, before they change
+            float unit[FK];
+#pragma unroll
+            for (int j = 0; j < FK; j++) unit[j] = __uint_as_float(sc[s / 2][j] << 23);
+            if (s == STEPS - 1) {
+                lds_barrier();
+                take_scales();
+#pragma unroll
+                for (int i = 0; i < FN; i++) off_a[i] ^= BUF;
+#pragma unroll
+                for (int j = 0; j < FK; j++) off_b[j] ^= BUF;
+            }
+            read((s + 1) % STEPS, fa[then], fb[then]);
+            __builtin_amdgcn_sched_barrier(0);
+            u32x4_t b[FK];
+#pragma unroll
+            for (int j = 0; j < FK; j++) {
+                if constexpr (KEPT) b[j] = widen<DT>(fb[now][j], unit[j]);
+                else b[j] = fb[now][j];
             }
 #pragma unroll
             for (int i = 0; i < FN; i++)
 #pragma unroll
-                for (int j = 0; j < FK; j++) mfma<DT>(fa[s & 1][i], fb[s & 1][j], acc[i][j]);
+                for (int j = 0; j < FK; j++) mfma<DT>(fa[now][i], b[j], acc[i][j]);
+            if (s == 1) {
+                // the buffer's last readers passed the previous barrier
+                put();
+                fetch(t0 + (int64_t)(it + 2) * kStep);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
-#pragma unroll
-        for (int g = 0; g < 2; g++)
-#pragma unroll
-            for (int j = 0; j < FK; j++) sc[g][j] = sc_next[g][j];
-        const int64_t t = t0 + (int64_t)(it + 2) * kStep;
-        pa.load(t, t1);
-        pb.load(t, t1);
-        load_scales(t);
-        lds_barrier();
     }
 
     // Element r of a 32 x 32 block: row 8 (r / 4) + 4 (lane / 32) + r % 4,
@@ -428,7 +483,7 @@ uint64_t addr(const void *p) { return (uint64_t)(uintptr_t)p; }
 
 template <int DT, bool KEPT, bool FAST, int B, int WAVES_N, int WAVES_K>
 qm_status launch_product(const ProductArgs &a, hipStream_t q) {
-    constexpr size_t lds = 2 * (kStep * B * 2 + kStep * B * (KEPT ? 1 : 2));
+    constexpr size_t lds = kBufStride<B> + kStep * B * (KEPT ? 3 : 4);
     auto kern = weight_grad_kernel<DT, KEPT, FAST, B, WAVES_N, WAVES_K>;
     static std::atomic<bool> set[kMaxDevices] = {};
     if (qm_status e = reserve_lds(reinterpret_cast<const void *>(kern), lds, set)) return e;
