@@ -157,14 +157,16 @@ template <int DT, int B, int NT, bool BYTES, bool FAST> struct Panel {
 #pragma unroll
             for (int i = 0; i < kPieces; i++) {
                 const uint32_t off = (uint32_t)min(row + i * kRowsPass, rows - 1) * (uint32_t)pitch + voff;
-                Packed<16> w = {};
-                if (cols >= 8) w = load_bytes<16>(p, off);
+                // panels are read by several workgroups: loads that stay in the
+                // caches (no hint), at any address
+                u32x4_e w = {};
+                if (cols >= 8) w = *reinterpret_cast<const u32x4_e *>(gmem<const char>(p) + off);
                 else {
 #pragma unroll
                     for (int j = 0; j < 8; j++)
-                        if (j + shift < 8) w.w[j / 2] |= (unsigned)gmem<const uint16_t>(p + off)[j] << (16 * (j % 2));
+                        if (j + shift < 8) w[j / 2] |= (unsigned)gmem<const uint16_t>(p + off)[j] << (16 * (j % 2));
                 }
-                r[i] = u32x4_t{w.w[0], w.w[1], w.w[2], w.w[3]};
+                r[i] = w;
             }
         }
     }
@@ -286,41 +288,57 @@ __global__ __launch_bounds__(WAVES_N *WAVES_K * 64, B == 256 ? 2 : 2) void weigh
 #pragma unroll
         for (int i = 0; i < FN; i++) PanelA::read(lds + off_a[i], s, x[i]);
     };
-    auto fetch = [&](int64_t t) {
-        pa.load(t, t1);
-        pb.load(t, t1);
-        load_scales(t);
-    };
-    auto put = [&]() {
-        pa.store(lds + off_next);
-        pb.store(lds + off_next + PanelA::kBytes);
-        off_next ^= BUF;
-#pragma unroll
-        for (int g = 0; g < 2; g++)
-#pragma unroll
-            for (int j = 0; j < FK; j++) sc_put[g][j] = sc_next[g][j];
-    };
     auto take_scales = [&]() {
 #pragma unroll
         for (int g = 0; g < 2; g++)
 #pragma unroll
             for (int j = 0; j < FK; j++) sc[g][j] = sc_put[g][j];
     };
+    auto put_scales = [&]() {
+#pragma unroll
+        for (int g = 0; g < 2; g++)
+#pragma unroll
+            for (int j = 0; j < FK; j++) sc_put[g][j] = sc_next[g][j];
+    };
     // A step's four slices of 16 rows.  While a slice is multiplied, the next
     // one's fragments are read into the other register set; the barrier between
     // two steps stands before the last slice's products, so that those cover
-    // the first reads of the next step.  The scheduling barriers keep the reads
-    // ahead of the products they overlap: left alone the compiler moves each
-    // read down to its use, which saves registers that nothing else needs.
+    // the first reads of the next step.  Left alone the compiler moves each
+    // read down to its use; issued in one run ahead of the products they would
+    // hold up the wave's matrix instructions, and right after a barrier those
+    // of every wave.  So each product is followed by its share of the slice's
+    // LDS and global accesses.
+    constexpr int kProducts = FN * FK, kReads = 2 * FN + (KEPT ? FK : 2 * FK);
+    auto interleave = [&](auto writes, auto loads) {
+        constexpr int W = decltype(writes)::value, V = decltype(loads)::value;
+#pragma unroll
+        for (int m = 0; m < kProducts; m++) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);      // a matrix product
+            if constexpr (kReads > kProducts) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);      // LDS reads
+            else __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            if constexpr (W > 0) __builtin_amdgcn_sched_group_barrier(0x200, (W + kProducts - 1) / kProducts, 0);
+            if constexpr (V > 0) __builtin_amdgcn_sched_group_barrier(0x020, (V + kProducts - 1) / kProducts, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    using std::integral_constant;
     if (steps > 0) {
-        fetch(t0);
-        put();
+        pa.load(t0, t1);
+        pb.load(t0, t1);
+        load_scales(t0);
+        pa.store(lds);
+        pb.store(lds + PanelA::kBytes);
+        off_next = BUF;
+        put_scales();
         take_scales();
-        fetch((int64_t)t0 + kStep);
+        pa.load((int64_t)t0 + kStep, t1);
+        pb.load((int64_t)t0 + kStep, t1);
+        load_scales((int64_t)t0 + kStep);
         lds_barrier();
         read(0, fa[0], fb[0]);
     }
     for (int it = 0; it < steps; it++) {
+        const int64_t ahead = t0 + (int64_t)(it + 2) * kStep;
 #pragma unroll
         for (int s = 0; s < STEPS; s++) {
             const int now = s & 1, then = now ^ 1;
@@ -335,9 +353,21 @@ __global__ __launch_bounds__(WAVES_N *WAVES_K * 64, B == 256 ? 2 : 2) void weigh
                 for (int i = 0; i < FN; i++) off_a[i] ^= BUF;
 #pragma unroll
                 for (int j = 0; j < FK; j++) off_b[j] ^= BUF;
+                __builtin_amdgcn_sched_barrier(0);
             }
             read((s + 1) % STEPS, fa[then], fb[then]);
-            __builtin_amdgcn_sched_barrier(0);
+            // the other buffer's last readers passed the previous barrier
+            if (s == 1) {
+                pa.store(lds + off_next);
+                pa.load(ahead, t1);
+            }
+            if (s == 2) {
+                pb.store(lds + off_next + PanelA::kBytes);
+                off_next ^= BUF;
+                pb.load(ahead, t1);
+                put_scales();
+                load_scales(ahead);
+            }
             u32x4_t b[FK];
 #pragma unroll
             for (int j = 0; j < FK; j++) {
@@ -348,12 +378,10 @@ __global__ __launch_bounds__(WAVES_N *WAVES_K * 64, B == 256 ? 2 : 2) void weigh
             for (int i = 0; i < FN; i++)
 #pragma unroll
                 for (int j = 0; j < FK; j++) mfma<DT>(fa[now][i], b[j], acc[i][j]);
-            if (s == 1) {
-                // the buffer's last readers passed the previous barrier
-                put();
-                fetch(t0 + (int64_t)(it + 2) * kStep);
-            }
-            __builtin_amdgcn_sched_barrier(0);
+            if (s == 1) interleave(integral_constant<int, PanelA::kPieces>(), integral_constant<int, PanelA::kPieces>());
+            else if (s == 2)
+                interleave(integral_constant<int, PanelB::kPieces>(), integral_constant<int, PanelB::kPieces + (KEPT ? 2 * FK : 0)>());
+            else interleave(integral_constant<int, 0>(), integral_constant<int, 0>());
         }
     }
 
