@@ -665,7 +665,7 @@ QM_API qm_status act_read(const qm_act8 *kept, void *out, int32_t dtype,
  * dy: rows x n, bf16 or f16.  x: rows x k of the same type, or null with
  * `kept` in its place (its values, in f16 rounded to f16).  Products exact,
  * sums in fp32 in an order that the sizes determine; the result is rounded
- * once.  out: any dtype.  rows = 0: zeros, or nothing to add.
+ * once.  out: any dtype, ld_out < 2^21.  rows = 0: zeros, or nothing to add.
  *   ws: >= weight_grad_workspace_bytes(rows, n, k) bytes (0: none needed),
  *   16-byte aligned.
  * Errors: QM_E_ARG, QM_E_ALIGN, QM_E_DTYPE, QM_E_SHAPE, QM_E_WORKSPACE,

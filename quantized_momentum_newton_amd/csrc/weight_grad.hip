@@ -14,7 +14,7 @@
 // number times a power of two).  That is why groups run along the rows.
 //
 // Tiles of 256 x 256 (eight waves of 128 x 64, fp32 accumulators) or 128 x 128
-// (four waves of 64 x 64), 64 rows a step, two LDS buffers; the rows of the step
+// (four waves of 64 x 64), 64 rows a step, two LDS buffers; the rows of the steps
 // after the next are in flight to registers while this one is multiplied.  Rows and columns past
 // the ends read as zeros (buffer descriptors with their extents), so the loop
 // has no edge cases.  Tiles that do not fill a round of the GPU are split over
@@ -51,6 +51,7 @@ struct ProductArgs {
     int tiles_n, tiles_k;
     int whole, rest, splits, split_steps;   // whole tiles, tiles in parts, parts of each, steps of a part
     int out_dtype, accumulate;
+    int early_n, early_k;         // the last tiles of n, of k end with the matrix (kAny)
 };
 
 // Workgroup barrier that completes this wave's LDS accesses and leaves its
@@ -69,6 +70,14 @@ __device__ __forceinline__ void tile_at(int p, int tiles_n, int tiles_k, int &bn
 __device__ __forceinline__ int spread(int i, int count) {
     const int x = i & 7, l = i >> 3;
     return x * (count >> 3) + min(x, count & 7) + l;
+}
+
+// Descriptor of `bytes` bytes at p, both uniform over the wave (said to the
+// compiler, which otherwise loops over the values that lanes might have).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(uint64_t p, int bytes) {
+    const uint64_t u = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(p >> 32)) << 32 |
+                       (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)p);
+    return __builtin_amdgcn_make_buffer_rsrc((void *)u, 0, __builtin_amdgcn_readfirstlane(bytes), 0x00027000);
 }
 
 template <int DT> __device__ __forceinline__ void mfma(const u32x4_t &a, const u32x4_t &b, f32x16_t &c) {
@@ -94,25 +103,32 @@ template <int DT> __device__ __forceinline__ u32x4_t widen(u32x2_t w, float unit
     return r;
 }
 
+// How a panel is read.  kAligned: 16-byte pieces at 16-byte addresses, rows of
+// a multiple of 8 elements (or kept bytes).  kAny: at any address, from a
+// matrix of at least B columns: its last panel ends with the matrix and
+// overlaps the one before, so no piece is cut.  kNarrow: any address and
+// width; pieces that pass a row's end are moved back and shifted.
+enum { kAligned = 0, kAny = 1, kNarrow = 2 };
+
 // One operand's 64 x B panel of a step: PIECES 16-byte pieces a thread, kept
 // in registers between their loads and the LDS writes.
 //
 // LDS row t holds the panel's B elements; its 16-byte pieces lie at
 // p ^ swizzle(t), so that what one transposing read takes together (four rows
 // of 64 bytes, or eight of 32) comes from all banks.
-template <int DT, int B, int NT, bool BYTES, bool FAST> struct Panel {
+template <int DT, int B, int NT, bool BYTES, int MODE, int DEPTH> struct Panel {
     static constexpr int kSize = BYTES ? 1 : 2, kRow = B * kSize, kPer = 16 / kSize;
     static constexpr int kAcross = kRow / 16, kRowsPass = NT / kAcross, kPieces = kStep / kRowsPass;
     static_assert(kPieces * kRowsPass == kStep && kRowsPass % 8 == 0, "panel split");
     static constexpr int kBytes = kStep * kRow;
     using Raw = std::conditional_t<BYTES, u32x2_t, u32x4_t>;      // a lane's eight t of a column, as they lie in LDS
 
-    u32x4_t r[kPieces];
+    u32x4_t r[DEPTH][kPieces];      // DEPTH steps in flight
     uint64_t base;           // row 0 of the matrix, from the panel's first column on
     int64_t pitch;           // bytes
     int col, cols;           // the panel's first column, the matrix's columns
     uint32_t voff, at;       // this thread's first piece: byte offset in the panel, in LDS
-    int row, shift, rows;    // unaligned: elements the piece was moved back by, rows of the last load
+    int row, shift, rows[DEPTH];      // unaligned: elements the piece was moved back by; rows of the loads
 
     static __device__ __forceinline__ int swizzle(int t) {
         if constexpr (!BYTES) return (t & 3) << 2;
@@ -126,7 +142,8 @@ template <int DT, int B, int NT, bool BYTES, bool FAST> struct Panel {
         row = threadIdx.x / kAcross;
         const int piece = threadIdx.x % kAcross, limit = cols - col;
         at = row * kRow + ((piece ^ swizzle(row)) << 4);
-        if constexpr (FAST) voff = piece * kPer < limit ? (uint32_t)(row * pitch + piece * 16) : 0x80000000u;
+        if constexpr (MODE == kAligned) voff = piece * kPer < limit ? (uint32_t)(row * pitch + piece * 16) : 0x80000000u;
+        else if constexpr (MODE == kAny) voff = piece * 16;
         else {
             // the last eight columns of the row where the piece would pass its
             // end; from 8 on nothing of the piece exists
@@ -137,28 +154,36 @@ template <int DT, int B, int NT, bool BYTES, bool FAST> struct Panel {
     }
     // rows t .. t + 63 below `end`; past it, and past the last column: zeros
     // (of an unaligned panel made by store)
-    __device__ __forceinline__ void load(int64_t t, int64_t end) {
-        rows = (int)max((int64_t)0, min((int64_t)kStep, end - t));
-        if constexpr (FAST) {
+    __device__ __forceinline__ void load(int d, int t, int end) {
+        const int have = rows[d] = max(0, min(kStep, end - t));
+        if constexpr (MODE == kAligned) {
             // extent: the rows' bytes from the panel's first column on (kept rows
             // are there up to a multiple of 16).  The whole offset is in the
             // vector operand: the scalar one is not part of the bounds check.
-            const uint64_t p = base + (uint64_t)(t * pitch);
+            const uint64_t p = base + (uint64_t)((int64_t)t * pitch);
             const int last = BYTES ? (cols - col + 15) / 16 * 16 : (cols - col) * kSize;
-            const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, rows ? (int)((rows - 1) * pitch) + last : 0, 0x00027000);
+            // none without rows: last <= pitch (no branch, which would cut the
+            // loop that this stands in)
+            const auto rsrc = buffer(p, max(0, (have - 1) * (int)pitch + last));
 #pragma unroll
             for (int i = 0; i < kPieces; i++)
-                r[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                r[d][i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
                                                        rsrc, (int)(voff + (uint32_t)(i * kRowsPass) * (uint32_t)pitch), 0, 0));
+        } else if constexpr (MODE == kAny) {
+            // rows past the end: the last one's, cleared by store.  Panels are
+            // read by several workgroups: loads that stay in the caches.
+            const uint64_t p = base + (uint64_t)((int64_t)min(t, end - 1) * pitch);
+#pragma unroll
+            for (int i = 0; i < kPieces; i++)
+                r[d][i] = *reinterpret_cast<const u32x4_e *>(gmem<const char>(p) + voff +
+                                                             (uint32_t)max(0, min(row + i * kRowsPass, have - 1)) * (uint32_t)pitch);
         } else {
-            static_assert(FAST || !BYTES, "kept bytes are aligned");
-            if (rows == 0) return;
-            const uint64_t p = base + (uint64_t)(t * pitch);
+            static_assert(!BYTES, "kept bytes are aligned");
+            if (have == 0) return;
+            const uint64_t p = base + (uint64_t)((int64_t)t * pitch);
 #pragma unroll
             for (int i = 0; i < kPieces; i++) {
-                const uint32_t off = (uint32_t)min(row + i * kRowsPass, rows - 1) * (uint32_t)pitch + voff;
-                // panels are read by several workgroups: loads that stay in the
-                // caches (no hint), at any address
+                const uint32_t off = (uint32_t)min(row + i * kRowsPass, have - 1) * (uint32_t)pitch + voff;
                 u32x4_e w = {};
                 if (cols >= 8) w = *reinterpret_cast<const u32x4_e *>(gmem<const char>(p) + off);
                 else {
@@ -166,27 +191,33 @@ template <int DT, int B, int NT, bool BYTES, bool FAST> struct Panel {
                     for (int j = 0; j < 8; j++)
                         if (j + shift < 8) w[j / 2] |= (unsigned)gmem<const uint16_t>(p + off)[j] << (16 * (j % 2));
                 }
-                r[i] = w;
+                r[d][i] = w;
             }
         }
     }
-    __device__ __forceinline__ void store(char *lds) {
-        if constexpr (!FAST) {
-            if (rows < kStep || cols - col < B) {
+    __device__ __forceinline__ void store(int d, char *lds) {
+        if constexpr (MODE == kAny) {
+#pragma unroll
+            for (int i = 0; i < kPieces; i++)
+#pragma unroll
+                for (int j = 0; j < 4; j++) r[d][i][j] = row + i * kRowsPass < rows[d] ? r[d][i][j] : 0;
+        }
+        if constexpr (MODE == kNarrow) {
+            if (rows[d] < kStep || cols - col < B) {
 #pragma unroll
                 for (int i = 0; i < kPieces; i++) {
-                    u32x4_t &v = r[i];
+                    u32x4_t &v = r[d][i];
                     const int s = cols >= 8 ? shift : shift & 8;
                     if (s & 1) v = u32x4_t{v.x >> 16 | v.y << 16, v.y >> 16 | v.z << 16, v.z >> 16 | v.w << 16, v.w >> 16};
                     if (s & 2) v = u32x4_t{v.y, v.z, v.w, 0};
                     if (s & 4) v = u32x4_t{v.z, v.w, 0, 0};
-                    if ((s & 8) || row + i * kRowsPass >= rows) v = u32x4_t{0, 0, 0, 0};
+                    if ((s & 8) || row + i * kRowsPass >= rows[d]) v = u32x4_t{0, 0, 0, 0};
                 }
             }
         }
 #pragma unroll
         for (int i = 0; i < kPieces; i++)
-            *reinterpret_cast<u32x4_t *>(lds + at + i * kRowsPass * kRow) = r[i];
+            *reinterpret_cast<u32x4_t *>(lds + at + i * kRowsPass * kRow) = r[d][i];
     }
 
     // A lane's part of a fragment read: 32 columns from c0 on, rows 16 s + 8
@@ -215,26 +246,32 @@ template <int DT, int B, int NT, bool BYTES, bool FAST> struct Panel {
     }
 };
 
-template <int DT, bool KEPT, bool FAST, int B, int WAVES_N, int WAVES_K>
+template <int DT, bool KEPT, int MODE, int B, int WAVES_N, int WAVES_K>
 __global__ __launch_bounds__(WAVES_N *WAVES_K * 64, B == 256 ? 2 : 2) void weight_grad_kernel(ProductArgs a) {
     constexpr int NT = WAVES_N * WAVES_K * 64;
     constexpr int FN = B / WAVES_N / 32, FK = B / WAVES_K / 32, STEPS = kStep / 16;
-    using PanelA = Panel<DT, B, NT, false, FAST>;
-    using PanelB = Panel<DT, B, NT, KEPT, FAST || KEPT>;
+    // Steps in flight to registers.  A 128 tile's step takes less than a load,
+    // and leaves registers for a second.
+    constexpr int DEPTH = B == 256 ? 1 : 2;
+    using PanelA = Panel<DT, B, NT, false, MODE, DEPTH>;
+    using PanelB = Panel<DT, B, NT, KEPT, KEPT ? kAligned : MODE, DEPTH>;
     constexpr int BUF = kBufStride<B>;      // a power of two: the buffers are told apart by one address bit
-    static_assert(PanelA::kBytes + PanelB::kBytes <= BUF, "LDS buffers");
+    static_assert(PanelA::kBytes + PanelB::kBytes + (KEPT ? 2 * B : 0) <= BUF, "LDS buffers");
     extern __shared__ __attribute__((aligned(16))) char lds[];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int wn = wave / WAVES_K, wk = wave % WAVES_K;
     int tile, t0 = 0, t1 = a.rows;
     uint64_t part = 0;
-    if ((int)blockIdx.x < a.whole) {
-        const int w = blockIdx.x;
+    // Half of the parts come first, so that the whole tiles behind them end at
+    // different times and one half's results leave while the other multiplies.
+    const int parts = a.rest * a.splits, early = a.whole ? parts / 2 & ~7 : parts;
+    const int w = (int)blockIdx.x - early;
+    if (w >= 0 && w < a.whole) {
         // whole: a multiple of 256
         tile = (w >> 8) * 256 + spread(w & 255, 256);
     } else {
-        const int p = spread((int)blockIdx.x - a.whole, a.rest * a.splits);
+        const int p = spread(w < 0 ? (int)blockIdx.x : (int)blockIdx.x - a.whole, parts);
         const int split = p / a.rest, i = p % a.rest;
         tile = a.whole + i;
         t0 = min(a.rows, split * a.split_steps * kStep);
@@ -244,31 +281,33 @@ __global__ __launch_bounds__(WAVES_N *WAVES_K * 64, B == 256 ? 2 : 2) void weigh
     int bn, bk;
     tile_at(tile, a.tiles_n, a.tiles_k, bn, bk);
 
-    PanelA pa(a.dy, a.ld_dy, bn * B, a.n);
-    PanelB pb(a.x, a.ld_x, bk * B, a.k);
+    // the tile's first row and column: panels that end with the matrix start early
+    const int row_at = MODE == kAny ? min(bn * B, a.n - B) : bn * B;
+    const int col_at = MODE == kAny && !KEPT ? min(bk * B, a.k - B) : bk * B;
+    PanelA pa(a.dy, a.ld_dy, row_at, a.n);
+    PanelB pb(a.x, a.ld_x, col_at, a.k);
     uint32_t off_a[FN], off_b[FK], off_next = 0;      // of the buffer to be read, of the one to be written
+    uint32_t off_s = PanelA::kBytes + PanelB::kBytes + wk * FK * 32 + (lane & 31);
 #pragma unroll
     for (int i = 0; i < FN; i++) off_a[i] = PanelA::lane_at(lane, wn * FN * 32 + i * 32);
 #pragma unroll
     for (int j = 0; j < FK; j++) off_b[j] = PanelA::kBytes + PanelB::lane_at(lane, wk * FK * 32 + j * 32);
 
-    // scale bytes of the lane's columns, for the step's two groups of 32 rows
-    // of the step multiplied, of the one in LDS, of the one in flight
-    uint32_t sc[2][FK] = {}, sc_put[2][FK] = {}, sc_next[2][FK] = {};
-    auto load_scales = [&](int64_t t) {
+    // Scales of a kept step: two groups of 32 rows, B bytes each, one byte a
+    // thread, behind the panels in LDS.
+    constexpr int SCALES = PanelA::kBytes + PanelB::kBytes;
+    static_assert(2 * B == NT, "a scale byte for each thread");
+    uint32_t sc[DEPTH];
+    const int sc_group = threadIdx.x / B, sc_col = threadIdx.x % B;
+    auto load_scales = [&](int d, int t) {
         if constexpr (KEPT) {
-            const int64_t groups = max((int64_t)0, min((int64_t)2, (t1 - t + 31) / 32));
-            const int limit = a.k - bk * B;
-            const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)(a.scale + (uint64_t)(t / 32 * a.ld_x + bk * B)), 0,
-                                                                groups ? (int)((groups - 1) * a.ld_x) + limit : 0, 0x00027000);
-#pragma unroll
-            for (int g = 0; g < 2; g++)
-#pragma unroll
-                for (int j = 0; j < FK; j++) {
-                    const int c = wk * FK * 32 + j * 32 + (lane & 31);
-                    sc_next[g][j] = __builtin_amdgcn_raw_buffer_load_b8(rsrc, c < limit ? c + g * (int)a.ld_x : (int)0x80000000u, 0, 0);
-                }
+            const int groups = max(0, min(2, (t1 - t + 31) >> 5)), limit = a.k - bk * B;
+            const auto rsrc = buffer(a.scale + (uint64_t)((t >> 5) * a.ld_x + bk * B), max(0, (groups - 1) * (int)a.ld_x + limit));
+            sc[d] = __builtin_amdgcn_raw_buffer_load_b8(rsrc, sc_col < limit ? sc_col + sc_group * (int)a.ld_x : (int)0x80000000u, 0, 0);
         }
+    };
+    auto store_scales = [&](int d, char *buf) {
+        if constexpr (KEPT) buf[SCALES + threadIdx.x] = (char)sc[d];
     };
 
     f32x16_t acc[FN][FK];
@@ -282,23 +321,17 @@ __global__ __launch_bounds__(WAVES_N *WAVES_K * 64, B == 256 ? 2 : 2) void weigh
     const int steps = (t1 - t0 + kStep - 1) / kStep;
     u32x4_t fa[2][FN];
     typename PanelB::Raw fb[2][FK];
+    uint32_t unit[2][FK];      // scale bytes of the lane's columns, of both groups
     auto read = [&](int s, u32x4_t *x, typename PanelB::Raw *y) {
+        if constexpr (KEPT) {
+            if (s % 2 == 0)
+#pragma unroll
+                for (int j = 0; j < FK; j++) unit[s / 2][j] = (uint8_t)lds[off_s + s / 2 * B + j * 32];
+        }
 #pragma unroll
         for (int j = 0; j < FK; j++) PanelB::read(lds + off_b[j], s, y[j]);
 #pragma unroll
         for (int i = 0; i < FN; i++) PanelA::read(lds + off_a[i], s, x[i]);
-    };
-    auto take_scales = [&]() {
-#pragma unroll
-        for (int g = 0; g < 2; g++)
-#pragma unroll
-            for (int j = 0; j < FK; j++) sc[g][j] = sc_put[g][j];
-    };
-    auto put_scales = [&]() {
-#pragma unroll
-        for (int g = 0; g < 2; g++)
-#pragma unroll
-            for (int j = 0; j < FK; j++) sc_put[g][j] = sc_next[g][j];
     };
     // A step's four slices of 16 rows.  While a slice is multiplied, the next
     // one's fragments are read into the other register set; the barrier between
@@ -308,7 +341,7 @@ __global__ __launch_bounds__(WAVES_N *WAVES_K * 64, B == 256 ? 2 : 2) void weigh
     // hold up the wave's matrix instructions, and right after a barrier those
     // of every wave.  So each product is followed by its share of the slice's
     // LDS and global accesses.
-    constexpr int kProducts = FN * FK, kReads = 2 * FN + (KEPT ? FK : 2 * FK);
+    constexpr int kProducts = FN * FK, kReads = 2 * FN + 2 * FK;
     auto interleave = [&](auto writes, auto loads) {
         constexpr int W = decltype(writes)::value, V = decltype(loads)::value;
 #pragma unroll
@@ -323,32 +356,31 @@ __global__ __launch_bounds__(WAVES_N *WAVES_K * 64, B == 256 ? 2 : 2) void weigh
     };
     using std::integral_constant;
     if (steps > 0) {
-        pa.load(t0, t1);
-        pb.load(t0, t1);
-        load_scales(t0);
-        pa.store(lds);
-        pb.store(lds + PanelA::kBytes);
+        pa.load(0, t0, t1);
+        pb.load(0, t0, t1);
+        load_scales(0, t0);
+        pa.store(0, lds);
+        pb.store(0, lds + PanelA::kBytes);
+        store_scales(0, lds);
         off_next = BUF;
-        put_scales();
-        take_scales();
-        pa.load((int64_t)t0 + kStep, t1);
-        pb.load((int64_t)t0 + kStep, t1);
-        load_scales((int64_t)t0 + kStep);
+#pragma unroll
+        for (int d = 0; d < DEPTH; d++) {
+            pa.load(d, t0 + (d + 1) * kStep, t1);
+            pb.load(d, t0 + (d + 1) * kStep, t1);
+            load_scales(d, t0 + (d + 1) * kStep);
+        }
         lds_barrier();
         read(0, fa[0], fb[0]);
     }
-    for (int it = 0; it < steps; it++) {
-        const int64_t ahead = t0 + (int64_t)(it + 2) * kStep;
+    // step `it`, whose successor is in the registers d
+    auto step = [&](int it, int d) {
+        const int ahead = t0 + (it + 1 + DEPTH) * kStep;
 #pragma unroll
         for (int s = 0; s < STEPS; s++) {
             const int now = s & 1, then = now ^ 1;
-            // the scales of this slice, before they change
-            float unit[FK];
-#pragma unroll
-            for (int j = 0; j < FK; j++) unit[j] = __uint_as_float(sc[s / 2][j] << 23);
             if (s == STEPS - 1) {
                 lds_barrier();
-                take_scales();
+                off_s ^= BUF;
 #pragma unroll
                 for (int i = 0; i < FN; i++) off_a[i] ^= BUF;
 #pragma unroll
@@ -358,20 +390,20 @@ __global__ __launch_bounds__(WAVES_N *WAVES_K * 64, B == 256 ? 2 : 2) void weigh
             read((s + 1) % STEPS, fa[then], fb[then]);
             // the other buffer's last readers passed the previous barrier
             if (s == 1) {
-                pa.store(lds + off_next);
-                pa.load(ahead, t1);
+                pa.store(d, lds + off_next);
+                pa.load(d, ahead, t1);
             }
             if (s == 2) {
-                pb.store(lds + off_next + PanelA::kBytes);
+                pb.store(d, lds + off_next + PanelA::kBytes);
+                store_scales(d, lds + off_next);
                 off_next ^= BUF;
-                pb.load(ahead, t1);
-                put_scales();
-                load_scales(ahead);
+                pb.load(d, ahead, t1);
+                load_scales(d, ahead);
             }
             u32x4_t b[FK];
 #pragma unroll
             for (int j = 0; j < FK; j++) {
-                if constexpr (KEPT) b[j] = widen<DT>(fb[now][j], unit[j]);
+                if constexpr (KEPT) b[j] = widen<DT>(fb[now][j], __uint_as_float(unit[s / 2][j] << 23));
                 else b[j] = fb[now][j];
             }
 #pragma unroll
@@ -380,8 +412,14 @@ __global__ __launch_bounds__(WAVES_N *WAVES_K * 64, B == 256 ? 2 : 2) void weigh
                 for (int j = 0; j < FK; j++) mfma<DT>(fa[now][i], b[j], acc[i][j]);
             if (s == 1) interleave(integral_constant<int, PanelA::kPieces>(), integral_constant<int, PanelA::kPieces>());
             else if (s == 2)
-                interleave(integral_constant<int, PanelB::kPieces>(), integral_constant<int, PanelB::kPieces + (KEPT ? 2 * FK : 0)>());
+                interleave(integral_constant<int, PanelB::kPieces + KEPT>(), integral_constant<int, PanelB::kPieces + KEPT>());
             else interleave(integral_constant<int, 0>(), integral_constant<int, 0>());
+        }
+    };
+    for (int it = 0; it < steps; it += DEPTH) {
+        step(it, 0);
+        if constexpr (DEPTH == 2) {
+            if (it + 1 < steps) step(it + 1, 1);
         }
     }
 
@@ -398,30 +436,42 @@ __global__ __launch_bounds__(WAVES_N *WAVES_K * 64, B == 256 ? 2 : 2) void weigh
                     gmem<float>(part)[(row0 + i * 32 + 8 * (r / 4) + r % 4) * B + col0 + j * 32] = acc[i][j][r];
         return;
     }
+    // What does not exist, or is a neighbouring tile's where this one starts
+    // early, lies outside the descriptor (rows before its first: negative, so
+    // large) or is sent there.
     auto leave = [&](auto dt) {
-        constexpr int OT = decltype(dt)::value;
+        constexpr int OT = decltype(dt)::value, S = kSizeOf<OT>;
+        const int pitch = (int)a.ld_out * S;
+        const auto rsrc = buffer(a.out + (uint64_t)((int64_t)bn * B * a.ld_out + bk * B) * S,
+                                 (min(B, a.n - bn * B) - 1) * pitch + (a.k - bk * B) * S);
 #pragma unroll
         for (int i = 0; i < FN; i++)
 #pragma unroll
             for (int j = 0; j < FK; j++) {
-                const int64_t c = (int64_t)bk * B + col0 + j * 32, n0 = (int64_t)bn * B + row0 + i * 32;
+                const int c = col_at - bk * B + col0 + j * 32, n0 = row_at - bn * B + row0 + i * 32;
+                const bool there = c >= 0 && c < min(B, a.k - bk * B);
+                int at[16];
                 float old[16];
 #pragma unroll
                 for (int r = 0; r < 16; r++) {
-                    const int64_t n = n0 + 8 * (r / 4) + r % 4;
+                    at[r] = there ? (n0 + 8 * (r / 4) + r % 4) * pitch + c * S : -16;
                     old[r] = 0.0f;
-                    if (a.accumulate && n < a.n && c < a.k) {
-                        if constexpr (OT == QM_F32) old[r] = gmem<float>(a.out)[n * a.ld_out + c];
+                }
+                if (a.accumulate) {
+#pragma unroll
+                    for (int r = 0; r < 16; r++) {
+                        if constexpr (OT == QM_F32) old[r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rsrc, at[r], 0, 0));
                         else {
-                            const uint16_t h = gmem<uint16_t>(a.out)[n * a.ld_out + c];
+                            const uint16_t h = __builtin_amdgcn_raw_buffer_load_b16(rsrc, at[r], 0, 0);
                             old[r] = OT == QM_BF16 ? bf16_val(h) : f16_val(h);
                         }
                     }
                 }
 #pragma unroll
                 for (int r = 0; r < 16; r++) {
-                    const int64_t n = n0 + 8 * (r / 4) + r % 4;
-                    if (n < a.n && c < a.k) store_one<OT>(a.out, n * a.ld_out + c, in_fp32(old[r] + acc[i][j][r]));
+                    const float x = in_fp32(old[r] + acc[i][j][r]);
+                    if constexpr (OT == QM_F32) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), rsrc, at[r], 0, 0);
+                    else __builtin_amdgcn_raw_buffer_store_b16(OT == QM_BF16 ? bf16_rne(x) : f16_rne(x), rsrc, at[r], 0, 0);
                 }
             }
     };
@@ -430,32 +480,32 @@ __global__ __launch_bounds__(WAVES_N *WAVES_K * 64, B == 256 ? 2 : 2) void weigh
     else leave(std::integral_constant<int, QM_F16>());
 }
 
-// The parts of the split tiles, added in order: a thread takes eight columns
-// of a row.
+// The parts of the split tiles, added in order.  A thread takes eight columns
+// of a row of the parts; of a tile that starts early, those that are its own.
 template <int OT, int B> __global__ __launch_bounds__(256) void weight_grad_join_kernel(ProductArgs a) {
     constexpr int kPerTile = B * B / 8 / 256;
     const int i = blockIdx.x / kPerTile, e = (blockIdx.x % kPerTile) * 256 + threadIdx.x;
     int bn, bk;
     tile_at(a.whole + i, a.tiles_n, a.tiles_k, bn, bk);
     const int row = e / (B / 8), col = e % (B / 8) * 8;
-    const int64_t n = (int64_t)bn * B + row, c = (int64_t)bk * B + col;
-    const int cols = (int)min((int64_t)8, a.k - c);
-    if (n >= a.n || cols <= 0) return;
-    float y[8] = {};
+    const int row_at = a.early_n ? min(bn * B, a.n - B) : bn * B, col_at = a.early_k ? min(bk * B, a.k - B) : bk * B;
+    const int64_t n = (int64_t)row_at + row, c = (int64_t)col_at + col;
+    // the thread's columns from `from` to `to` are this tile's and exist
+    const int from = (int)max((int64_t)0, bk * B - c), to = (int)min((int64_t)8, a.k - c);
+    if (n < bn * B || n >= a.n || from >= to) return;
+    const bool full = from == 0 && to == 8;
     const uint64_t at = a.out + (uint64_t)(n * a.ld_out + c) * kSizeOf<OT>;
+    PackedOf<OT, 8> old = {};
     if (a.accumulate) {
-        PackedOf<OT, 8> w = {};
-        if (cols == 8) w = load_bytes<8 * kSizeOf<OT>>(at, 0);
+        if (full) old = load_bytes<8 * kSizeOf<OT>>(at, 0);
         else {
 #pragma unroll
             for (int j = 0; j < 8; j++) {
-                if (j >= cols) continue;
-                if constexpr (OT == QM_F32) w.w[j] = gmem<const uint32_t>(at)[j];
-                else w.w[j / 2] |= (unsigned)gmem<const uint16_t>(at)[j] << (16 * (j % 2));
+                if (j < from || j >= to) continue;
+                if constexpr (OT == QM_F32) old.w[j] = gmem<const uint32_t>(at)[j];
+                else old.w[j / 2] |= (unsigned)gmem<const uint16_t>(at)[j] << (16 * (j % 2));
             }
         }
-#pragma unroll
-        for (int j = 0; j < 8; j++) y[j] = unpack<OT>(w, j);
     }
     float acc[8] = {};
     const uint64_t p = a.part + (uint64_t)i * a.splits * (B * B * 4) + (uint64_t)(row * B + col) * 4;
@@ -465,13 +515,14 @@ template <int OT, int B> __global__ __launch_bounds__(256) void weight_grad_join
 #pragma unroll
         for (int j = 0; j < 8; j++) acc[j] += __uint_as_float(w.w[j]);
     }
+    float y[8];
 #pragma unroll
-    for (int j = 0; j < 8; j++) y[j] = in_fp32(y[j] + acc[j]);
-    if (cols == 8) store_bytes(at, 0, qm::pack<OT, 8>(y));
+    for (int j = 0; j < 8; j++) y[j] = in_fp32(unpack<OT>(old, j) + acc[j]);
+    if (full) store_bytes(at, 0, qm::pack<OT, 8>(y));
     else {
 #pragma unroll
         for (int j = 0; j < 8; j++)
-            if (j < cols) store_one<OT>(at, j, y[j]);
+            if (j >= from && j < to) store_one<OT>(at, j, y[j]);
     }
 }
 
@@ -501,7 +552,10 @@ Cut cut_for(int b, int64_t rows, int64_t n, int64_t k) {
     return c;
 }
 
+// Sides below 256 (rows at any address are read in tiles that both sides
+// hold) or little work: 128.
 Cut choose_cut(int64_t rows, int64_t n, int64_t k) {
+    if (n < 256 || k < 256) return cut_for(128, rows, n, k);
     const int64_t tiles = ((n + 255) / 256) * ((k + 255) / 256);
     const int64_t steps = (rows + kStep - 1) / kStep;
     return cut_for(tiles * steps >= 4 * kCus ? 256 : 128, rows, n, k);
@@ -509,22 +563,20 @@ Cut choose_cut(int64_t rows, int64_t n, int64_t k) {
 
 uint64_t addr(const void *p) { return (uint64_t)(uintptr_t)p; }
 
-template <int DT, bool KEPT, bool FAST, int B, int WAVES_N, int WAVES_K>
+template <int DT, bool KEPT, int MODE, int B, int WAVES_N, int WAVES_K>
 qm_status launch_product(const ProductArgs &a, hipStream_t q) {
-    constexpr size_t lds = kBufStride<B> + kStep * B * (KEPT ? 3 : 4);
-    auto kern = weight_grad_kernel<DT, KEPT, FAST, B, WAVES_N, WAVES_K>;
+    constexpr size_t lds = kBufStride<B> + kStep * B * (KEPT ? 3 : 4) + (KEPT ? 2 * B : 0);
+    auto kern = weight_grad_kernel<DT, KEPT, MODE, B, WAVES_N, WAVES_K>;
     static std::atomic<bool> set[kMaxDevices] = {};
     if (qm_status e = reserve_lds(reinterpret_cast<const void *>(kern), lds, set)) return e;
     kern<<<(unsigned)(a.whole + a.rest * a.splits), WAVES_N * WAVES_K * 64, lds, q>>>(a);
     return launch_status("weight_grad");
 }
-template <int DT, bool KEPT, bool FAST> qm_status launch_cut(const ProductArgs &a, int b, hipStream_t q) {
-    if (b == 256) return launch_product<DT, KEPT, FAST, 256, 2, 4>(a, q);
-    return launch_product<DT, KEPT, FAST, 128, 2, 2>(a, q);
-}
-template <int DT> qm_status launch_type(const ProductArgs &a, bool kept, bool fast, int b, hipStream_t q) {
-    if (kept) return fast ? launch_cut<DT, true, true>(a, b, q) : launch_cut<DT, true, false>(a, b, q);
-    return fast ? launch_cut<DT, false, true>(a, b, q) : launch_cut<DT, false, false>(a, b, q);
+template <int DT, bool KEPT> qm_status launch_kind(const ProductArgs &a, int mode, int b, hipStream_t q) {
+    if (mode == kNarrow) return launch_product<DT, KEPT, kNarrow, 128, 2, 2>(a, q);
+    if (mode == kAligned)
+        return b == 256 ? launch_product<DT, KEPT, kAligned, 256, 2, 4>(a, q) : launch_product<DT, KEPT, kAligned, 128, 2, 2>(a, q);
+    return b == 256 ? launch_product<DT, KEPT, kAny, 256, 2, 4>(a, q) : launch_product<DT, KEPT, kAny, 128, 2, 2>(a, q);
 }
 template <int OT> void launch_join(const ProductArgs &a, int b, hipStream_t q) {
     if (b == 256) weight_grad_join_kernel<OT, 256><<<(unsigned)a.rest * 32, 256, 0, q>>>(a);
@@ -557,6 +609,8 @@ extern "C" qm_status weight_grad(const void *dy, int32_t dtype, int64_t ld_dy, c
     } else if (qm_status e = check_matrix("x", x, dtype, rows, k, ld_x)) return e;
     if (qm_status e = check_matrix("out", out, out_dtype, n, k, ld_out)) return e;
     if (n == 0 || k == 0 || (rows == 0 && accumulate)) return QM_OK;
+    // 256 rows within a 31-bit byte offset
+    if (ld_out >= (int64_t)1 << 21) return fail(QM_E_SHAPE, "out: row pitch above 2^21 - 1");
     const Cut c = choose_cut(rows, n, k);
     if ((int64_t)c.tiles_n * c.tiles_k >= (int64_t)1 << 22) return fail(QM_E_UNSUPPORTED, "more than 2^22 tiles");
     if (c.bytes) {
@@ -580,11 +634,15 @@ extern "C" qm_status weight_grad(const void *dy, int32_t dtype, int64_t ld_dy, c
     a.splits = c.splits, a.split_steps = c.split_steps;
     a.out_dtype = out_dtype, a.accumulate = accumulate;
     auto wide = [](const void *p, int64_t ld, int64_t cols) { return aligned(p, 16) && ld % 8 == 0 && cols % 8 == 0; };
-    const bool fast = wide(dy, ld_dy, n) && (kept || wide(x, ld_x, k));
+    int mode = kAligned;
+    if (!wide(dy, ld_dy, n) || !(kept || wide(x, ld_x, k))) mode = n >= c.b && (kept || k >= c.b) ? kAny : kNarrow;
+    a.early_n = mode == kAny, a.early_k = mode == kAny && !kept;
     const hipStream_t q = static_cast<hipStream_t>(stream);
-    if (qm_status e = dtype == QM_BF16 ? launch_type<QM_BF16>(a, kept != nullptr, fast, c.b, q)
-                                       : launch_type<QM_F16>(a, kept != nullptr, fast, c.b, q))
-        return e;
+    const bool bf = dtype == QM_BF16;
+    qm_status e;
+    if (kept) e = bf ? launch_kind<QM_BF16, true>(a, mode, c.b, q) : launch_kind<QM_F16, true>(a, mode, c.b, q);
+    else e = bf ? launch_kind<QM_BF16, false>(a, mode, c.b, q) : launch_kind<QM_F16, false>(a, mode, c.b, q);
+    if (e) return e;
     if (c.splits == 1) return QM_OK;
     if (out_dtype == QM_F32) launch_join<QM_F32>(a, c.b, q);
     else if (out_dtype == QM_BF16) launch_join<QM_BF16>(a, c.b, q);
