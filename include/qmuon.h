@@ -669,7 +669,7 @@ QM_API qm_status act_read(const qm_act8 *kept, void *out, int32_t dtype,
  *   ws: >= weight_grad_workspace_bytes(rows, n, k) bytes (0: none needed),
  *   16-byte aligned.
  * Errors: QM_E_ARG, QM_E_ALIGN, QM_E_DTYPE, QM_E_SHAPE, QM_E_WORKSPACE,
- * QM_E_UNSUPPORTED (more than 2^22 tiles of 128 or 256 squared), QM_E_HIP. */
+ * QM_E_UNSUPPORTED (more than 2^22 tiles of 128 x 128), QM_E_HIP. */
 QM_API size_t weight_grad_workspace_bytes(int64_t rows, int64_t n, int64_t k);
 QM_API qm_status weight_grad(const void *dy, int32_t dtype, int64_t ld_dy,
                              const void *x, int64_t ld_x, const qm_act8 *kept,

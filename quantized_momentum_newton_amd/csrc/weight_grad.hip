@@ -20,6 +20,8 @@
 // has no edge cases.  Tiles that do not fill a round of the GPU are split over
 // t; their parts go to the workspace and are added in order by a second
 // kernel.
+#include <math.h>
+
 #include <algorithm>
 #include <type_traits>
 
@@ -535,7 +537,7 @@ struct Cut {
     size_t bytes;                // of the parts
 };
 
-Cut cut_for(int b, int64_t rows, int64_t n, int64_t k) {
+Cut cut_for(int b, int splits, int64_t rows, int64_t n, int64_t k) {
     Cut c{};
     c.b = b;
     c.tiles_n = (int)((n + b - 1) / b);
@@ -544,21 +546,49 @@ Cut cut_for(int b, int64_t rows, int64_t n, int64_t k) {
     const int steps = (int)((rows + kStep - 1) / kStep);
     c.whole = (int)(tiles / slots * slots);
     c.rest = (int)(tiles - c.whole);
-    c.splits = 1;
-    if (c.rest) c.splits = (int)std::max<int64_t>(1, std::min<int64_t>(slots / c.rest, steps / 4));
-    c.split_steps = (steps + c.splits - 1) / c.splits;
-    if (c.split_steps) c.splits = std::max(1, (steps + c.split_steps - 1) / c.split_steps);
+    c.split_steps = std::max(1, (steps + splits - 1) / splits);
+    c.splits = c.rest ? std::max(1, (steps + c.split_steps - 1) / c.split_steps) : 1;
+    if (c.splits == 1) c.split_steps = steps;
     c.bytes = c.splits > 1 ? (size_t)c.rest * c.splits * b * b * 4 : 0;
     return c;
 }
 
-// Sides below 256 (rows at any address are read in tiles that both sides
-// hold) or little work: 128.
-Cut choose_cut(int64_t rows, int64_t n, int64_t k) {
-    if (n < 256 || k < 256) return cut_for(128, rows, n, k);
-    const int64_t tiles = ((n + 255) / 256) * ((k + 255) / 256);
-    const int64_t steps = (rows + kStep - 1) / kStep;
-    return cut_for(tiles * steps >= 4 * kCus ? 256 : 128, rows, n, k);
+// Expected microseconds of a cut, from measured steps: a 256 tile's step takes
+// 1.7 (kept input 1.55) with one workgroup a CU; a 128 tile's 0.6 alone on its
+// CU, 1.0 with a second one.  3 + 3 for the launch and what a tile starts and
+// ends with; parts are written and read at 5 TB/s, by a launch that costs 4.
+double cost(const Cut &c, int steps, bool kept) {
+    const double full = c.b == 256 ? (kept ? 1.55 : 1.7) : 1.0;
+    const int slots = c.b == 256 ? kCus : 2 * kCus, parts = c.rest * c.splits;
+    double us = 6 + c.whole / slots * steps * full + parts / slots * c.split_steps * full;
+    const int last = parts % slots;
+    if (last) us += c.split_steps * (c.b == 128 && last <= kCus ? 0.6 : full);
+    if (c.bytes) us += 4 + 2 * c.bytes / 5e6;
+    return us;
+}
+
+// The cut that should take least.  Measured, cut by cut (us; tile / parts):
+// 2048 x 1008 over 5001 rows 128/1 47, 128/2 39, 128/4 40, 256/6 47; 1024 x 4096
+// over 8192 128/1 84, 128/2 88, 256/4 87; 6144 x 2048 over 8192 128/1 217,
+// 256/1 234, from kept input 216 and 195; 1024 x 2048 over 65536 256/8 255,
+// 128/4 305; 256 x 256 over 16384 128/8 24, 128/24 18, 128/64 23; 1000 x 1000
+// over 300 128/1 9, 128/2 13.  Sides below 256 take tiles of 128: rows at any
+// address are read in tiles that both sides hold.
+Cut choose_cut(int64_t rows, int64_t n, int64_t k, bool kept) {
+    const int steps = (int)((rows + kStep - 1) / kStep);
+    Cut best{};
+    double least = INFINITY;
+    for (int b = 128; b <= (n < 256 || k < 256 ? 128 : 256); b += 128)
+        for (int splits = 1; splits <= std::max(1, std::min(64, steps / 2)); splits++) {
+            const Cut c = cut_for(b, splits, rows, n, k);
+            const double us = cost(c, steps, kept);
+            if (us < least) {
+                least = us;
+                best = c;
+            }
+            if (c.rest == 0 || c.rest * (splits + 1) > 8 * kCus) break;
+        }
+    return best;
 }
 
 uint64_t addr(const void *p) { return (uint64_t)(uintptr_t)p; }
@@ -591,8 +621,8 @@ bool bad_side(int64_t v) { return v < 0 || v >= (int64_t)1 << 30; }
 using namespace qm;
 
 extern "C" size_t weight_grad_workspace_bytes(int64_t rows, int64_t n, int64_t k) {
-    if (bad_side(rows) || bad_side(n) || bad_side(k)) return 0;
-    return choose_cut(rows, n, k).bytes;
+    if (bad_side(rows) || bad_side(n) || bad_side(k) || ((n + 127) / 128) * ((k + 127) / 128) >= (int64_t)1 << 22) return 0;
+    return std::max(choose_cut(rows, n, k, false).bytes, choose_cut(rows, n, k, true).bytes);
 }
 
 extern "C" qm_status weight_grad(const void *dy, int32_t dtype, int64_t ld_dy, const void *x, int64_t ld_x,
@@ -611,8 +641,8 @@ extern "C" qm_status weight_grad(const void *dy, int32_t dtype, int64_t ld_dy, c
     if (n == 0 || k == 0 || (rows == 0 && accumulate)) return QM_OK;
     // 256 rows within a 31-bit byte offset
     if (ld_out >= (int64_t)1 << 21) return fail(QM_E_SHAPE, "out: row pitch above 2^21 - 1");
-    const Cut c = choose_cut(rows, n, k);
-    if ((int64_t)c.tiles_n * c.tiles_k >= (int64_t)1 << 22) return fail(QM_E_UNSUPPORTED, "more than 2^22 tiles");
+    if (((n + 127) / 128) * ((k + 127) / 128) >= (int64_t)1 << 22) return fail(QM_E_UNSUPPORTED, "more than 2^22 tiles of 128 x 128");
+    const Cut c = choose_cut(rows, n, k, kept != nullptr);
     if (c.bytes) {
         if (!ws || ws_bytes < c.bytes) return fail(QM_E_WORKSPACE, "workspace: need %zu bytes", c.bytes);
         if (!aligned(ws, 16)) return fail(QM_E_ALIGN, "workspace needs 16-byte alignment");

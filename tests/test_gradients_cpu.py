@@ -149,6 +149,8 @@ def weight(dy=X, dtype=1, ld_dy=64, x=Y, ld_x=40, k8=None, rows=64, n=64, k=40, 
     (WORKSPACE, lambda: weight(rows=4096, ws=BASE, nws=LIB.weight_grad_workspace_bytes(4096, 64, 40) - 1)),
     (ALIGN, lambda: weight(rows=4096, ws=BASE + 8, nws=1 << 30)),
     (ARG, lambda: weight(rows=4096, ws=X + 4096, nws=1 << 30)),
+    (SHAPE, lambda: weight(ld_out=1 << 21)),
+    (UNSUPPORTED, lambda: weight(rows=1, n=1 << 18, k=1 << 18, ld_dy=1 << 18, ld_x=1 << 18, ld_out=1 << 18)),
 ])
 def test_weight_grad_refuses(status, call):
     assert call() == status
