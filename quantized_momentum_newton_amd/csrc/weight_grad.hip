@@ -321,8 +321,11 @@ __global__ __launch_bounds__(WAVES_N *WAVES_K * 64, B == 256 ? 2 : 2) void weigh
             for (int r = 0; r < 16; r++) acc[i][j][r] = 0.0f;
 
     const int steps = (t1 - t0 + kStep - 1) / kStep;
-    u32x4_t fa[2][FN];
-    typename PanelB::Raw fb[2][FK];
+    // Slices whose fragments are read ahead.  A 128 tile's slice (four products,
+    // 128 cycles, often one wave on a SIMD) is shorter than a read.
+    constexpr int AHEAD = B == 256 ? 1 : 2, SETS = B == 256 ? 2 : 4;
+    u32x4_t fa[SETS][FN];
+    typename PanelB::Raw fb[SETS][FK];
     uint32_t unit[2][FK];      // scale bytes of the lane's columns, of both groups
     auto read = [&](int s, u32x4_t *x, typename PanelB::Raw *y) {
         if constexpr (KEPT) {
@@ -335,10 +338,10 @@ __global__ __launch_bounds__(WAVES_N *WAVES_K * 64, B == 256 ? 2 : 2) void weigh
 #pragma unroll
         for (int i = 0; i < FN; i++) PanelA::read(lds + off_a[i], s, x[i]);
     };
-    // A step's four slices of 16 rows.  While a slice is multiplied, the next
-    // one's fragments are read into the other register set; the barrier between
-    // two steps stands before the last slice's products, so that those cover
-    // the first reads of the next step.  Left alone the compiler moves each
+    // A step's four slices of 16 rows.  While a slice is multiplied, the
+    // fragments of one after it are read into another register set; the barrier
+    // between two steps stands before the last AHEAD slices' products, so that
+    // those cover the first reads of the next step.  Left alone the compiler moves each
     // read down to its use; issued in one run ahead of the products they would
     // hold up the wave's matrix instructions, and right after a barrier those
     // of every wave.  So each product is followed by its share of the slice's
@@ -372,15 +375,18 @@ __global__ __launch_bounds__(WAVES_N *WAVES_K * 64, B == 256 ? 2 : 2) void weigh
             load_scales(d, t0 + (d + 1) * kStep);
         }
         lds_barrier();
-        read(0, fa[0], fb[0]);
+#pragma unroll
+        for (int s = 0; s < AHEAD; s++) read(s, fa[s], fb[s]);
     }
-    // step `it`, whose successor is in the registers d
+    // step `it`, whose successor is in the registers d and goes to LDS in the
+    // two slices before the barrier
+    constexpr int PUT = STEPS - AHEAD - 2;
     auto step = [&](int it, int d) {
         const int ahead = t0 + (it + 1 + DEPTH) * kStep;
 #pragma unroll
         for (int s = 0; s < STEPS; s++) {
-            const int now = s & 1, then = now ^ 1;
-            if (s == STEPS - 1) {
+            const int now = s % SETS, then = (s + AHEAD) % SETS;
+            if (s == STEPS - AHEAD) {
                 lds_barrier();
                 off_s ^= BUF;
 #pragma unroll
@@ -389,13 +395,13 @@ __global__ __launch_bounds__(WAVES_N *WAVES_K * 64, B == 256 ? 2 : 2) void weigh
                 for (int j = 0; j < FK; j++) off_b[j] ^= BUF;
                 __builtin_amdgcn_sched_barrier(0);
             }
-            read((s + 1) % STEPS, fa[then], fb[then]);
+            read((s + AHEAD) % STEPS, fa[then], fb[then]);
             // the other buffer's last readers passed the previous barrier
-            if (s == 1) {
+            if (s == PUT) {
                 pa.store(d, lds + off_next);
                 pa.load(d, ahead, t1);
             }
-            if (s == 2) {
+            if (s == PUT + 1) {
                 pb.store(d, lds + off_next + PanelA::kBytes);
                 store_scales(d, lds + off_next);
                 off_next ^= BUF;
@@ -412,8 +418,8 @@ __global__ __launch_bounds__(WAVES_N *WAVES_K * 64, B == 256 ? 2 : 2) void weigh
             for (int i = 0; i < FN; i++)
 #pragma unroll
                 for (int j = 0; j < FK; j++) mfma<DT>(fa[now][i], b[j], acc[i][j]);
-            if (s == 1) interleave(integral_constant<int, PanelA::kPieces>(), integral_constant<int, PanelA::kPieces>());
-            else if (s == 2)
+            if (s == PUT) interleave(integral_constant<int, PanelA::kPieces>(), integral_constant<int, PanelA::kPieces>());
+            else if (s == PUT + 1)
                 interleave(integral_constant<int, PanelB::kPieces + KEPT>(), integral_constant<int, PanelB::kPieces + KEPT>());
             else interleave(integral_constant<int, 0>(), integral_constant<int, 0>());
         }
