@@ -705,7 +705,7 @@ QM_API qm_status gated_act_backward(const qm_act8 *gate8, const qm_act8 *up8,
 /* out[i] = scale * table[tokens[i]], rounded once; a token outside [0, vocab)
  * (padding) gives a row of zeros.  tokens: contiguous int32 or int64
  * (token_bits); fewer than 2^30 tokens and values.  Errors: QM_E_ARG, QM_E_ALIGN, QM_E_DTYPE,
- * QM_E_SHAPE, QM_E_UNSUPPORTED (more than 2^34 pieces of 8 columns),
+ * QM_E_SHAPE, QM_E_UNSUPPORTED (more than 2^34 pieces of 4 or 8 columns),
  * QM_E_HIP. */
 QM_API qm_status embedding_lookup(const void *tokens, int32_t token_bits,
                                   int64_t n_tokens, const void *table,

@@ -15,11 +15,13 @@
 //          contiguous part of the tokens, so (value, wave, position) is the
 //          order, and the place of equal values among a wave's 64 comes from
 //          one ballot per bit of the value.
-//   sum    A row of at most 64 tokens is summed by one wave (per 512 columns)
-//          and stored.  Longer rows are cut where multiples of 64 positions
-//          of the order lie: a cut part is summed by one wave into the
-//          workspace.  A gradient that is written whole also gets its zeros
-//          here, one that is added to is touched in rows that have tokens.
+//   sum    A wave takes the rows that start in a range of 16 positions of the
+//          order (per 1024 columns) and runs through their tokens, several rows
+//          of dy in flight whichever row of the table they go to.  Rows of more
+//          than 64 tokens are cut where multiples of 64 positions lie: a cut
+//          part is summed by one wave into the workspace.  A gradient that is
+//          written whole also gets its zeros here, one that is added to is
+//          touched in rows that have tokens.
 //   join   The parts of a long row are added, in order, by one workgroup.
 #include <algorithm>
 #include <type_traits>
@@ -33,30 +35,33 @@ namespace {
 constexpr int kChunk = 64;        // positions of a part, and the longest row without parts
 constexpr int kSortWaves = 16, kSortValues = 1024;
 constexpr int kSumWaves = 4, kJoinWaves = 8;
+constexpr int kFill = 16;         // rows that a wave looks at for empty ones
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;     // tokens, and values: their counts stay 32-bit numbers
 
-// A lane's n <= 8 elements at `at` as fp32.
-template <int DT> __device__ __forceinline__ void load_cols(uint64_t at, int n, float *x) {
-    PackedOf<DT, 8> r = {};
-    if (n == 8) r = load_bytes<8 * kSizeOf<DT>>(at, 0);
+// A lane's n <= V elements at `at` as fp32.  V is 8 where everything a kernel
+// moves has 16 bits and 4 where a part has 32: an access of a wave is then one
+// run of 1 KiB of the widest type, and never every other 16 bytes of one.
+template <int DT, int V> __device__ __forceinline__ void load_cols(uint64_t at, int n, float *x) {
+    PackedOf<DT, V> r = {};
+    if (n == V) r = load_bytes<V * kSizeOf<DT>>(at, 0);
     else {
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
+        for (int j = 0; j < V; j++) {
             if (j >= n) continue;
             if constexpr (DT == QM_F32) r.w[j] = gmem<const uint32_t>(at)[j];
             else r.w[j / 2] |= (unsigned)gmem<const uint16_t>(at)[j] << (16 * (j % 2));
         }
     }
 #pragma unroll
-    for (int j = 0; j < 8; j++) x[j] = unpack<DT>(r, j);
+    for (int j = 0; j < V; j++) x[j] = unpack<DT>(r, j);
 }
-template <int DT> __device__ __forceinline__ void store_cols(uint64_t at, int n, const float *x) {
-    if (n == 8) {
-        store_bytes(at, 0, qm::pack<DT, 8>(x));
+template <int DT, int V> __device__ __forceinline__ void store_cols(uint64_t at, int n, const float *x) {
+    if (n == V) {
+        store_bytes(at, 0, qm::pack<DT, V>(x));
         return;
     }
 #pragma unroll
-    for (int j = 0; j < 8; j++)
+    for (int j = 0; j < V; j++)
         if (j < n) store_one<DT>(at, j, x[j]);
 }
 
@@ -64,18 +69,27 @@ __device__ __forceinline__ int64_t token_at(uint64_t tokens, int bits, int64_t i
     return bits == 64 ? gmem<const int64_t>(tokens)[i] : (int64_t)gmem<const int32_t>(tokens)[i];
 }
 
+// The token as a 32-bit number, what a table cannot have as the largest.
+__device__ __forceinline__ uint32_t token32_at(uint64_t tokens, int bits, int64_t i) {
+    if (bits == 32) return gmem<const uint32_t>(tokens)[i];      // negative: large
+    const uint64_t t = gmem<const uint64_t>(tokens)[i];
+    return t >> 32 ? 0xffffffffu : (uint32_t)t;
+}
+
 // ------------------------------------------------------------------ lookup
 
 struct LookupArgs {
     uint64_t tokens, table, out;
     int64_t n_tokens, ld_table, ld_out;
-    int vocab, cols, pieces, token_bits;     // pieces: of 8 columns, in a row
+    int vocab, cols, pieces, token_bits;     // pieces: of a thread's columns, in a row
     float scale;
 };
 
 constexpr int kLookupThreads = 256, kLookupEach = 4;
+template <int DT, int OUT> constexpr int kLookupCols = DT == QM_F32 || OUT == QM_F32 ? 4 : 8;
 
 template <int DT, int OUT> __global__ __launch_bounds__(kLookupThreads) void embedding_lookup_kernel(LookupArgs a) {
+    constexpr int V = kLookupCols<DT, OUT>;
     // the workgroup's pieces follow one another through rows and columns
     const int64_t first = (int64_t)blockIdx.x * (kLookupThreads * kLookupEach);
     const int64_t row0 = first / a.pieces;
@@ -86,22 +100,22 @@ template <int DT, int OUT> __global__ __launch_bounds__(kLookupThreads) void emb
     for (int k = 0; k < kLookupEach; k++) {
         const uint32_t at = at0 + k * kLookupThreads + threadIdx.x;
         row[k] = row0 + at / (uint32_t)a.pieces;
-        col[k] = (int)(at % (uint32_t)a.pieces) * 8;
+        col[k] = (int)(at % (uint32_t)a.pieces) * V;
         tok[k] = row[k] < a.n_tokens ? token_at(a.tokens, a.token_bits, row[k]) : -1;
     }
-    float x[kLookupEach][8];
+    float x[kLookupEach][V];
 #pragma unroll
     for (int k = 0; k < kLookupEach; k++) {
         const bool inside = (uint64_t)tok[k] < (uint64_t)a.vocab;
-        const int n = inside ? min(8, a.cols - col[k]) : 0;
-        load_cols<DT>(a.table + (uint64_t)(tok[k] * a.ld_table + col[k]) * kSizeOf<DT>, n, x[k]);
+        const int n = inside ? min(V, a.cols - col[k]) : 0;
+        load_cols<DT, V>(a.table + (uint64_t)(tok[k] * a.ld_table + col[k]) * kSizeOf<DT>, n, x[k]);
     }
 #pragma unroll
     for (int k = 0; k < kLookupEach; k++) {
         if (row[k] >= a.n_tokens) continue;
 #pragma unroll
-        for (int j = 0; j < 8; j++) x[k][j] = in_fp32(x[k][j] * a.scale);
-        store_cols<OUT>(a.out + (uint64_t)(row[k] * a.ld_out + col[k]) * kSizeOf<OUT>, min(8, a.cols - col[k]), x[k]);
+        for (int j = 0; j < V; j++) x[k][j] = in_fp32(x[k][j] * a.scale);
+        store_cols<OUT, V>(a.out + (uint64_t)(row[k] * a.ld_out + col[k]) * kSizeOf<OUT>, min(V, a.cols - col[k]), x[k]);
     }
 }
 
@@ -128,22 +142,21 @@ __global__ __launch_bounds__(kSortWaves * 64) void embedding_sort_kernel(SortArg
     const int begin = min(wave * share, a.n), end = min(begin + share, a.n);
     int32_t *mine = count + wave * a.values;
 
-    constexpr int kAhead = 4;    // tokens of a lane in flight
-    int less = 0;
+    constexpr int kAhead = 16;   // tokens of a lane in flight
+    int less = 0;                // of the wave
     for (int c = begin; c < end; c += 64 * kAhead) {
-        int64_t t[kAhead];
+        uint32_t t[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; k++) {
             const int i = c + k * 64 + lane;
-            t[k] = i < end ? token_at(a.tokens, a.token_bits, i) : -1;
+            t[k] = i < end ? token32_at(a.tokens, a.token_bits, i) : 0xffffffffu;
         }
 #pragma unroll
         for (int k = 0; k < kAhead; k++) {
-            less += t[k] >= 0 && t[k] < lo;
-            if (t[k] >= lo && t[k] < lo + values) atomicAdd(&mine[t[k] - lo], 1);
+            less += __popcll(__ballot(t[k] < (uint32_t)lo));
+            if (t[k] - lo < (uint32_t)values) atomicAdd(&mine[t[k] - lo], 1);
         }
     }
-    for (int k = 1; k < 64; k *= 2) less += __shfl_xor(less, k);
     if (lane == 0) wave_less[wave] = less;
     __syncthreads();
 
@@ -176,15 +189,15 @@ __global__ __launch_bounds__(kSortWaves * 64) void embedding_sort_kernel(SortArg
     __syncthreads();
 
     for (int c = begin; c < end; c += 64 * kAhead) {
-        int64_t t[kAhead];
+        uint32_t t[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; k++) {
             const int i = c + k * 64 + lane;
-            t[k] = i < end ? token_at(a.tokens, a.token_bits, i) : -1;
+            t[k] = i < end ? token32_at(a.tokens, a.token_bits, i) : 0xffffffffu;
         }
 #pragma unroll
         for (int k = 0; k < kAhead; k++) {
-            const bool in = t[k] >= lo && t[k] < lo + values;
+            const bool in = t[k] - lo < (uint32_t)values;
             uint64_t same = __ballot(in);
             if (same == 0) continue;
             const int value = in ? (int)(t[k] - lo) : 0;
@@ -206,139 +219,241 @@ __global__ __launch_bounds__(kSortWaves * 64) void embedding_sort_kernel(SortArg
 struct SumArgs {
     uint64_t sorted, start, head, part, dy, grad;
     int64_t ld_dy, ld_grad;
-    int vocab, cols, n_tokens;
-    int slabs, part_ld;      // slabs: of 8 * lanes columns; part_ld: columns rounded up to 8
-    int chunks, rows;        // units of the launch: chunks * slabs, then rows * slabs
-    int accumulate;
+    int vocab, cols;
+    int slabs, part_ld;                     // slabs: units across a row; part_ld: columns rounded up to 8
+    int chunks, ranges, range, fills;       // units down: chunks, ranges of `range` positions, kFill rows each
+    int accumulate, grad_dtype;
     float scale;
 };
 
-__device__ __forceinline__ Sorted sorted_at(uint64_t sorted, int i) { return gmem<const Sorted>(sorted)[i]; }
 __device__ __forceinline__ int start_of(uint64_t start, int v) { return gmem<const int32_t>(start)[v]; }
 
-// acc = the dy rows of positions first .. first + n - 1 of the order, in that
-// order; n >= 1.
-template <int DT> __device__ __forceinline__ void sum_positions(const SumArgs &a, int first, int n, int col, int cols, float *acc) {
-    constexpr int kAhead = 4;     // rows in flight
-    const uint64_t base = a.dy + (uint64_t)col * kSizeOf<DT>;
-    load_cols<DT>(base + (uint64_t)(sorted_at(a.sorted, first).position * a.ld_dy) * kSizeOf<DT>, cols, acc);
-    for (int k = 1; k < n; k += kAhead) {
-        float x[kAhead][8];
-        int at[kAhead];
-#pragma unroll
-        for (int u = 0; u < kAhead; u++) at[u] = sorted_at(a.sorted, first + min(k + u, n - 1)).position;
-#pragma unroll
-        for (int u = 0; u < kAhead; u++) load_cols<DT>(base + (uint64_t)(at[u] * a.ld_dy) * kSizeOf<DT>, cols, x[u]);
-#pragma unroll
-        for (int u = 0; u < kAhead; u++)
-#pragma unroll
-            for (int j = 0; j < 8; j++) acc[j] += k + u < n ? x[u][j] : 0.0f;
+// A lane's columns: P pieces of V.
+template <int V, int P> struct Columns {
+    int first, cols;        // the lane's first column; the row's columns
+    __device__ __forceinline__ Columns(int slab, int lane, int n) : first(slab * (64 * V * P) + lane * V), cols(n) {}
+    __device__ __forceinline__ int col(int p) const { return first + p * (64 * V); }
+    // how many of piece p exist.  The empty asm has it looked at anew at each
+    // use: kept, the outcomes for V elements of every piece fill the scalar
+    // registers.
+    __device__ __forceinline__ int n(int p) const {
+        int r = max(0, min(V, cols - col(p)));
+        asm volatile("" : "+v"(r));
+        return r;
     }
-}
+};
 
-template <int GT> __device__ __forceinline__ void finish_row(const SumArgs &a, int token, int col, int cols, const float *acc) {
-    const uint64_t at = a.grad + (uint64_t)(token * a.ld_grad + col) * kSizeOf<GT>;
-    float y[8] = {};
-    if (a.accumulate) load_cols<GT>(at, cols, y);
+template <int DT, int V, int P> struct Piece {
+    PackedOf<DT, V> w[P];
+    __device__ __forceinline__ void load(uint64_t row, const Columns<V, P> &c) {
 #pragma unroll
-    for (int j = 0; j < 8; j++) y[j] = in_fp32(y[j] + a.scale * acc[j]);
-    store_cols<GT>(at, cols, y);
-}
-
-template <int DT, int GT, int LANES> __global__ __launch_bounds__(kSumWaves * 64) void embedding_sum_kernel(SumArgs a) {
-    const int lane = threadIdx.x % LANES;
-    const int64_t unit = (int64_t)blockIdx.x * (kSumWaves * 64 / LANES) + threadIdx.x / LANES;
-    const int64_t chunk_units = (int64_t)a.chunks * a.slabs;
-    const int slab = (int)(unit % a.slabs), col = slab * LANES * 8 + lane * 8;
-    const int cols = max(0, min(8, a.cols - col));
-    float acc[8];
-    if (unit < chunk_units) {
-        // the parts of long rows that end, pass through or start in this chunk
-        const int chunk = (int)(unit / a.slabs), n_sorted = start_of(a.start, a.vocab);
-        const int first = chunk * kChunk, last = min(first + kChunk, n_sorted) - 1;
-        int head = -1;
-        if (first <= last) {
-            const int t0 = sorted_at(a.sorted, first).token, t1 = sorted_at(a.sorted, last).token;
-            const uint64_t part = a.part + ((uint64_t)chunk * 2 * a.part_ld + col) * 4;
-            const int s0 = start_of(a.start, t0), e0 = start_of(a.start, t0 + 1);
-            if (e0 - s0 > kChunk) {
-                if (s0 == first) head = t0;
-                if (cols) {
-                    sum_positions<DT>(a, first, min(e0 - 1, last) - first + 1, col, cols, acc);
-                    store_cols<QM_F32>(part, cols, acc);
-                }
-            }
-            const int s1 = start_of(a.start, t1), e1 = start_of(a.start, t1 + 1);
-            if (t1 != t0 && e1 - s1 > kChunk) {
-                head = t1;
-                if (cols) {
-                    sum_positions<DT>(a, s1, last - s1 + 1, col, cols, acc);
-                    store_cols<QM_F32>(part + (uint64_t)a.part_ld * 4, cols, acc);
+        for (int p = 0; p < P; p++) {
+            const uint64_t at = row + (uint64_t)c.col(p) * kSizeOf<DT>;
+            const int n = c.n(p);
+            w[p] = {};
+            if (n == V) w[p] = load_bytes<V * kSizeOf<DT>>(at, 0);
+            else {
+#pragma unroll
+                for (int j = 0; j < V; j++) {
+                    if (j >= n) continue;
+                    if constexpr (DT == QM_F32) w[p].w[j] = gmem<const uint32_t>(at)[j];
+                    else w[p].w[j / 2] |= (unsigned)gmem<const uint16_t>(at)[j] << (16 * (j % 2));
                 }
             }
         }
-        if (slab == 0 && lane == 0) gmem<int32_t>(a.head)[chunk] = head;
-        return;
     }
-    const int64_t row = (unit - chunk_units) / a.slabs;
-    if (row >= a.rows) return;
-    int token, first, n;
-    if (a.accumulate) {      // one unit a position: the first of each row is taken
-        first = (int)row;
-        if (first >= start_of(a.start, a.vocab)) return;
-        token = sorted_at(a.sorted, first).token;
-        if (first > 0 && sorted_at(a.sorted, first - 1).token == token) return;
-        n = start_of(a.start, token + 1) - first;
-    } else {
-        token = (int)row;
-        first = start_of(a.start, token);
-        n = start_of(a.start, token + 1) - first;
-    }
-    if (n > kChunk || !cols) return;
-    if (n > 0) sum_positions<DT>(a, first, n, col, cols, acc);
-    else
+};
+
+// Sums dy rows along the order: entries `from` .. `to` - 1 of a window of 128
+// whose positions lanes hold (entry w in lane w % 64 of pos[w / 64]), several
+// rows in flight whatever they belong to.  ends(w): whether a row of the table
+// ends with entry w; then old.load has its gradient under way with the entry's
+// own loads and leave(w, acc, old) takes the sum.
+template <int DT, int V, int P, typename Old, typename Ends, typename Fetch, typename Leave>
+__device__ __forceinline__ void stream(const SumArgs &a, const int *pos, int from, int to, const Columns<V, P> &c, Ends ends,
+                                       Fetch fetch, Leave leave) {
+    constexpr int kAhead = P * V >= 16 ? 4 : 8;
+    float acc[P][V] = {};
+    for (int w = from; w < to; w += kAhead) {
+        Piece<DT, V, P> x[kAhead];
+        Old old[kAhead];
 #pragma unroll
-        for (int j = 0; j < 8; j++) acc[j] = 0.0f;
-    finish_row<GT>(a, token, col, cols, acc);
+        for (int u = 0; u < kAhead; u++) {
+            if (w + u >= to) continue;
+            const int at = __builtin_amdgcn_readlane(w + u < 64 ? pos[0] : pos[1], (w + u) & 63);
+            x[u].load(a.dy + (uint64_t)(at * a.ld_dy) * kSizeOf<DT>, c);
+            if (ends(w + u)) fetch(w + u, old[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; u++) {
+            if (w + u >= to) continue;
+#pragma unroll
+            for (int p = 0; p < P; p++)
+#pragma unroll
+                for (int j = 0; j < V; j++) acc[p][j] += unpack<DT>(x[u].w[p], j);
+            if (ends(w + u)) {
+                leave(w + u, acc, old[u]);
+#pragma unroll
+                for (int p = 0; p < P; p++)
+#pragma unroll
+                    for (int j = 0; j < V; j++) acc[p][j] = 0.0f;
+            }
+        }
+    }
 }
 
-// One workgroup per chunk and 512 columns; those in whose chunk no long row
+struct Nothing {};
+
+template <int DT, int GT, int V, int P, bool ACC> __global__ __launch_bounds__(kSumWaves * 64) void embedding_sum_kernel(SumArgs a) {
+    const int lane = threadIdx.x & 63;
+    const int unit = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * kSumWaves + (threadIdx.x >> 6)));
+    const int slab = unit % a.slabs;
+    int down = unit / a.slabs;
+    const Columns<V, P> c(slab, lane, a.cols);
+    const int n_sorted = start_of(a.start, a.vocab);
+    auto sorted_at = [&](int i) { return gmem<const Sorted>(a.sorted)[i]; };
+
+    if (down < a.chunks) {
+        // the parts of long rows that end, pass through or start in this chunk
+        const int first = down * kChunk, last = min(first + kChunk, n_sorted) - 1;
+        int head = -1;
+        if (first <= last) {
+            const Sorted e = sorted_at(min(first + lane, last));
+            const int pos[2] = {e.position, 0};
+            const int t0 = __builtin_amdgcn_readlane(e.token, 0), t1 = __builtin_amdgcn_readlane(e.token, last - first);
+            const int s0 = start_of(a.start, t0), e0 = start_of(a.start, t0 + 1), s1 = start_of(a.start, t1), e1 = start_of(a.start, t1 + 1);
+            auto part = [&](int slot, int from, int to) {
+                stream<DT, V, P, Nothing>(a, pos, from, to, c, [&](int w) { return w == to - 1; }, [](int, Nothing &) {},
+                                          [&](int, float (*acc)[V], Nothing &) {
+#pragma unroll
+                                              for (int p = 0; p < P; p++)
+                                                  store_cols<QM_F32, V>(a.part + (((uint64_t)down * 2 + slot) * a.part_ld + c.col(p)) * 4,
+                                                                        c.n(p), acc[p]);
+                                          });
+            };
+            if (e0 - s0 > kChunk) {
+                if (s0 == first) head = t0;
+                part(0, 0, min(e0 - 1, last) - first + 1);
+            }
+            if (t1 != t0 && e1 - s1 > kChunk) {
+                head = t1;
+                part(1, s1 - first, last - first + 1);
+            }
+        }
+        if (slab == 0 && lane == 0) gmem<int32_t>(a.head)[down] = head;
+        return;
+    }
+    down -= a.chunks;
+    if (down < a.ranges) {
+        // the rows that start in this range of the order, but for long ones;
+        // window entry w is position begin - 1 + w
+        const int begin = down * a.range;
+        if (begin >= n_sorted) return;
+        auto entry = [&](int i) { return i < 0 || i >= n_sorted ? Sorted{i < 0 ? -2 : -3, 0} : sorted_at(i); };
+        const Sorted lo = entry(begin - 1 + lane), hi = entry(begin + 63 + lane);
+        const int pos[2] = {lo.position, hi.position};
+        const int before_lo = __shfl_up(lo.token, 1), before_hi = __shfl_up(hi.token, 1);
+        const uint64_t head_lo = __ballot(lane > 0 && lo.token != before_lo);
+        const uint64_t head_hi = __ballot(hi.token != (lane > 0 ? before_hi : __builtin_amdgcn_readlane(lo.token, 63)));
+        const uint64_t here = head_lo & ((2ull << a.range) - 2);
+        if (here == 0) return;
+        const int from = __ffsll((unsigned long long)here) - 1, last = 63 - __clzll((long long)here);
+        const uint64_t after = head_lo & ~((2ull << last) - 1);
+        int to = after ? __ffsll((unsigned long long)after) - 1 : head_hi ? 64 + __ffsll((unsigned long long)head_hi) - 1 : 128;
+        if (to - last > kChunk) to = last;      // a long row: its parts are summed elsewhere
+        auto ends = [&](int w) { return w + 1 == to || (w + 1 < 64 && head_lo >> (w + 1) & 1); };
+        auto row = [&](int w) {
+            const int token = __builtin_amdgcn_readlane(w < 64 ? lo.token : hi.token, w & 63);
+            return a.grad + (uint64_t)(token * a.ld_grad) * kSizeOf<GT>;
+        };
+        using Old = std::conditional_t<ACC, Piece<GT, V, P>, Nothing>;
+        stream<DT, V, P, Old>(
+            a, pos, from, to, c, ends,
+            [&](int w, Old &old) {
+                if constexpr (ACC) old.load(row(w), c);
+            },
+            [&](int w, float (*acc)[V], Old &old) {
+                const uint64_t to_row = row(w);
+#pragma unroll
+                for (int p = 0; p < P; p++) {
+                    float y[V];
+#pragma unroll
+                    for (int j = 0; j < V; j++) {
+                        y[j] = a.scale * acc[p][j];
+                        if constexpr (ACC) y[j] += unpack<GT>(old.w[p], j);
+                        y[j] = in_fp32(y[j]);
+                    }
+                    store_cols<GT, V>(to_row + (uint64_t)c.col(p) * kSizeOf<GT>, c.n(p), y);
+                }
+            });
+        return;
+    }
+    down -= a.ranges;
+    if (down < a.fills) {
+        // rows without tokens, of a gradient that is written whole
+        const int row0 = down * kFill;
+        const int s = start_of(a.start, min(row0 + lane, a.vocab)), next = __shfl_down(s, 1);
+        uint64_t empty = __ballot(lane < kFill && row0 + lane < a.vocab && s == next);
+        const float zero[V] = {};
+        while (empty) {
+            const int row = row0 + __ffsll((unsigned long long)empty) - 1;
+            empty &= empty - 1;
+#pragma unroll
+            for (int p = 0; p < P; p++)
+                store_cols<GT, V>(a.grad + (uint64_t)(row * a.ld_grad + c.col(p)) * kSizeOf<GT>, c.n(p), zero);
+        }
+    }
+}
+
+template <int GT, int V> __device__ __forceinline__ void finish_as(const SumArgs &a, int token, int col, int n, const float *acc) {
+    if (n == 0) return;
+    const uint64_t at = a.grad + (uint64_t)(token * a.ld_grad + col) * kSizeOf<GT>;
+    float y[V] = {};
+    if (a.accumulate) load_cols<GT, V>(at, n, y);
+#pragma unroll
+    for (int j = 0; j < V; j++) y[j] = in_fp32(y[j] + a.scale * acc[j]);
+    store_cols<GT, V>(at, n, y);
+}
+
+// One workgroup per chunk and 256 columns; those in whose chunk no long row
 // starts have nothing to do.
-template <int GT> __global__ __launch_bounds__(kJoinWaves * 64) void embedding_join_kernel(SumArgs a) {
-    __shared__ float sums[kJoinWaves][512];
-    const int slabs = (a.cols + 511) / 512;
+__global__ __launch_bounds__(kJoinWaves * 64) void embedding_join_kernel(SumArgs a) {
+    constexpr int V = 4, kAhead = 8;
+    __shared__ float sums[kJoinWaves][64 * V];
+    const int slabs = (a.cols + 64 * V - 1) / (64 * V);
     const int chunk = blockIdx.x / slabs, slab = blockIdx.x % slabs;
     const int token = gmem<const int32_t>(a.head)[chunk];
     if (token < 0) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int col = slab * 512 + lane * 8, cols = max(0, min(8, a.cols - col));
+    const int col = slab * 64 * V + lane * V, cols = max(0, min(V, a.cols - col));
     const int s = start_of(a.start, token), last = (start_of(a.start, token + 1) - 1) / kChunk;
     // wave w adds an eighth of the parts, contiguous, so that the order stays
     const int parts = last - chunk + 1, each = (parts + kJoinWaves - 1) / kJoinWaves;
     const int p0 = min(wave * each, parts), p1 = min(p0 + each, parts);
-    float acc[8] = {};
-    constexpr int kAhead = 4;
+    float acc[V] = {};
     for (int p = p0; p < p1; p += kAhead) {
-        float x[kAhead][8];
+        float x[kAhead][V];
 #pragma unroll
         for (int u = 0; u < kAhead; u++) {
             const int c = chunk + min(p + u, p1 - 1);
             const int slot = c == chunk && s % kChunk != 0 ? 1 : 0;
-            load_cols<QM_F32>(a.part + (((uint64_t)c * 2 + slot) * a.part_ld + col) * 4, cols, x[u]);
+            load_cols<QM_F32, V>(a.part + (((uint64_t)c * 2 + slot) * a.part_ld + col) * 4, cols, x[u]);
         }
 #pragma unroll
         for (int u = 0; u < kAhead; u++)
 #pragma unroll
-            for (int j = 0; j < 8; j++) acc[j] += p + u < p1 ? x[u][j] : 0.0f;
+            for (int j = 0; j < V; j++) acc[j] += p + u < p1 ? x[u][j] : 0.0f;
     }
 #pragma unroll
-    for (int j = 0; j < 8; j++) sums[wave][lane * 8 + j] = acc[j];
+    for (int j = 0; j < V; j++) sums[wave][lane * V + j] = acc[j];
     __syncthreads();
-    if (wave != 0 || !cols) return;
+    if (wave != 0) return;
     for (int w = 1; w < kJoinWaves; w++)
 #pragma unroll
-        for (int j = 0; j < 8; j++) acc[j] += sums[w][lane * 8 + j];
-    finish_row<GT>(a, token, col, cols, acc);
+        for (int j = 0; j < V; j++) acc[j] += sums[w][lane * V + j];
+    if (a.grad_dtype == QM_F32) finish_as<QM_F32, V>(a, token, col, cols, acc);
+    else if (a.grad_dtype == QM_BF16) finish_as<QM_BF16, V>(a, token, col, cols, acc);
+    else finish_as<QM_F16, V>(a, token, col, cols, acc);
 }
 
 // -------------------------------------------------------------------- host
@@ -349,6 +464,11 @@ template <typename F> void with_dtype(int32_t dtype, F f) {
     if (dtype == QM_F32) f(std::integral_constant<int, QM_F32>());
     else if (dtype == QM_BF16) f(std::integral_constant<int, QM_BF16>());
     else f(std::integral_constant<int, QM_F16>());
+}
+
+template <int DT, int GT, int V, int P> void launch_sum(const SumArgs &a, unsigned grid, hipStream_t q) {
+    if (a.accumulate) embedding_sum_kernel<DT, GT, V, P, true><<<grid, kSumWaves * 64, 0, q>>>(a);
+    else embedding_sum_kernel<DT, GT, V, P, false><<<grid, kSumWaves * 64, 0, q>>>(a);
 }
 
 qm_status check_tokens(const void *tokens, int32_t token_bits, int64_t n_tokens, int64_t vocab) {
@@ -394,8 +514,9 @@ extern "C" qm_status embedding_lookup(const void *tokens, int32_t token_bits, in
     s.matrix(table, table_dtype, vocab, cols, ld_table, false);
     s.matrix(out, out_dtype, n_tokens, cols, ld_out, true);
     if (s.clash()) return fail(QM_E_ARG, "out overlaps another buffer");
-    const int64_t pieces = (cols + 7) / 8, each = kLookupThreads * kLookupEach, wgs = (n_tokens * pieces + each - 1) / each;
-    if (wgs >= (int64_t)1 << 24) return fail(QM_E_UNSUPPORTED, "more than 2^34 pieces of 8 columns");
+    const int per = table_dtype == QM_F32 || out_dtype == QM_F32 ? 4 : 8;
+    const int64_t pieces = (cols + per - 1) / per, each = kLookupThreads * kLookupEach, wgs = (n_tokens * pieces + each - 1) / each;
+    if (wgs >= (int64_t)1 << 24) return fail(QM_E_UNSUPPORTED, "more than 2^34 pieces of 4 or 8 columns");
     const LookupArgs a{addr(tokens), addr(table), addr(out), n_tokens, ld_table, ld_out, (int)vocab, (int)cols, (int)pieces,
                        token_bits, scale};
     with_dtype(table_dtype, [&](auto dt) {
@@ -438,33 +559,35 @@ extern "C" qm_status embedding_grad(const void *tokens, int32_t token_bits, int6
     int value_bits = 0;
     while ((1 << value_bits) < values) value_bits++;
     const SortArgs sort{addr(tokens), w + sp.sorted, w + sp.start, (int)n_tokens, (int)vocab, token_bits, values, value_bits};
-    const int lanes = cols <= 64 ? 8 : cols <= 128 ? 16 : cols <= 256 ? 32 : 64;
+    // a unit's columns: 1024, or 256 or 512 where a row is no longer
+    const int v = dy_dtype == QM_F32 || grad_dtype == QM_F32 ? 4 : 8, pieces = cols <= 64 * v ? 1 : 1024 / (64 * v);
+    const int span = 64 * v * pieces;
     SumArgs a{};
     a.sorted = sort.sorted, a.start = sort.start, a.head = w + sp.head, a.part = w + sp.part;
     a.dy = addr(dy), a.grad = addr(grad), a.ld_dy = ld_dy, a.ld_grad = ld_grad;
-    a.vocab = (int)vocab, a.cols = (int)cols, a.n_tokens = (int)n_tokens;
-    a.slabs = (int)((cols + lanes * 8 - 1) / (lanes * 8)), a.part_ld = (int)sp.part_ld;
-    a.chunks = (int)sp.chunks, a.rows = accumulate ? (int)n_tokens : (int)vocab;
-    a.accumulate = accumulate, a.scale = scale;
-    const int64_t units = ((int64_t)a.chunks + a.rows) * a.slabs, each = kSumWaves * 64 / lanes;
-    const int64_t sum_wgs = (units + each - 1) / each, join_wgs = sp.chunks * ((cols + 511) / 512);
-    if (sum_wgs >= (int64_t)1 << 24 || join_wgs >= (int64_t)1 << 23)
-        return fail(QM_E_UNSUPPORTED, "more than 2^32 threads");
+    a.vocab = (int)vocab, a.cols = (int)cols;
+    a.slabs = (int)((cols + span - 1) / span), a.part_ld = (int)sp.part_ld;
+    // positions of a range: 16, or fewer as long as there are less than 4096 units
+    a.range = 16;
+    while (a.range > 1 && n_tokens * a.slabs / a.range < 4096) a.range /= 2;
+    a.chunks = (int)sp.chunks, a.ranges = (int)((n_tokens + a.range - 1) / a.range);
+    a.fills = accumulate ? 0 : (int)((vocab + kFill - 1) / kFill);
+    a.accumulate = accumulate, a.grad_dtype = grad_dtype, a.scale = scale;
+    const int64_t units = ((int64_t)a.chunks + a.ranges + a.fills) * a.slabs, join_wgs = sp.chunks * ((cols + 255) / 256);
+    if (units >= (int64_t)1 << 25 || join_wgs >= (int64_t)1 << 22) return fail(QM_E_UNSUPPORTED, "more than 2^31 threads");
+    const unsigned sum_wgs = (unsigned)((units + kSumWaves - 1) / kSumWaves);
     const hipStream_t q = static_cast<hipStream_t>(stream);
     embedding_sort_kernel<<<(unsigned)((vocab + values - 1) / values), kSortWaves * 64, 0, q>>>(sort);
     if (qm_status e = launch_status("embedding_grad")) return e;
     with_dtype(dy_dtype, [&](auto dt) {
         with_dtype(grad_dtype, [&](auto gt) {
-            constexpr int DT = decltype(dt)::value, GT = decltype(gt)::value;
-            const unsigned grid = (unsigned)sum_wgs;
-            if (lanes == 8) embedding_sum_kernel<DT, GT, 8><<<grid, kSumWaves * 64, 0, q>>>(a);
-            else if (lanes == 16) embedding_sum_kernel<DT, GT, 16><<<grid, kSumWaves * 64, 0, q>>>(a);
-            else if (lanes == 32) embedding_sum_kernel<DT, GT, 32><<<grid, kSumWaves * 64, 0, q>>>(a);
-            else embedding_sum_kernel<DT, GT, 64><<<grid, kSumWaves * 64, 0, q>>>(a);
+            constexpr int DT = decltype(dt)::value, GT = decltype(gt)::value, V = DT == QM_F32 || GT == QM_F32 ? 4 : 8;
+            if (pieces == 1) launch_sum<DT, GT, V, 1>(a, sum_wgs, q);
+            else launch_sum<DT, GT, V, 1024 / (64 * V)>(a, sum_wgs, q);
         });
     });
     if (qm_status e = launch_status("embedding_grad")) return e;
     if (join_wgs == 0) return QM_OK;
-    with_dtype(grad_dtype, [&](auto gt) { embedding_join_kernel<decltype(gt)::value><<<(unsigned)join_wgs, kJoinWaves * 64, 0, q>>>(a); });
+    embedding_join_kernel<<<(unsigned)join_wgs, kJoinWaves * 64, 0, q>>>(a);
     return launch_status("embedding_grad");
 }
