@@ -18,7 +18,7 @@
 //   sum    A wave takes the rows that start in a range of 16 positions of the
 //          order (per 1024 columns) and runs through their tokens, several rows
 //          of dy in flight whichever row of the table they go to.  Rows of more
-//          than 64 tokens are cut where multiples of 64 positions lie: a cut
+//          than 32 tokens are cut where multiples of 32 positions lie: a cut
 //          part is summed by one wave into the workspace.  A gradient that is
 //          written whole also gets its zeros here, one that is added to is
 //          touched in rows that have tokens.
@@ -32,7 +32,7 @@
 namespace qm {
 namespace {
 
-constexpr int kChunk = 64;        // positions of a part, and the longest row without parts
+constexpr int kChunk = 32;        // positions of a part, and the longest row without parts
 constexpr int kSortWaves = 16, kSortValues = 1024;
 constexpr int kSumWaves = 4, kJoinWaves = 8;
 constexpr int kFill = 16;         // rows that a wave looks at for empty ones
@@ -142,20 +142,36 @@ __global__ __launch_bounds__(kSortWaves * 64) void embedding_sort_kernel(SortArg
     const int begin = min(wave * share, a.n), end = min(begin + share, a.n);
     int32_t *mine = count + wave * a.values;
 
-    constexpr int kAhead = 16;   // tokens of a lane in flight
-    int less = 0;                // of the wave
-    for (int c = begin; c < end; c += 64 * kAhead) {
-        uint32_t t[kAhead];
+    // A lane's tokens, 16 in flight; the first 32 (all of them up to 32768
+    // tokens) stay in registers for the second time.
+    constexpr int kAhead = 16, kHeld = 32;
+    uint32_t held[kHeld];
+    auto load = [&](int c, uint32_t *t) {
 #pragma unroll
         for (int k = 0; k < kAhead; k++) {
             const int i = c + k * 64 + lane;
             t[k] = i < end ? token32_at(a.tokens, a.token_bits, i) : 0xffffffffu;
         }
+    };
+    int less = 0;                // of the wave
+    auto tally = [&](const uint32_t *t) {
 #pragma unroll
         for (int k = 0; k < kAhead; k++) {
             less += __popcll(__ballot(t[k] < (uint32_t)lo));
             if (t[k] - lo < (uint32_t)values) atomicAdd(&mine[t[k] - lo], 1);
         }
+    };
+    constexpr int kBatch = 64 * kAhead;
+#pragma unroll
+    for (int h = 0; h < kHeld; h += kAhead) {
+        if (begin + h * 64 >= end) break;
+        load(begin + h * 64, held + h);
+        tally(held + h);
+    }
+    for (int c = begin + kHeld * 64; c < end; c += kBatch) {
+        uint32_t t[kAhead];
+        load(c, t);
+        tally(t);
     }
     if (lane == 0) wave_less[wave] = less;
     __syncthreads();
@@ -188,22 +204,25 @@ __global__ __launch_bounds__(kSortWaves * 64) void embedding_sort_kernel(SortArg
     if (threadIdx.x == 0 && lo + values == a.vocab) gmem<int32_t>(a.start)[a.vocab] = all;
     __syncthreads();
 
-    for (int c = begin; c < end; c += 64 * kAhead) {
-        uint32_t t[kAhead];
-#pragma unroll
-        for (int k = 0; k < kAhead; k++) {
-            const int i = c + k * 64 + lane;
-            t[k] = i < end ? token32_at(a.tokens, a.token_bits, i) : 0xffffffffu;
-        }
+    auto place = [&](int c, const uint32_t *t) {
 #pragma unroll
         for (int k = 0; k < kAhead; k++) {
             const bool in = t[k] - lo < (uint32_t)values;
             uint64_t same = __ballot(in);
             if (same == 0) continue;
-            const int value = in ? (int)(t[k] - lo) : 0;
-            for (int b = 0; b < a.value_bits; b++) {
-                const uint64_t set = __ballot(value >> b & 1);
-                same &= value >> b & 1 ? set : ~set;
+            const int value = in ? (int)(t[k] - lo) : -1;
+            if (__popcll(same) > a.value_bits) {
+                for (int b = 0; b < a.value_bits; b++) {
+                    const uint64_t set = __ballot(value >> b & 1);
+                    same &= value >> b & 1 ? set : ~set;
+                }
+            } else {
+                // few: one ballot for each value that is there
+                for (uint64_t left = same; left;) {
+                    const uint64_t these = __ballot(value == __builtin_amdgcn_readlane(value, __ffsll((unsigned long long)left) - 1));
+                    same = these >> lane & 1 ? these : same;
+                    left &= ~these;
+                }
             }
             if (in) {
                 const int before = __popcll(same & ((1ull << lane) - 1)), next = mine[value];
@@ -211,6 +230,16 @@ __global__ __launch_bounds__(kSortWaves * 64) void embedding_sort_kernel(SortArg
                 gmem<Sorted>(a.sorted)[next + before] = Sorted{(int32_t)t[k], c + k * 64 + lane};
             }
         }
+    };
+#pragma unroll
+    for (int h = 0; h < kHeld; h += kAhead) {
+        if (begin + h * 64 >= end) break;
+        place(begin + h * 64, held + h);
+    }
+    for (int c = begin + kHeld * 64; c < end; c += kBatch) {
+        uint32_t t[kAhead];
+        load(c, t);
+        place(c, t);
     }
 }
 
