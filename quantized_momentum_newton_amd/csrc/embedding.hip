@@ -34,7 +34,7 @@ namespace {
 
 constexpr int kChunk = 32;        // positions of a part, and the longest row without parts
 constexpr int kSortWaves = 16, kSortValues = 1024;
-constexpr int kSumWaves = 4, kJoinWaves = 8;
+constexpr int kSumWaves = 4, kJoinWaves = 8, kJoinChunks = 8;
 constexpr int kFill = 16;         // rows that a wave looks at for empty ones
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;     // tokens, and values: their counts stay 32-bit numbers
 
@@ -332,6 +332,7 @@ __device__ __forceinline__ void stream(const SumArgs &a, const int *pos, int fro
 }
 
 struct Nothing {};
+template <int N> using zeros_t = unsigned __attribute__((ext_vector_type(N), aligned(1)));
 
 template <int DT, int GT, int V, int P, bool ACC> __global__ __launch_bounds__(kSumWaves * 64) void embedding_sum_kernel(SumArgs a) {
     const int lane = threadIdx.x & 63;
@@ -427,9 +428,12 @@ template <int DT, int GT, int V, int P, bool ACC> __global__ __launch_bounds__(k
         while (empty) {
             const int row = row0 + __ffsll((unsigned long long)empty) - 1;
             empty &= empty - 1;
+            const uint64_t to = a.grad + (uint64_t)(row * a.ld_grad) * kSizeOf<GT>;
 #pragma unroll
-            for (int p = 0; p < P; p++)
-                store_cols<GT, V>(a.grad + (uint64_t)(row * a.ld_grad + c.col(p)) * kSizeOf<GT>, c.n(p), zero);
+            for (int p = 0; p < P; p++) {
+                if (c.n(p) == V) *reinterpret_cast<zeros_t<V * kSizeOf<GT> / 4> *>(gmem<char>(to) + (int64_t)c.col(p) * kSizeOf<GT>) = 0;
+                else store_cols<GT, V>(to + (uint64_t)c.col(p) * kSizeOf<GT>, c.n(p), zero);
+            }
         }
     }
 }
@@ -444,45 +448,48 @@ template <int GT, int V> __device__ __forceinline__ void finish_as(const SumArgs
     store_cols<GT, V>(at, n, y);
 }
 
-// One workgroup per chunk and 256 columns; those in whose chunk no long row
-// starts have nothing to do.
+// One workgroup per eight chunks and 256 columns: the long rows that start in
+// those chunks, one after the other.
 __global__ __launch_bounds__(kJoinWaves * 64) void embedding_join_kernel(SumArgs a) {
     constexpr int V = 4, kAhead = 8;
     __shared__ float sums[kJoinWaves][64 * V];
     const int slabs = (a.cols + 64 * V - 1) / (64 * V);
-    const int chunk = blockIdx.x / slabs, slab = blockIdx.x % slabs;
-    const int token = gmem<const int32_t>(a.head)[chunk];
-    if (token < 0) return;
+    const int chunk0 = blockIdx.x / slabs * kJoinChunks, slab = blockIdx.x % slabs;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int col = slab * 64 * V + lane * V, cols = max(0, min(V, a.cols - col));
-    const int s = start_of(a.start, token), last = (start_of(a.start, token + 1) - 1) / kChunk;
-    // wave w adds an eighth of the parts, contiguous, so that the order stays
-    const int parts = last - chunk + 1, each = (parts + kJoinWaves - 1) / kJoinWaves;
-    const int p0 = min(wave * each, parts), p1 = min(p0 + each, parts);
-    float acc[V] = {};
-    for (int p = p0; p < p1; p += kAhead) {
-        float x[kAhead][V];
+    const int head = lane < min(kJoinChunks, a.chunks - chunk0) ? gmem<const int32_t>(a.head)[chunk0 + lane] : -1;
+    for (uint64_t left = __ballot(head >= 0); left; left &= left - 1) {
+        const int k = __ffsll((unsigned long long)left) - 1, chunk = chunk0 + k, token = __builtin_amdgcn_readlane(head, k);
+        const int s = start_of(a.start, token), last = (start_of(a.start, token + 1) - 1) / kChunk;
+        // wave w adds an eighth of the parts, contiguous, so that the order stays
+        const int parts = last - chunk + 1, each = (parts + kJoinWaves - 1) / kJoinWaves;
+        const int p0 = min(wave * each, parts), p1 = min(p0 + each, parts);
+        float acc[V] = {};
+        for (int p = p0; p < p1; p += kAhead) {
+            float x[kAhead][V];
 #pragma unroll
-        for (int u = 0; u < kAhead; u++) {
-            const int c = chunk + min(p + u, p1 - 1);
-            const int slot = c == chunk && s % kChunk != 0 ? 1 : 0;
-            load_cols<QM_F32, V>(a.part + (((uint64_t)c * 2 + slot) * a.part_ld + col) * 4, cols, x[u]);
+            for (int u = 0; u < kAhead; u++) {
+                const int c = chunk + min(p + u, p1 - 1);
+                const int slot = c == chunk && s % kChunk != 0 ? 1 : 0;
+                load_cols<QM_F32, V>(a.part + (((uint64_t)c * 2 + slot) * a.part_ld + col) * 4, cols, x[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; u++)
+#pragma unroll
+                for (int j = 0; j < V; j++) acc[j] += p + u < p1 ? x[u][j] : 0.0f;
         }
+        __syncthreads();      // the row before has been read
 #pragma unroll
-        for (int u = 0; u < kAhead; u++)
+        for (int j = 0; j < V; j++) sums[wave][lane * V + j] = acc[j];
+        __syncthreads();
+        if (wave != 0) continue;
+        for (int w = 1; w < kJoinWaves; w++)
 #pragma unroll
-            for (int j = 0; j < V; j++) acc[j] += p + u < p1 ? x[u][j] : 0.0f;
+            for (int j = 0; j < V; j++) acc[j] += sums[w][lane * V + j];
+        if (a.grad_dtype == QM_F32) finish_as<QM_F32, V>(a, token, col, cols, acc);
+        else if (a.grad_dtype == QM_BF16) finish_as<QM_BF16, V>(a, token, col, cols, acc);
+        else finish_as<QM_F16, V>(a, token, col, cols, acc);
     }
-#pragma unroll
-    for (int j = 0; j < V; j++) sums[wave][lane * V + j] = acc[j];
-    __syncthreads();
-    if (wave != 0) return;
-    for (int w = 1; w < kJoinWaves; w++)
-#pragma unroll
-        for (int j = 0; j < V; j++) acc[j] += sums[w][lane * V + j];
-    if (a.grad_dtype == QM_F32) finish_as<QM_F32, V>(a, token, col, cols, acc);
-    else if (a.grad_dtype == QM_BF16) finish_as<QM_BF16, V>(a, token, col, cols, acc);
-    else finish_as<QM_F16, V>(a, token, col, cols, acc);
 }
 
 // -------------------------------------------------------------------- host
@@ -602,7 +609,7 @@ extern "C" qm_status embedding_grad(const void *tokens, int32_t token_bits, int6
     a.chunks = (int)sp.chunks, a.ranges = (int)((n_tokens + a.range - 1) / a.range);
     a.fills = accumulate ? 0 : (int)((vocab + kFill - 1) / kFill);
     a.accumulate = accumulate, a.grad_dtype = grad_dtype, a.scale = scale;
-    const int64_t units = ((int64_t)a.chunks + a.ranges + a.fills) * a.slabs, join_wgs = sp.chunks * ((cols + 255) / 256);
+    const int64_t units = ((int64_t)a.chunks + a.ranges + a.fills) * a.slabs, join_wgs = (sp.chunks + kJoinChunks - 1) / kJoinChunks * ((cols + 255) / 256);
     if (units >= (int64_t)1 << 25 || join_wgs >= (int64_t)1 << 22) return fail(QM_E_UNSUPPORTED, "more than 2^31 threads");
     const unsigned sum_wgs = (unsigned)((units + kSumWaves - 1) / kSumWaves);
     const hipStream_t q = static_cast<hipStream_t>(stream);
