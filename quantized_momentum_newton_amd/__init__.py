@@ -790,18 +790,25 @@ def _space(ws, nbytes, device, stream):
     return (None, 0, ws) if ws is None else (ws.data_ptr(), ws.nbytes, ws)
 
 
+def _kept_ld(cols):
+    """Row length of new checkpoints: a multiple of 16, and of a cache line
+    where that adds little."""
+    return -(-cols // 128) * 128 if cols >= 512 else -(-cols // 16) * 16
+
+
 class ActCheckpoint:
     """A rows x cols activation in 8 bits (the layout of qm_act8): data uint8
     (E4M3) [rows, ld], scale uint8 (E8M0) [ceil(rows / 32), ld], ld the columns
-    rounded up to a multiple of 16.  Buffers that are given are used as they
-    are, their row length being ld."""
+    rounded up to a multiple of 16 (of 128 from 512 columns on).  Buffers that
+    are given are used as they are, their row length, a multiple of 16, being
+    ld."""
 
     def __init__(self, rows, cols, device="cuda", data=None, scale=None):
         if rows < 0 or cols < 0:
             raise ValueError(f"bad size {rows} x {cols}")
         given = data if data is not None else scale
         home = given.device if given is not None else torch.device(device)
-        ld = given.shape[-1] if given is not None else -(-cols // 16) * 16
+        ld = given.shape[-1] if given is not None else _kept_ld(cols)
         groups = -(-rows // GROUP_ROWS)
         if data is None:
             data = torch.empty((rows, ld), dtype=torch.uint8, device=home)
@@ -824,7 +831,7 @@ class ActCheckpoint:
 def _kept(ckpt, name, shape, device, stream):
     """ckpt, checked, or a new one for None."""
     if ckpt is None:
-        ld = -(-shape[1] // 16) * 16
+        ld = _kept_ld(shape[1])
         return ActCheckpoint(*shape, data=_alloc((shape[0], ld), torch.uint8, device, stream),
                              scale=_alloc((-(-shape[0] // GROUP_ROWS), ld), torch.uint8, device, stream))
     if not isinstance(ckpt, ActCheckpoint):

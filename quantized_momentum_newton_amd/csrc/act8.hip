@@ -37,20 +37,21 @@ struct PackArgs {
     int patches, across;
 };
 
-template <int DT> __global__ __launch_bounds__(kWaves * 64) void act_pack_kernel(PackArgs a) {
+// LINES: the rows that are written start on cache lines.
+template <int DT, bool LINES> __global__ __launch_bounds__(kWaves * 64) void act_pack_kernel(PackArgs a) {
     const int patch = wave_patch();
     if (patch >= a.patches) return;
-    const Patch p(a.rows, a.cols, patch, a.across, threadIdx.x % 64);
+    const Patch<DT> p(a.rows, a.cols, patch, a.across, threadIdx.x % 64);
     PackedOf<DT, 8> r[kLaneRows];
 #pragma unroll
     for (int i = 0; i < kLaneRows; i++) r[i] = patch_load<DT>(a.x, a.ld, p, i);
-    encode(p, [&](int i, int j) { return unpack<DT>(r[i], j); }, a.data, a.scale, a.ld8);
+    encode<LINES>(p, [&](int i, int j) { return unpack<DT>(r[i], j); }, a.data, a.scale, a.ld8);
 }
 
-template <int DT> __global__ __launch_bounds__(kWaves * 64) void act_read_kernel(PackArgs a) {
+template <int DT, bool LINES> __global__ __launch_bounds__(kWaves * 64) void act_read_kernel(PackArgs a) {
     const int patch = wave_patch();
     if (patch >= a.patches) return;
-    const Patch p(a.rows, a.cols, patch, a.across, threadIdx.x % 64);
+    const Patch<DT> p(a.rows, a.cols, patch, a.across, threadIdx.x % 64);
     Packed<8> w[kLaneRows];
 #pragma unroll
     for (int i = 0; i < kLaneRows; i++) w[i] = load_codes(p, a.data, a.ld8, i);
@@ -60,7 +61,7 @@ template <int DT> __global__ __launch_bounds__(kWaves * 64) void act_read_kernel
     for (int i = 0; i < kLaneRows; i++) {
         float x[8];
         decode(w[i], unit, x);
-        patch_store<DT>(a.x, a.ld, p, i, x);
+        patch_store<LINES>(a.x, a.ld, p, i, x);
     }
 }
 
@@ -107,10 +108,10 @@ struct GatedArgs {
     int patches, across;
 };
 
-template <int DT, int ACT> __global__ __launch_bounds__(kWaves * 64) void gated_forward_kernel(GatedArgs a) {
+template <int DT, int ACT, bool LINES> __global__ __launch_bounds__(kWaves * 64) void gated_forward_kernel(GatedArgs a) {
     const int patch = wave_patch();
     if (patch >= a.patches) return;
-    const Patch p(a.rows, a.cols, patch, a.across, threadIdx.x % 64);
+    const Patch<DT> p(a.rows, a.cols, patch, a.across, threadIdx.x % 64);
     PackedOf<DT, 8> g[kLaneRows], u[kLaneRows];
 #pragma unroll
     for (int i = 0; i < kLaneRows; i++) {
@@ -122,18 +123,18 @@ template <int DT, int ACT> __global__ __launch_bounds__(kWaves * 64) void gated_
         float h[8];
 #pragma unroll
         for (int j = 0; j < 8; j++) h[j] = in_fp32(act_value<ACT, DT != QM_F32>(unpack<DT>(g[i], j)) * unpack<DT>(u[i], j));
-        patch_store<DT>(a.h, a.ld_h, p, i, h);
+        patch_store<LINES>(a.h, a.ld_h, p, i, h);
     }
     if (a.gate_data) {
-        encode(p, [&](int i, int j) { return unpack<DT>(g[i], j); }, a.gate_data, a.gate_scale, a.ld_gate8);
-        encode(p, [&](int i, int j) { return unpack<DT>(u[i], j); }, a.up_data, a.up_scale, a.ld_up8);
+        encode<LINES>(p, [&](int i, int j) { return unpack<DT>(g[i], j); }, a.gate_data, a.gate_scale, a.ld_gate8);
+        encode<LINES>(p, [&](int i, int j) { return unpack<DT>(u[i], j); }, a.up_data, a.up_scale, a.ld_up8);
     }
 }
 
-template <int DT, int ACT> __global__ __launch_bounds__(kWaves * 64) void gated_backward_kernel(GatedArgs a) {
+template <int DT, int ACT, bool LINES> __global__ __launch_bounds__(kWaves * 64) void gated_backward_kernel(GatedArgs a) {
     const int patch = wave_patch();
     if (patch >= a.patches) return;
-    const Patch p(a.rows, a.cols, patch, a.across, threadIdx.x % 64);
+    const Patch<DT> p(a.rows, a.cols, patch, a.across, threadIdx.x % 64);
     Packed<8> g8[kLaneRows], u8[kLaneRows];
     PackedOf<DT, 8> d[kLaneRows];
     float gs[8], us[8];
@@ -158,9 +159,9 @@ template <int DT, int ACT> __global__ __launch_bounds__(kWaves * 64) void gated_
             du[j] = in_fp32(dh * v);
             h[j] = in_fp32(v * u[j]);
         }
-        patch_store<DT>(a.gate, a.ld_gate, p, i, dg);
-        patch_store<DT>(a.up, a.ld_up, p, i, du);
-        if (a.h) patch_store<DT>(a.h, a.ld_h, p, i, h);
+        patch_store<LINES>(a.gate, a.ld_gate, p, i, dg);
+        patch_store<LINES>(a.up, a.ld_up, p, i, du);
+        if (a.h) patch_store<LINES>(a.h, a.ld_h, p, i, h);
     }
 }
 
@@ -178,11 +179,18 @@ qm_status patch_grid(int64_t rows, int64_t cols, int &patches, int &across) {
 unsigned wgs(int patches) { return (unsigned)((patches + kWaves - 1) / kWaves); }
 uint64_t addr(const void *p) { return (uint64_t)(uintptr_t)p; }
 
-// Calls f with the type as a constant.
-template <typename F> void with_dtype(int32_t dtype, F f) {
-    if (dtype == QM_F32) f(std::integral_constant<int, QM_F32>());
-    else if (dtype == QM_BF16) f(std::integral_constant<int, QM_BF16>());
-    else f(std::integral_constant<int, QM_F16>());
+// Whether every row starts on a cache line.
+bool on_lines(const void *p, int64_t pitch_bytes) { return aligned(p, 128) && pitch_bytes % 128 == 0; }
+
+// Calls f with the type and with `lines` as constants.
+template <typename F> void with_kind(int32_t dtype, bool lines, F f) {
+    auto as = [&](auto l) {
+        if (dtype == QM_F32) f(std::integral_constant<int, QM_F32>(), l);
+        else if (dtype == QM_BF16) f(std::integral_constant<int, QM_BF16>(), l);
+        else f(std::integral_constant<int, QM_F16>(), l);
+    };
+    if (lines) as(std::true_type());
+    else as(std::false_type());
 }
 
 }  // namespace
@@ -203,8 +211,8 @@ extern "C" qm_status act_pack(const void *x, int32_t dtype, int64_t ld, const qm
     if (s.clash()) return fail(QM_E_ARG, "x and kept overlap");
     PackArgs a{addr(x), addr(kept->data), addr(kept->scale), rows, cols, ld, kept->ld, 0, 0};
     if (qm_status e = patch_grid(rows, cols, a.patches, a.across)) return e;
-    with_dtype(dtype, [&](auto dt) {
-        act_pack_kernel<decltype(dt)::value><<<wgs(a.patches), kWaves * 64, 0, static_cast<hipStream_t>(stream)>>>(a);
+    with_kind(dtype, on_lines(kept->data, kept->ld), [&](auto dt, auto lines) {
+        act_pack_kernel<decltype(dt)::value, decltype(lines)::value><<<wgs(a.patches), kWaves * 64, 0, static_cast<hipStream_t>(stream)>>>(a);
     });
     return launch_status("act_pack");
 }
@@ -222,8 +230,8 @@ extern "C" qm_status act_read(const qm_act8 *kept, void *out, int32_t dtype, int
     if (s.clash()) return fail(QM_E_ARG, "out and kept overlap");
     PackArgs a{addr(out), addr(kept->data), addr(kept->scale), rows, cols, ld, kept->ld, 0, 0};
     if (qm_status e = patch_grid(rows, cols, a.patches, a.across)) return e;
-    with_dtype(dtype, [&](auto dt) {
-        act_read_kernel<decltype(dt)::value><<<wgs(a.patches), kWaves * 64, 0, static_cast<hipStream_t>(stream)>>>(a);
+    with_kind(dtype, on_lines(out, ld * elem_size(dtype)), [&](auto dt, auto lines) {
+        act_read_kernel<decltype(dt)::value, decltype(lines)::value><<<wgs(a.patches), kWaves * 64, 0, static_cast<hipStream_t>(stream)>>>(a);
     });
     return launch_status("act_read");
 }
@@ -258,10 +266,12 @@ extern "C" qm_status gated_act_forward(const void *gate, int64_t ld_gate, const 
     }
     if (qm_status e = patch_grid(rows, cols, a.patches, a.across)) return e;
     const hipStream_t q = static_cast<hipStream_t>(stream);
-    with_dtype(dtype, [&](auto dt) {
+    const bool on = on_lines(h, ld_h * elem_size(dtype)) && (!gate8 || (on_lines(gate8->data, gate8->ld) && on_lines(up8->data, up8->ld)));
+    with_kind(dtype, on, [&](auto dt, auto lines) {
         constexpr int DT = decltype(dt)::value;
-        if (act == kSilu) gated_forward_kernel<DT, kSilu><<<wgs(a.patches), kWaves * 64, 0, q>>>(a);
-        else gated_forward_kernel<DT, kGelu><<<wgs(a.patches), kWaves * 64, 0, q>>>(a);
+        constexpr bool LINES = decltype(lines)::value;
+        if (act == kSilu) gated_forward_kernel<DT, kSilu, LINES><<<wgs(a.patches), kWaves * 64, 0, q>>>(a);
+        else gated_forward_kernel<DT, kGelu, LINES><<<wgs(a.patches), kWaves * 64, 0, q>>>(a);
     });
     return launch_status("gated_act_forward");
 }
@@ -296,10 +306,13 @@ extern "C" qm_status gated_act_backward(const qm_act8 *gate8, const qm_act8 *up8
     a.rows = rows, a.cols = cols, a.ld_gate = ld_dgate, a.ld_up = ld_dup, a.ld_h = ld_h, a.ld_dh = ld_dh;
     if (qm_status e = patch_grid(rows, cols, a.patches, a.across)) return e;
     const hipStream_t q = static_cast<hipStream_t>(stream);
-    with_dtype(dtype, [&](auto dt) {
+    const int64_t size = elem_size(dtype);
+    const bool on = on_lines(dgate, ld_dgate * size) && on_lines(dup, ld_dup * size) && (!h || on_lines(h, ld_h * size));
+    with_kind(dtype, on, [&](auto dt, auto lines) {
         constexpr int DT = decltype(dt)::value;
-        if (act == kSilu) gated_backward_kernel<DT, kSilu><<<wgs(a.patches), kWaves * 64, 0, q>>>(a);
-        else gated_backward_kernel<DT, kGelu><<<wgs(a.patches), kWaves * 64, 0, q>>>(a);
+        constexpr bool LINES = decltype(lines)::value;
+        if (act == kSilu) gated_backward_kernel<DT, kSilu, LINES><<<wgs(a.patches), kWaves * 64, 0, q>>>(a);
+        else gated_backward_kernel<DT, kGelu, LINES><<<wgs(a.patches), kWaves * 64, 0, q>>>(a);
     });
     return launch_status("gated_act_backward");
 }
