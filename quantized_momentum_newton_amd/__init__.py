@@ -764,16 +764,19 @@ def _matrix(t, name, device=None, shape=None, dtype=None):
     """(address, qm_dtype, row pitch) of a 2-D tensor with unit column stride."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions, not {t.dim()}")
-    rows, cols = t.shape
-    code = _DTYPES.get(t.dtype)
-    if code is None or (dtype is not None and t.dtype != dtype):
-        raise TypeError(f"{name} is {t.dtype}" + (f", expected {dtype}" if dtype is not None else ", which is not supported"))
+    size, dt = t.shape, t.dtype
+    if len(size) != 2:
+        raise ValueError(f"{name} must have two dimensions, not {len(size)}")
+    code = _DTYPES.get(dt)
+    if code is None or (dtype is not None and dt != dtype):
+        raise TypeError(f"{name} is {dt}" + (f", expected {dtype}" if dtype is not None else ", which is not supported"))
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if shape is not None and (rows, cols) != shape:
-        raise ValueError(f"{name} has shape {(rows, cols)}, expected {shape}")
+    if shape is not None and size != shape:
+        raise ValueError(f"{name} has shape {tuple(size)}, expected {tuple(shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), code, size[1]
+    rows, cols = size
     ld = t.stride(0) if rows > 1 else cols
     if (cols > 1 and t.stride(1) != 1) or ld < cols:
         raise ValueError(f"{name} needs unit column stride and rows that do not overlap")
@@ -803,37 +806,60 @@ class ActCheckpoint:
     are given are used as they are, their row length, a multiple of 16, being
     ld."""
 
+    __slots__ = ("rows", "cols", "shape", "device", "c", "_both", "_data", "_scale")
+
     def __init__(self, rows, cols, device="cuda", data=None, scale=None):
         if rows < 0 or cols < 0:
             raise ValueError(f"bad size {rows} x {cols}")
-        given = data if data is not None else scale
-        home = given.device if given is not None else torch.device(device)
-        ld = given.shape[-1] if given is not None else _kept_ld(cols)
+        if data is None and scale is None:
+            self._own(rows, cols, torch.device(device), None)
+            return
+        home, ld = (data if data is not None else scale).device, (data if data is not None else scale).shape[-1]
         groups = -(-rows // GROUP_ROWS)
         if data is None:
             data = torch.empty((rows, ld), dtype=torch.uint8, device=home)
-            home = data.device      # with its index
         if scale is None:
             scale = torch.empty((groups, ld), dtype=torch.uint8, device=home)
         _require(data, "data", torch.uint8, home, shape=(rows, ld))
         _require(scale, "scale", torch.uint8, home, shape=(groups, ld))
         if ld % 16 or ld < cols:
             raise ValueError(f"rows of {ld} bytes: a multiple of 16 that holds {cols} columns is needed")
-        self.rows, self.cols, self.data, self.scale, self.device = rows, cols, data, scale, data.device
-        self.shape = (rows, cols)
+        self.rows, self.cols, self.shape, self.device = rows, cols, (rows, cols), home
+        self._both, self._data, self._scale = None, data, scale
         self.c = L.Act8(data.data_ptr(), scale.data_ptr(), rows, cols, ld)
+
+    def _own(self, rows, cols, device, stream):
+        """New buffers, in one allocation."""
+        ld = _kept_ld(cols)
+        both = _alloc((rows + -(-rows // GROUP_ROWS), ld), torch.uint8, device, stream)
+        self.rows, self.cols, self.shape, self.device = rows, cols, (rows, cols), both.device
+        self._both, self._data, self._scale = both, None, None
+        at = both.data_ptr()
+        self.c = L.Act8(at, at + rows * ld, rows, cols, ld)
+
+    @property
+    def data(self):
+        if self._data is None:
+            self._data = self._both[:self.rows]
+        return self._data
+
+    @property
+    def scale(self):
+        if self._scale is None:
+            self._scale = self._both[self.rows:]
+        return self._scale
 
     @property
     def nbytes(self):
-        return self.data.nbytes + self.scale.nbytes
+        return self._both.nbytes if self._both is not None else self._data.nbytes + self._scale.nbytes
 
 
 def _kept(ckpt, name, shape, device, stream):
     """ckpt, checked, or a new one for None."""
     if ckpt is None:
-        ld = _kept_ld(shape[1])
-        return ActCheckpoint(*shape, data=_alloc((shape[0], ld), torch.uint8, device, stream),
-                             scale=_alloc((-(-shape[0] // GROUP_ROWS), ld), torch.uint8, device, stream))
+        ckpt = ActCheckpoint.__new__(ActCheckpoint)
+        ckpt._own(*shape, device, stream)
+        return ckpt
     if not isinstance(ckpt, ActCheckpoint):
         raise TypeError(f"{name} must be an ActCheckpoint")
     if ckpt.shape != shape:

@@ -19,6 +19,8 @@
 
 #include "act8_device.h"
 #include "act_host.h"
+#include "cu_share.h"
+#include "reserve_lds.h"
 
 namespace qm {
 namespace {
@@ -45,7 +47,7 @@ template <int DT, bool LINES> __global__ __launch_bounds__(kWaves * 64) void act
     PackedOf<DT, 8> r[kLaneRows];
 #pragma unroll
     for (int i = 0; i < kLaneRows; i++) r[i] = patch_load<DT>(a.x, a.ld, p, i);
-    encode<LINES>(p, [&](int i, int j) { return unpack<DT>(r[i], j); }, a.data, a.scale, a.ld8);
+    encode<LINES>(p, r, a.data, a.scale, a.ld8);
 }
 
 template <int DT, bool LINES> __global__ __launch_bounds__(kWaves * 64) void act_read_kernel(PackArgs a) {
@@ -126,8 +128,10 @@ template <int DT, int ACT, bool LINES> __global__ __launch_bounds__(kWaves * 64)
         patch_store<LINES>(a.h, a.ld_h, p, i, h);
     }
     if (a.gate_data) {
-        encode<LINES>(p, [&](int i, int j) { return unpack<DT>(g[i], j); }, a.gate_data, a.gate_scale, a.ld_gate8);
-        encode<LINES>(p, [&](int i, int j) { return unpack<DT>(u[i], j); }, a.up_data, a.up_scale, a.ld_up8);
+        unpack_anew(g);
+        unpack_anew(u);
+        encode<LINES>(p, g, a.gate_data, a.gate_scale, a.ld_gate8);
+        encode<LINES>(p, u, a.up_data, a.up_scale, a.ld_up8);
     }
 }
 
@@ -176,6 +180,11 @@ qm_status patch_grid(int64_t rows, int64_t cols, int &patches, int &across) {
     across = (int)a;
     return QM_OK;
 }
+// Workgroups a CU, of those that fit (us, 8192 x 14336 bf16): pack 58.4 with
+// all (7), 56.7 with 4; read 60.2 (8), 57.5 (3); forward 162.1 (4), 157.6 (3);
+// backward 211.7 (4), 202.1 (2).
+constexpr unsigned kPackShare = wgs_per_cu(4), kReadShare = wgs_per_cu(3), kForwardShare = wgs_per_cu(3), kBackwardShare = wgs_per_cu(2);
+
 unsigned wgs(int patches) { return (unsigned)((patches + kWaves - 1) / kWaves); }
 uint64_t addr(const void *p) { return (uint64_t)(uintptr_t)p; }
 
@@ -212,7 +221,7 @@ extern "C" qm_status act_pack(const void *x, int32_t dtype, int64_t ld, const qm
     PackArgs a{addr(x), addr(kept->data), addr(kept->scale), rows, cols, ld, kept->ld, 0, 0};
     if (qm_status e = patch_grid(rows, cols, a.patches, a.across)) return e;
     with_kind(dtype, on_lines(kept->data, kept->ld), [&](auto dt, auto lines) {
-        act_pack_kernel<decltype(dt)::value, decltype(lines)::value><<<wgs(a.patches), kWaves * 64, 0, static_cast<hipStream_t>(stream)>>>(a);
+        act_pack_kernel<decltype(dt)::value, decltype(lines)::value><<<wgs(a.patches), kWaves * 64, kPackShare, static_cast<hipStream_t>(stream)>>>(a);
     });
     return launch_status("act_pack");
 }
@@ -231,7 +240,7 @@ extern "C" qm_status act_read(const qm_act8 *kept, void *out, int32_t dtype, int
     PackArgs a{addr(out), addr(kept->data), addr(kept->scale), rows, cols, ld, kept->ld, 0, 0};
     if (qm_status e = patch_grid(rows, cols, a.patches, a.across)) return e;
     with_kind(dtype, on_lines(out, ld * elem_size(dtype)), [&](auto dt, auto lines) {
-        act_read_kernel<decltype(dt)::value, decltype(lines)::value><<<wgs(a.patches), kWaves * 64, 0, static_cast<hipStream_t>(stream)>>>(a);
+        act_read_kernel<decltype(dt)::value, decltype(lines)::value><<<wgs(a.patches), kWaves * 64, kReadShare, static_cast<hipStream_t>(stream)>>>(a);
     });
     return launch_status("act_read");
 }
@@ -270,8 +279,8 @@ extern "C" qm_status gated_act_forward(const void *gate, int64_t ld_gate, const 
     with_kind(dtype, on, [&](auto dt, auto lines) {
         constexpr int DT = decltype(dt)::value;
         constexpr bool LINES = decltype(lines)::value;
-        if (act == kSilu) gated_forward_kernel<DT, kSilu, LINES><<<wgs(a.patches), kWaves * 64, 0, q>>>(a);
-        else gated_forward_kernel<DT, kGelu, LINES><<<wgs(a.patches), kWaves * 64, 0, q>>>(a);
+        if (act == kSilu) gated_forward_kernel<DT, kSilu, LINES><<<wgs(a.patches), kWaves * 64, kForwardShare, q>>>(a);
+        else gated_forward_kernel<DT, kGelu, LINES><<<wgs(a.patches), kWaves * 64, kForwardShare, q>>>(a);
     });
     return launch_status("gated_act_forward");
 }
@@ -306,13 +315,16 @@ extern "C" qm_status gated_act_backward(const qm_act8 *gate8, const qm_act8 *up8
     a.rows = rows, a.cols = cols, a.ld_gate = ld_dgate, a.ld_up = ld_dup, a.ld_h = ld_h, a.ld_dh = ld_dh;
     if (qm_status e = patch_grid(rows, cols, a.patches, a.across)) return e;
     const hipStream_t q = static_cast<hipStream_t>(stream);
+    qm_status st = QM_OK;
     const int64_t size = elem_size(dtype);
     const bool on = on_lines(dgate, ld_dgate * size) && on_lines(dup, ld_dup * size) && (!h || on_lines(h, ld_h * size));
     with_kind(dtype, on, [&](auto dt, auto lines) {
         constexpr int DT = decltype(dt)::value;
         constexpr bool LINES = decltype(lines)::value;
-        if (act == kSilu) gated_backward_kernel<DT, kSilu, LINES><<<wgs(a.patches), kWaves * 64, 0, q>>>(a);
-        else gated_backward_kernel<DT, kGelu, LINES><<<wgs(a.patches), kWaves * 64, 0, q>>>(a);
+        auto kern = act == kSilu ? gated_backward_kernel<DT, kSilu, LINES> : gated_backward_kernel<DT, kGelu, LINES>;
+        static std::atomic<bool> set[2][kMaxDevices] = {};
+        st = reserve_lds(reinterpret_cast<const void *>(kern), kBackwardShare, set[act]);
+        if (st == QM_OK) kern<<<wgs(a.patches), kWaves * 64, kBackwardShare, q>>>(a);
     });
-    return launch_status("gated_act_backward");
+    return st != QM_OK ? st : launch_status("gated_act_backward");
 }

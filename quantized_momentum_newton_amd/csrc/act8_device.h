@@ -140,18 +140,27 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
     return (uint32_t)min(max(b, kScaleLow), kScaleHigh);
 }
 
-// Codes of the lane's eight rows and the scale bytes of its columns.  x(i, j):
-// the element in row i, column j as fp32.
-template <bool LINES, int DT, typename X>
-__device__ __forceinline__ void encode(const Patch<DT> &p, X x, uint64_t data, uint64_t scale, int64_t ld) {
+// Packed elements to be unpacked anew: the compiler otherwise keeps all of them
+// unpacked from one use to the next, which takes half of the waves in flight.
+template <int BYTES, int N> __device__ __forceinline__ void unpack_anew(Packed<BYTES> (&r)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i++)
+#pragma unroll
+        for (int k = 0; k < BYTES / 4; k++) asm volatile("" : "+v"(r[i].w[k]));
+}
+
+// Codes of the lane's eight rows and the scale bytes of its columns.
+template <bool LINES, int DT>
+__device__ __forceinline__ void encode(const Patch<DT> &p, PackedOf<DT, 8> (&r)[kLaneRows], uint64_t data, uint64_t scale, int64_t ld) {
     uint32_t top[8];
 #pragma unroll
     for (int j = 0; j < 8; j++) {
         top[j] = 0;
 #pragma unroll
-        for (int i = 0; i < kLaneRows; i++) top[j] = max(top[j], __float_as_uint(x(i, j)) & 0x7fffffffu);
+        for (int i = 0; i < kLaneRows; i++) top[j] = max(top[j], __float_as_uint(unpack<DT>(r[i], j)) & 0x7fffffffu);
     }
     column_max(top);
+    unpack_anew(r);
     float inv[8];
     uint32_t sb[8], bad[2] = {0, 0};
 #pragma unroll
@@ -166,7 +175,7 @@ __device__ __forceinline__ void encode(const Patch<DT> &p, X x, uint64_t data, u
         float c[8];
         // past 448 only where the exponent met its upper limit
 #pragma unroll
-        for (int j = 0; j < 8; j++) c[j] = __builtin_amdgcn_fmed3f(x(i, j) * inv[j], -448.0f, 448.0f);
+        for (int j = 0; j < 8; j++) c[j] = __builtin_amdgcn_fmed3f(unpack<DT>(r[i], j) * inv[j], -448.0f, 448.0f);
         Packed<8> w;
 #pragma unroll
         for (int h = 0; h < 2; h++) {
