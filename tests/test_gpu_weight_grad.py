@@ -74,6 +74,27 @@ def test_larger(rows, n, k):
         assert torch.equal(q.weight_grad(dy, arg, torch.empty(n, k, device=DEV)).double(), want)
 
 
+@pytest.mark.parametrize("acc", [False, True])
+@pytest.mark.parametrize("rows,n,k", [(2, 257, 129), (1, 1000, 400), (66, 129, 513), (6000, 2047, 1001), (4096, 1001, 130), (40000, 129, 255),
+                                      (3000, 2049, 1283), (9000, 511, 3001), (5001, 7, 1300)])
+def test_last_panels_that_start_early(rows, n, k, acc):
+    """Sides that are no multiple of a tile, at odd addresses, whole and split:
+    overlapping tiles add what they share once, to f32 and to 16-bit results in
+    rows of any pitch."""
+    gen = torch.Generator(device=DEV).manual_seed(rows + k)
+    dy, x = whole(gen, rows, n, B, n + 3, 1), whole(gen, rows, k, B)
+    want = (dy.float().t() @ x.float()).double()      # exact as well
+    kept = q.act_pack(x)
+    for arg in (x, kept):
+        for extra in (0, 1):
+            room = torch.full((n, k + extra), 3.0, device=DEV)
+            out = q.weight_grad(dy, arg, room[:, :k], accumulate=acc)
+            assert torch.equal(out.double(), want + 3 * acc)
+            assert torch.all(room[:, k:] == 3)
+        out = q.weight_grad(dy, arg, torch.full((n, k), 3.0, dtype=B, device=DEV), accumulate=acc)
+        assert torch.equal(out, (want + 3 * acc).float().to(B))
+
+
 @pytest.mark.parametrize("dt", [B, H])
 @pytest.mark.parametrize("out_t", [F, B, H])
 @pytest.mark.parametrize("rows,n,k,kept", [(500, 136, 264, True), (500, 136, 264, False), (3000, 64, 50, True), (77, 70, 33, False)])
