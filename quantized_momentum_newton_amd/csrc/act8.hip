@@ -25,10 +25,10 @@
 namespace qm {
 namespace {
 
-constexpr int kWaves = 4;
+constexpr int kWaves = kPatchWaves;
 
-__device__ __forceinline__ int64_t wave_patch() {
-    return __builtin_amdgcn_readfirstlane((int)(blockIdx.x * kWaves + threadIdx.x / 64));
+template <bool WIDE> __device__ __forceinline__ int patch_of() {
+    return WIDE ? (int)blockIdx.x : __builtin_amdgcn_readfirstlane((int)(blockIdx.x * kWaves + threadIdx.x / 64));
 }
 
 // ------------------------------------------------------------ pack and read
@@ -40,20 +40,24 @@ struct PackArgs {
 };
 
 // LINES: the rows that are written start on cache lines.
-template <int DT, bool LINES> __global__ __launch_bounds__(kWaves * 64) void act_pack_kernel(PackArgs a) {
-    const int patch = wave_patch();
+template <int DT, bool LINES, bool WIDE> __global__ __launch_bounds__(kWaves * 64) void act_pack_kernel(PackArgs a) {
+    const int patch = patch_of<WIDE>();
     if (patch >= a.patches) return;
-    const Patch<DT> p(a.rows, a.cols, patch, a.across, threadIdx.x % 64);
+    const Patch<DT, WIDE> p(a.rows, a.cols, patch, a.across);
     PackedOf<DT, 8> r[kLaneRows];
 #pragma unroll
-    for (int i = 0; i < kLaneRows; i++) r[i] = patch_load<DT>(a.x, a.ld, p, i);
-    encode<LINES>(p, r, a.data, a.scale, a.ld8);
+    for (int i = 0; i < kLaneRows; i++) r[i] = patch_load(a.x, a.ld, p, i);
+    uint32_t top[1][8];
+    lane_tops<DT>(r, top[0]);
+    group_tops<Patch<DT, WIDE>>(top);
+    unpack_anew(r);
+    encode<LINES>(p, r, top[0], a.data, a.scale, a.ld8);
 }
 
-template <int DT, bool LINES> __global__ __launch_bounds__(kWaves * 64) void act_read_kernel(PackArgs a) {
-    const int patch = wave_patch();
+template <int DT, bool LINES, bool WIDE> __global__ __launch_bounds__(kWaves * 64) void act_read_kernel(PackArgs a) {
+    const int patch = patch_of<WIDE>();
     if (patch >= a.patches) return;
-    const Patch<DT> p(a.rows, a.cols, patch, a.across, threadIdx.x % 64);
+    const Patch<DT, WIDE> p(a.rows, a.cols, patch, a.across);
     Packed<8> w[kLaneRows];
 #pragma unroll
     for (int i = 0; i < kLaneRows; i++) w[i] = load_codes(p, a.data, a.ld8, i);
@@ -110,15 +114,15 @@ struct GatedArgs {
     int patches, across;
 };
 
-template <int DT, int ACT, bool LINES> __global__ __launch_bounds__(kWaves * 64) void gated_forward_kernel(GatedArgs a) {
-    const int patch = wave_patch();
+template <int DT, int ACT, bool LINES, bool WIDE> __global__ __launch_bounds__(kWaves * 64) void gated_forward_kernel(GatedArgs a) {
+    const int patch = patch_of<WIDE>();
     if (patch >= a.patches) return;
-    const Patch<DT> p(a.rows, a.cols, patch, a.across, threadIdx.x % 64);
+    const Patch<DT, WIDE> p(a.rows, a.cols, patch, a.across);
     PackedOf<DT, 8> g[kLaneRows], u[kLaneRows];
 #pragma unroll
     for (int i = 0; i < kLaneRows; i++) {
-        g[i] = patch_load<DT>(a.gate, a.ld_gate, p, i);
-        u[i] = patch_load<DT>(a.up, a.ld_up, p, i);
+        g[i] = patch_load(a.gate, a.ld_gate, p, i);
+        u[i] = patch_load(a.up, a.ld_up, p, i);
     }
 #pragma unroll
     for (int i = 0; i < kLaneRows; i++) {
@@ -130,15 +134,21 @@ template <int DT, int ACT, bool LINES> __global__ __launch_bounds__(kWaves * 64)
     if (a.gate_data) {
         unpack_anew(g);
         unpack_anew(u);
-        encode<LINES>(p, g, a.gate_data, a.gate_scale, a.ld_gate8);
-        encode<LINES>(p, u, a.up_data, a.up_scale, a.ld_up8);
+        uint32_t top[2][8];
+        lane_tops<DT>(g, top[0]);
+        lane_tops<DT>(u, top[1]);
+        group_tops<Patch<DT, WIDE>>(top);
+        unpack_anew(g);
+        unpack_anew(u);
+        encode<LINES>(p, g, top[0], a.gate_data, a.gate_scale, a.ld_gate8);
+        encode<LINES>(p, u, top[1], a.up_data, a.up_scale, a.ld_up8);
     }
 }
 
-template <int DT, int ACT, bool LINES> __global__ __launch_bounds__(kWaves * 64) void gated_backward_kernel(GatedArgs a) {
-    const int patch = wave_patch();
+template <int DT, int ACT, bool LINES, bool WIDE> __global__ __launch_bounds__(kWaves * 64) void gated_backward_kernel(GatedArgs a) {
+    const int patch = patch_of<WIDE>();
     if (patch >= a.patches) return;
-    const Patch<DT> p(a.rows, a.cols, patch, a.across, threadIdx.x % 64);
+    const Patch<DT, WIDE> p(a.rows, a.cols, patch, a.across);
     Packed<8> g8[kLaneRows], u8[kLaneRows];
     PackedOf<DT, 8> d[kLaneRows];
     float gs[8], us[8];
@@ -146,7 +156,7 @@ template <int DT, int ACT, bool LINES> __global__ __launch_bounds__(kWaves * 64)
     for (int i = 0; i < kLaneRows; i++) {
         g8[i] = load_codes(p, a.gate_data, a.ld_gate8, i);
         u8[i] = load_codes(p, a.up_data, a.ld_up8, i);
-        d[i] = patch_load<DT>(a.dh, a.ld_dh, p, i);
+        d[i] = patch_load(a.dh, a.ld_dh, p, i);
     }
     load_scales(p, a.gate_scale, a.ld_gate8, gs);
     load_scales(p, a.up_scale, a.ld_up8, us);
@@ -171,35 +181,40 @@ template <int DT, int ACT, bool LINES> __global__ __launch_bounds__(kWaves * 64)
 
 // ------------------------------------------------------------------- host
 
-// Patches of a rows x cols matrix, one a wave; a launch has less than 2^32
-// threads.
+// Patches of a rows x cols matrix, one a wave or (wide) a workgroup; a launch
+// has less than 2^32 threads.
+bool is_wide(int64_t cols) { return cols >= 512; }
 qm_status patch_grid(int64_t rows, int64_t cols, int &patches, int &across) {
-    const int64_t a = (cols + kPatchCols - 1) / kPatchCols, n = a * ((rows + kGroupRows - 1) / kGroupRows);
-    if (n > (int64_t)1 << 25) return fail(QM_E_UNSUPPORTED, "more than 2^25 patches of 32 x 128 elements");
-    patches = (int)n;
-    across = (int)a;
+    if ((cols + 127) / 128 * ((rows + kGroupRows - 1) / kGroupRows) > (int64_t)1 << 25)
+        return fail(QM_E_UNSUPPORTED, "more than 2^25 patches of 32 x 128 elements");
+    const int64_t span = is_wide(cols) ? Patch<QM_F32, true>::kCols : Patch<QM_F32, false>::kCols;
+    across = (int)((cols + span - 1) / span);
+    patches = (int)(across * ((rows + kGroupRows - 1) / kGroupRows));
     return QM_OK;
 }
-// Workgroups a CU, of those that fit (us, 8192 x 14336 bf16): pack 58.4 with
-// all (7), 56.7 with 4; read 60.2 (8), 57.5 (3); forward 162.1 (4), 157.6 (3);
-// backward 211.7 (4), 202.1 (2).
-constexpr unsigned kPackShare = wgs_per_cu(4), kReadShare = wgs_per_cu(3), kForwardShare = wgs_per_cu(3), kBackwardShare = wgs_per_cu(2);
+// Workgroups a CU, of those that fit, for the stream's sake (us, 8192 x 14336
+// bf16): pack 57.8 with all (6), 56.2 with 4; read 61.1 (8), 57.6 (3); forward
+// 159.4 (3), 158.5 (2), at 4096 columns 50.6, 48.8; backward 211.3 (4), 204.0
+// (2).  Less what the wide kernels use themselves.
+constexpr unsigned kPackShare = wgs_per_cu(4) - (8u << 10), kReadShare = wgs_per_cu(3);
+constexpr unsigned kForwardShare = wgs_per_cu(2) - (16u << 10), kBackwardShare = wgs_per_cu(2);
 
-unsigned wgs(int patches) { return (unsigned)((patches + kWaves - 1) / kWaves); }
+unsigned wgs(int patches, int64_t cols) { return (unsigned)(is_wide(cols) ? patches : (patches + kWaves - 1) / kWaves); }
 uint64_t addr(const void *p) { return (uint64_t)(uintptr_t)p; }
 
 // Whether every row starts on a cache line.
 bool on_lines(const void *p, int64_t pitch_bytes) { return aligned(p, 128) && pitch_bytes % 128 == 0; }
 
-// Calls f with the type and with `lines` as constants.
-template <typename F> void with_kind(int32_t dtype, bool lines, F f) {
-    auto as = [&](auto l) {
-        if (dtype == QM_F32) f(std::integral_constant<int, QM_F32>(), l);
-        else if (dtype == QM_BF16) f(std::integral_constant<int, QM_BF16>(), l);
-        else f(std::integral_constant<int, QM_F16>(), l);
+// Calls f with the type, `lines` and is_wide(cols) as constants.
+template <typename F> void with_kind(int32_t dtype, bool lines, int64_t cols, F f) {
+    auto as = [&](auto l, auto w) {
+        if (dtype == QM_F32) f(std::integral_constant<int, QM_F32>(), l, w);
+        else if (dtype == QM_BF16) f(std::integral_constant<int, QM_BF16>(), l, w);
+        else f(std::integral_constant<int, QM_F16>(), l, w);
     };
-    if (lines) as(std::true_type());
-    else as(std::false_type());
+    if (!is_wide(cols)) as(std::false_type(), std::false_type());
+    else if (lines) as(std::true_type(), std::true_type());
+    else as(std::false_type(), std::true_type());
 }
 
 }  // namespace
@@ -220,8 +235,8 @@ extern "C" qm_status act_pack(const void *x, int32_t dtype, int64_t ld, const qm
     if (s.clash()) return fail(QM_E_ARG, "x and kept overlap");
     PackArgs a{addr(x), addr(kept->data), addr(kept->scale), rows, cols, ld, kept->ld, 0, 0};
     if (qm_status e = patch_grid(rows, cols, a.patches, a.across)) return e;
-    with_kind(dtype, on_lines(kept->data, kept->ld), [&](auto dt, auto lines) {
-        act_pack_kernel<decltype(dt)::value, decltype(lines)::value><<<wgs(a.patches), kWaves * 64, kPackShare, static_cast<hipStream_t>(stream)>>>(a);
+    with_kind(dtype, on_lines(kept->data, kept->ld), cols, [&](auto dt, auto lines, auto wide) {
+        act_pack_kernel<decltype(dt)::value, decltype(lines)::value, decltype(wide)::value><<<wgs(a.patches, cols), kWaves * 64, kPackShare, static_cast<hipStream_t>(stream)>>>(a);
     });
     return launch_status("act_pack");
 }
@@ -239,8 +254,8 @@ extern "C" qm_status act_read(const qm_act8 *kept, void *out, int32_t dtype, int
     if (s.clash()) return fail(QM_E_ARG, "out and kept overlap");
     PackArgs a{addr(out), addr(kept->data), addr(kept->scale), rows, cols, ld, kept->ld, 0, 0};
     if (qm_status e = patch_grid(rows, cols, a.patches, a.across)) return e;
-    with_kind(dtype, on_lines(out, ld * elem_size(dtype)), [&](auto dt, auto lines) {
-        act_read_kernel<decltype(dt)::value, decltype(lines)::value><<<wgs(a.patches), kWaves * 64, kReadShare, static_cast<hipStream_t>(stream)>>>(a);
+    with_kind(dtype, on_lines(out, ld * elem_size(dtype)), cols, [&](auto dt, auto lines, auto wide) {
+        act_read_kernel<decltype(dt)::value, decltype(lines)::value, decltype(wide)::value><<<wgs(a.patches, cols), kWaves * 64, kReadShare, static_cast<hipStream_t>(stream)>>>(a);
     });
     return launch_status("act_read");
 }
@@ -276,11 +291,11 @@ extern "C" qm_status gated_act_forward(const void *gate, int64_t ld_gate, const 
     if (qm_status e = patch_grid(rows, cols, a.patches, a.across)) return e;
     const hipStream_t q = static_cast<hipStream_t>(stream);
     const bool on = on_lines(h, ld_h * elem_size(dtype)) && (!gate8 || (on_lines(gate8->data, gate8->ld) && on_lines(up8->data, up8->ld)));
-    with_kind(dtype, on, [&](auto dt, auto lines) {
+    with_kind(dtype, on, cols, [&](auto dt, auto lines, auto wide) {
         constexpr int DT = decltype(dt)::value;
-        constexpr bool LINES = decltype(lines)::value;
-        if (act == kSilu) gated_forward_kernel<DT, kSilu, LINES><<<wgs(a.patches), kWaves * 64, kForwardShare, q>>>(a);
-        else gated_forward_kernel<DT, kGelu, LINES><<<wgs(a.patches), kWaves * 64, kForwardShare, q>>>(a);
+        constexpr bool LINES = decltype(lines)::value, WIDE = decltype(wide)::value;
+        if (act == kSilu) gated_forward_kernel<DT, kSilu, LINES, WIDE><<<wgs(a.patches, cols), kWaves * 64, kForwardShare, q>>>(a);
+        else gated_forward_kernel<DT, kGelu, LINES, WIDE><<<wgs(a.patches, cols), kWaves * 64, kForwardShare, q>>>(a);
     });
     return launch_status("gated_act_forward");
 }
@@ -318,13 +333,13 @@ extern "C" qm_status gated_act_backward(const qm_act8 *gate8, const qm_act8 *up8
     qm_status st = QM_OK;
     const int64_t size = elem_size(dtype);
     const bool on = on_lines(dgate, ld_dgate * size) && on_lines(dup, ld_dup * size) && (!h || on_lines(h, ld_h * size));
-    with_kind(dtype, on, [&](auto dt, auto lines) {
+    with_kind(dtype, on, cols, [&](auto dt, auto lines, auto wide) {
         constexpr int DT = decltype(dt)::value;
-        constexpr bool LINES = decltype(lines)::value;
-        auto kern = act == kSilu ? gated_backward_kernel<DT, kSilu, LINES> : gated_backward_kernel<DT, kGelu, LINES>;
+        constexpr bool LINES = decltype(lines)::value, WIDE = decltype(wide)::value;
+        auto kern = act == kSilu ? gated_backward_kernel<DT, kSilu, LINES, WIDE> : gated_backward_kernel<DT, kGelu, LINES, WIDE>;
         static std::atomic<bool> set[2][kMaxDevices] = {};
         st = reserve_lds(reinterpret_cast<const void *>(kern), kBackwardShare, set[act]);
-        if (st == QM_OK) kern<<<wgs(a.patches), kWaves * 64, kBackwardShare, q>>>(a);
+        if (st == QM_OK) kern<<<wgs(a.patches, cols), kWaves * 64, kBackwardShare, q>>>(a);
     });
     return st != QM_OK ? st : launch_status("gated_act_backward");
 }
