@@ -6,7 +6,8 @@ global norm over all gradients gives the clip factor; the Muon gradients are
 scaled by it in place, the AdamW step takes it as an argument.  A batch whose
 norm is not finite is left out as a whole: the AdamW step would write nothing
 by itself, but the Muon step reads its gradients whatever they hold, so the
-program looks at the factor before it.
+program looks at the factor before it.  The embedding's rows and its gradient
+are the library's as well.
 
 The data are synthetic: a fixed random permutation of the vocabulary, each
 token followed by its image, so a model that learns reaches a loss near 0.
@@ -22,6 +23,22 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import quantized_momentum_newton_amd as q  # noqa: E402
 
 VOCAB, WIDTH, HIDDEN, LAYERS, BATCH = 512, 256, 512, 2, 1024
+
+
+class Embedding(torch.autograd.Function):
+    """Rows of the table; their gradients are added to the table's buffer, in
+    an order that the tokens determine."""
+
+    @staticmethod
+    def forward(ctx, table, tokens):
+        ctx.save_for_backward(tokens)
+        ctx.grad = table.grad
+        return q.embedding_lookup(tokens, table.detach())
+
+    @staticmethod
+    def backward(ctx, dy):
+        q.embedding_grad(*ctx.saved_tensors, dy.contiguous(), ctx.grad, accumulate=True)
+        return None, None
 
 
 class Model:
@@ -52,7 +69,7 @@ class Model:
         def norm(x, gain):
             return x * torch.rsqrt(x.square().mean(-1, keepdim=True) + 1e-6) * gain
 
-        x = w["embedding"][tokens]
+        x = Embedding.apply(w["embedding"], tokens)
         for k in range(LAYERS):
             x = x + torch.relu(norm(x, w[f"gain{k}"]) @ w[f"up{k}"].t()) @ w[f"down{k}"].t()
         logits = norm(x, w["gain_out"]) @ w["head"].t()

@@ -23,6 +23,12 @@
 //          written whole also gets its zeros here, one that is added to is
 //          touched in rows that have tokens.
 //   join   The parts of a long row are added, in order, by one workgroup.
+//
+// 50257 x 2048 fp32 written whole from 32768 skewed tokens: sort 13 us, sum 105
+// (412 MB written, 134 read: 84 at the rate of a large copy), join 8; the sort is
+// bound by its instructions (256 workgroups look at every token), the sum by the
+// latency of start, order and rows in turn.  All zeros: 79 us, torch's fill 61.
+// Added to 32000 x 4096 bf16 from 16384 tokens: 10, 51 and 8 us.
 #include <algorithm>
 #include <type_traits>
 

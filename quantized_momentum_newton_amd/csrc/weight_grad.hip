@@ -15,11 +15,21 @@
 //
 // Tiles of 256 x 256 (eight waves of 128 x 64, fp32 accumulators) or 128 x 128
 // (four waves of 64 x 64), 64 rows a step, two LDS buffers; the rows of the steps
-// after the next are in flight to registers while this one is multiplied.  Rows and columns past
-// the ends read as zeros (buffer descriptors with their extents), so the loop
-// has no edge cases.  Tiles that do not fill a round of the GPU are split over
-// t; their parts go to the workspace and are added in order by a second
-// kernel.
+// after the next are in flight to registers while this one is multiplied.  Rows
+// and columns past the ends read as zeros (buffer descriptors with their
+// extents), so the loop has no edge cases.  Tiles that do not fill a round of the
+// GPU are split over t; their parts go to the workspace and are added in order by
+// a second kernel.
+//
+// What bounds it: 14336 x 4096 over 8192 rows of kept input, 759 us (1267
+// TFLOP/s) written and 795 (1210) added to 235 MB; a bf16 product of 8192 cubed
+// by the library reaches 1220.  The same call on zeros takes 587 us: the rest is
+// the clock, which falls to 1.7 GHz under the load of real operands.  There the
+// matrix units are busy 60 % of the cycles, with LDS reads and writes dealt out
+// between the products (all of a slice's reads ahead of its products: 735 us on
+// zeros).  LDS has no bank conflicts and is active in a quarter of the cycles.
+// Products that leave a CU one 128 tile (1024 x 4096 over 8192 rows, 84 us) are
+// bound by that tile's one wave a SIMD, which issues one thing at a time.
 #include <math.h>
 
 #include <algorithm>
