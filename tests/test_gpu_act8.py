@@ -69,6 +69,37 @@ def test_bytes_scales_and_values(dt, rows, cols, pitch, shift):
     assert torch.equal(q.act_read(c).double(), torch.tensor(v, device=DEV))
 
 
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("rows,cols,ld", [(33, 511, 512), (40, 512, 512), (40, 513, 528), (65, 700, 704), (100, 1025, 1152), (8, 516, 640),
+                                          (130, 2047, 2048)])
+def test_narrow_and_wide_patches_and_any_row_length(dt, rows, cols, ld):
+    """Both ways over a matrix, rows of kept bytes on and off cache lines."""
+    _, x = inputs(rows, cols, dt, rows + cols)
+    groups = -(-rows // 32)
+    c = q.ActCheckpoint(rows, cols, data=torch.zeros(rows, ld, dtype=torch.uint8, device=DEV),
+                        scale=torch.zeros(groups, ld, dtype=torch.uint8, device=DEV))
+    q.act_pack(x, c)
+    v = torch.tensor(check_codes(x, c, rows, cols), device=DEV)
+    for out_t in TYPES:
+        assert torch.equal(q.act_read(c, dtype=out_t), v.to(torch.float32).to(out_t))
+    up = x.flip(0).contiguous()
+    h, g8, u8 = q.gated_act_forward(x, up, gate_ckpt=c)
+    check_codes(up, u8, rows, cols)
+    assert torch.equal(q.act_read(g8), v.to(torch.bfloat16))
+    whole = q.gated_act_forward(x, up, keep=False)[0]
+    assert torch.equal(h, whole)
+    parts = torch.cat([q.gated_act_forward(x[:, k:k + 100], up[:, k:k + 100], keep=False)[0] for k in range(0, cols, 100)], 1)
+    assert torch.equal(h, parts)
+    wide = q.gated_act_backward(g8, u8, h, recompute=True)
+    for k in range(0, cols, 100):
+        part = [q.ActCheckpoint(rows, min(100, cols - k), device=DEV) for _ in range(2)]
+        for p, s in zip(part, (x, up)):
+            q.act_pack(s[:, k:k + 100], p)
+        narrow = q.gated_act_backward(*part, h[:, k:k + 100], recompute=True)
+        for a, b in zip(wide, narrow):
+            assert torch.equal(a[:, k:k + 100], b)
+
+
 def test_rows_behind_the_last_are_left_as_they_were():
     """A checkpoint inside larger buffers: only its rows are written."""
     data = torch.full((70, 64), 0x11, dtype=torch.uint8, device=DEV)

@@ -76,6 +76,17 @@ def test_whole_numbers_are_exact(kind, n, vocab, cols):
     assert torch.all(room[:, 0] == 9) and torch.all(room[:, 1 + cols] == 9)
 
 
+@pytest.mark.parametrize("kind", ["spread", "few", "padded"])
+@pytest.mark.parametrize("n,vocab,cols,dt", [(32768, 500, 24, torch.int64), (32769, 500, 24, torch.int32), (70000, 900, 40, torch.int64),
+                                             (140000, 50000, 16, torch.int32)])
+def test_more_tokens_than_a_wave_holds(kind, n, vocab, cols, dt):
+    """Up to 32768 tokens stay in registers between the two looks at them."""
+    tok = tokens(kind, n, vocab, n, dt)
+    dy = torch.randint(-3, 4, (n, cols), generator=torch.Generator(device=DEV).manual_seed(n), device=DEV).to(torch.bfloat16)
+    want = torch.tensor(O.embedding_grad(tok.cpu().numpy(), dy.float().cpu().numpy(), vocab, 1.0), device=DEV)
+    assert torch.equal(q.embedding_grad(tok, dy, torch.empty(vocab, cols, device=DEV)).double(), want)
+
+
 @pytest.mark.parametrize("dt", TYPES)
 @pytest.mark.parametrize("gt", TYPES)
 @pytest.mark.parametrize("acc", [False, True])
