@@ -14,12 +14,12 @@
 // number times a power of two).  That is why groups run along the rows.
 //
 // Tiles of 256 x 256 (eight waves of 128 x 64, fp32 accumulators) or 128 x 128
-// (four waves of 64 x 64), 64 rows a step, two LDS buffers; the rows of the steps
-// after the next are in flight to registers while this one is multiplied.  Rows
-// and columns past the ends read as zeros (buffer descriptors with their
-// extents), so the loop has no edge cases.  Tiles that do not fill a round of the
-// GPU are split over t; their parts go to the workspace and are added in order by
-// a second kernel.
+// (four waves of 64 x 64 or eight of 64 x 32), 64 rows a step, two LDS buffers;
+// the rows of the steps after the next are in flight to registers while this one
+// is multiplied.  Rows and columns past the ends read as zeros (buffer descriptors
+// with their extents), so the loop has no edge cases.  Tiles that do not fill a
+// round of the GPU are split over t; their parts go to the workspace and are added
+// in order by a second kernel.
 //
 // What bounds it: 14336 x 4096 over 8192 rows of kept input, 759 us (1267
 // TFLOP/s) written and 795 (1210) added to 235 MB; a bf16 product of 8192 cubed
@@ -28,8 +28,9 @@
 // matrix units are busy 60 % of the cycles, with LDS reads and writes dealt out
 // between the products (all of a slice's reads ahead of its products: 735 us on
 // zeros).  LDS has no bank conflicts and is active in a quarter of the cycles.
-// Products that leave a CU one 128 tile (1024 x 4096 over 8192 rows, 84 us) are
-// bound by that tile's one wave a SIMD, which issues one thing at a time.
+// Products that leave a CU one 128 tile (1024 x 4096 over 8192 rows, 92 us) are
+// bound by that tile's one wave a SIMD, which issues one thing at a time; where
+// there is more to issue than products and their reads, it has two (launch_kind).
 #include <math.h>
 
 #include <algorithm>
@@ -259,7 +260,7 @@ template <int DT, int B, int NT, bool BYTES, int MODE, int DEPTH> struct Panel {
 };
 
 template <int DT, bool KEPT, int MODE, int B, int WAVES_N, int WAVES_K>
-__global__ __launch_bounds__(WAVES_N *WAVES_K * 64, B == 256 ? 2 : 2) void weight_grad_kernel(ProductArgs a) {
+__global__ __launch_bounds__(WAVES_N *WAVES_K * 64, B / WAVES_K == 32 ? 4 : 2) void weight_grad_kernel(ProductArgs a) {
     constexpr int NT = WAVES_N * WAVES_K * 64;
     constexpr int FN = B / WAVES_N / 32, FK = B / WAVES_K / 32, STEPS = kStep / 16;
     // Steps in flight to registers.  A 128 tile's step takes less than a load,
@@ -308,9 +309,9 @@ __global__ __launch_bounds__(WAVES_N *WAVES_K * 64, B == 256 ? 2 : 2) void weigh
     // Scales of a kept step: two groups of 32 rows, B bytes each, one byte a
     // thread, behind the panels in LDS.
     constexpr int SCALES = PanelA::kBytes + PanelB::kBytes;
-    static_assert(2 * B == NT, "a scale byte for each thread");
+    static_assert(2 * B <= NT, "a scale byte for each thread");
     uint32_t sc[DEPTH];
-    const int sc_group = threadIdx.x / B, sc_col = threadIdx.x % B;
+    const int sc_group = threadIdx.x / B % 2, sc_col = threadIdx.x % B;
     auto load_scales = [&](int d, int t) {
         if constexpr (KEPT) {
             const int groups = max(0, min(2, (t1 - t + 31) >> 5)), limit = a.k - bk * B;
@@ -319,7 +320,7 @@ __global__ __launch_bounds__(WAVES_N *WAVES_K * 64, B == 256 ? 2 : 2) void weigh
         }
     };
     auto store_scales = [&](int d, char *buf) {
-        if constexpr (KEPT) buf[SCALES + threadIdx.x] = (char)sc[d];
+        if constexpr (KEPT) buf[SCALES + threadIdx.x % (2 * B)] = (char)sc[d];
     };
 
     f32x16_t acc[FN][FK];
@@ -331,9 +332,9 @@ __global__ __launch_bounds__(WAVES_N *WAVES_K * 64, B == 256 ? 2 : 2) void weigh
             for (int r = 0; r < 16; r++) acc[i][j][r] = 0.0f;
 
     const int steps = (t1 - t0 + kStep - 1) / kStep;
-    // Slices whose fragments are read ahead.  A 128 tile's slice (four products,
-    // 128 cycles, often one wave on a SIMD) is shorter than a read.
-    constexpr int AHEAD = B == 256 ? 1 : 2, SETS = B == 256 ? 2 : 4;
+    // Slices whose fragments are read ahead.  The slice of a wave that has its
+    // SIMD to itself (four products, 128 cycles) is shorter than a read.
+    constexpr int AHEAD = FN * FK == 4 ? 2 : 1, SETS = 2 * AHEAD;
     u32x4_t fa[SETS][FN];
     typename PanelB::Raw fb[SETS][FK];
     uint32_t unit[2][FK];      // scale bytes of the lane's columns, of both groups
@@ -362,8 +363,7 @@ __global__ __launch_bounds__(WAVES_N *WAVES_K * 64, B == 256 ? 2 : 2) void weigh
 #pragma unroll
         for (int m = 0; m < kProducts; m++) {
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);      // a matrix product
-            if constexpr (kReads > kProducts) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);      // LDS reads
-            else __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, (kReads + kProducts - 1) / kProducts, 0);      // LDS reads
             if constexpr (W > 0) __builtin_amdgcn_sched_group_barrier(0x200, (W + kProducts - 1) / kProducts, 0);
             if constexpr (V > 0) __builtin_amdgcn_sched_group_barrier(0x020, (V + kProducts - 1) / kProducts, 0);
         }
@@ -619,10 +619,16 @@ qm_status launch_product(const ProductArgs &a, hipStream_t q) {
     return launch_status("weight_grad");
 }
 template <int DT, bool KEPT> qm_status launch_kind(const ProductArgs &a, int mode, int b, hipStream_t q) {
-    if (mode == kNarrow) return launch_product<DT, KEPT, kNarrow, 128, 2, 2>(a, q);
+    // Waves of a 128 tile.  Eight, two a SIMD, where pieces are cleared or bytes
+    // converted between the products: 2047 x 1001 over 5001 rows 46 us, with four
+    // 49; 1024 x 4096 over 8192 kept rows 88 and 93.  Plain aligned panels: four,
+    // which read each panel's fragments fewer times: 1024 x 4096 over 8192 rows
+    // 92 us, with eight 96; 2560 x 2048 over 2048 43 and 46.
+    constexpr int kAlignedWaves = KEPT ? 4 : 2;      // along k, two along n
+    if (mode == kNarrow) return launch_product<DT, KEPT, kNarrow, 128, 2, 4>(a, q);
     if (mode == kAligned)
-        return b == 256 ? launch_product<DT, KEPT, kAligned, 256, 2, 4>(a, q) : launch_product<DT, KEPT, kAligned, 128, 2, 2>(a, q);
-    return b == 256 ? launch_product<DT, KEPT, kAny, 256, 2, 4>(a, q) : launch_product<DT, KEPT, kAny, 128, 2, 2>(a, q);
+        return b == 256 ? launch_product<DT, KEPT, kAligned, 256, 2, 4>(a, q) : launch_product<DT, KEPT, kAligned, 128, 2, kAlignedWaves>(a, q);
+    return b == 256 ? launch_product<DT, KEPT, kAny, 256, 2, 4>(a, q) : launch_product<DT, KEPT, kAny, 128, 2, 4>(a, q);
 }
 template <int OT> void launch_join(const ProductArgs &a, int b, hipStream_t q) {
     if (b == 256) weight_grad_join_kernel<OT, 256><<<(unsigned)a.rest * 32, 256, 0, q>>>(a);
