@@ -28,7 +28,7 @@
 // matrix units are busy 60 % of the cycles, with LDS reads and writes dealt out
 // between the products (all of a slice's reads ahead of its products: 735 us on
 // zeros).  LDS has no bank conflicts and is active in a quarter of the cycles.
-// Products that leave a CU one 128 tile (1024 x 4096 over 8192 rows, 92 us) are
+// Products that leave a CU one 128 tile (1024 x 4096 over 8192 rows, 84 to 92 us) are
 // bound by that tile's one wave a SIMD, which issues one thing at a time; where
 // there is more to issue than products and their reads, it has two (launch_kind).
 #include <math.h>
