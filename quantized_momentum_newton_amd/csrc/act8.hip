@@ -98,14 +98,15 @@ template <int ACT, bool FAST> __device__ __forceinline__ float act_value(float g
 }
 // The value and the slope.  s is 0 or 1 in fp32 long before |g| = 32; from
 // there on the slope's second term is left at its limit 0, where g^2 would
-// overflow for the largest g.
+// overflow for the largest g.  The limit is a compare and a select: minimum and
+// maximum would turn a NaN into -32 and its slope into 0.
 template <int ACT, bool FAST> __device__ __forceinline__ float act_slope(float g, float &value) {
     if constexpr (ACT == kSilu) {
         const float s = sigmoid<FAST>(g);
         value = g * s;
         return s * (1.0f + g * (1.0f - s));
     } else {
-        const float b = fminf(fmaxf(g, -32.0f), 32.0f);
+        const float b = fabsf(g) > 32.0f ? copysignf(32.0f, g) : g;
         const float s = sigmoid<FAST>(kGeluA * (b + 0.044715f * b * b * b));
         value = g * s;
         return s + b * (s * (1.0f - s)) * (kGeluA * (1.0f + kGeluB * b * b));
