@@ -109,10 +109,11 @@ template <int DT, int OUT> __global__ __launch_bounds__(kLookupThreads) void emb
         col[k] = (int)(at % (uint32_t)a.pieces) * V;
         tok[k] = row[k] < a.n_tokens ? token_at(a.tokens, a.token_bits, row[k]) : -1;
     }
-    float x[kLookupEach][V];
+    float x[kLookupEach][V], scale[kLookupEach];
 #pragma unroll
     for (int k = 0; k < kLookupEach; k++) {
         const bool inside = (uint64_t)tok[k] < (uint64_t)a.vocab;
+        scale[k] = inside ? a.scale : 0.0f;      // zeros whatever the scale
         const int n = inside ? min(V, a.cols - col[k]) : 0;
         load_cols<DT, V>(a.table + (uint64_t)(tok[k] * a.ld_table + col[k]) * kSizeOf<DT>, n, x[k]);
     }
@@ -120,7 +121,7 @@ template <int DT, int OUT> __global__ __launch_bounds__(kLookupThreads) void emb
     for (int k = 0; k < kLookupEach; k++) {
         if (row[k] >= a.n_tokens) continue;
 #pragma unroll
-        for (int j = 0; j < V; j++) x[k][j] = in_fp32(x[k][j] * a.scale);
+        for (int j = 0; j < V; j++) x[k][j] = in_fp32(x[k][j] * scale[k]);
         store_cols<OUT, V>(a.out + (uint64_t)(row[k] * a.ld_out + col[k]) * kSizeOf<OUT>, min(V, a.cols - col[k]), x[k]);
     }
 }
