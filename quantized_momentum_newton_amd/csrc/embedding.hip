@@ -128,6 +128,11 @@ template <int DT, int OUT> __global__ __launch_bounds__(kLookupThreads) void emb
 
 // -------------------------------------------------------------------- sort
 
+// Between LDS accesses by which lanes of a wave hand values to one another.  LDS
+// serves a wave's accesses in the order of its instructions, so there is nothing
+// to wait for; this holds the compiler to that order.
+__device__ __forceinline__ void wave_lds_order() { asm volatile("" ::: "memory"); }
+
 struct Sorted {
     int32_t token, position;
 };
@@ -231,11 +236,15 @@ __global__ __launch_bounds__(kSortWaves * 64) void embedding_sort_kernel(SortArg
                     left &= ~these;
                 }
             }
+            // all lanes of a value read its place, the first of them moves it on,
+            // for the next 64 tokens' lanes to read
             if (in) {
                 const int before = __popcll(same & ((1ull << lane) - 1)), next = mine[value];
+                wave_lds_order();
                 if (before == 0) mine[value] = next + __popcll(same);
                 gmem<Sorted>(a.sorted)[next + before] = Sorted{(int32_t)t[k], c + k * 64 + lane};
             }
+            wave_lds_order();
         }
     };
 #pragma unroll
