@@ -41,6 +41,7 @@ namespace {
 constexpr int kChunk = 32;        // positions of a part, and the longest row without parts
 constexpr int kSortWaves = 16, kSortValues = 1024;
 constexpr int kSumWaves = 4, kJoinWaves = 8, kJoinChunks = 8;
+constexpr int kRange = 16;        // most positions whose rows a wave starts
 constexpr int kFill = 16;         // rows that a wave looks at for empty ones
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;     // tokens, and values: their counts stay 32-bit numbers
 
@@ -309,13 +310,12 @@ template <int DT, int V, int P> struct Piece {
     }
 };
 
-// Sums dy rows along the order: entries `from` .. `to` - 1 of a window of 128
-// whose positions lanes hold (entry w in lane w % 64 of pos[w / 64]), several
-// rows in flight whatever they belong to.  ends(w): whether a row of the table
+// Sums dy rows along the order: entries `from` .. `to` - 1 of a window of 64
+// whose positions lanes hold, several rows in flight whatever they belong to.  ends(w): whether a row of the table
 // ends with entry w; then old.load has its gradient under way with the entry's
 // own loads and leave(w, acc, old) takes the sum.
 template <int DT, int V, int P, typename Old, typename Ends, typename Fetch, typename Leave>
-__device__ __forceinline__ void stream(const SumArgs &a, const int *pos, int from, int to, const Columns<V, P> &c, Ends ends,
+__device__ __forceinline__ void stream(const SumArgs &a, int pos, int from, int to, const Columns<V, P> &c, Ends ends,
                                        Fetch fetch, Leave leave) {
     constexpr int kAhead = P * V >= 16 ? 4 : 8;
     float acc[P][V] = {};
@@ -325,7 +325,7 @@ __device__ __forceinline__ void stream(const SumArgs &a, const int *pos, int fro
 #pragma unroll
         for (int u = 0; u < kAhead; u++) {
             if (w + u >= to) continue;
-            const int at = __builtin_amdgcn_readlane(w + u < 64 ? pos[0] : pos[1], (w + u) & 63);
+            const int at = __builtin_amdgcn_readlane(pos, w + u);
             x[u].load(a.dy + (uint64_t)(at * a.ld_dy) * kSizeOf<DT>, c);
             if (ends(w + u)) fetch(w + u, old[u]);
         }
@@ -365,11 +365,10 @@ template <int DT, int GT, int V, int P, bool ACC> __global__ __launch_bounds__(k
         int head = -1;
         if (first <= last) {
             const Sorted e = sorted_at(min(first + lane, last));
-            const int pos[2] = {e.position, 0};
             const int t0 = __builtin_amdgcn_readlane(e.token, 0), t1 = __builtin_amdgcn_readlane(e.token, last - first);
             const int s0 = start_of(a.start, t0), e0 = start_of(a.start, t0 + 1), s1 = start_of(a.start, t1), e1 = start_of(a.start, t1 + 1);
             auto part = [&](int slot, int from, int to) {
-                stream<DT, V, P, Nothing>(a, pos, from, to, c, [&](int w) { return w == to - 1; }, [](int, Nothing &) {},
+                stream<DT, V, P, Nothing>(a, e.position, from, to, c, [&](int w) { return w == to - 1; }, [](int, Nothing &) {},
                                           [&](int, float (*acc)[V], Nothing &) {
 #pragma unroll
                                               for (int p = 0; p < P; p++)
@@ -392,29 +391,29 @@ template <int DT, int GT, int V, int P, bool ACC> __global__ __launch_bounds__(k
     down -= a.chunks;
     if (down < a.ranges) {
         // the rows that start in this range of the order, but for long ones;
-        // window entry w is position begin - 1 + w
+        // window entry w is position begin - 1 + w.  The last row starts at most
+        // at entry kRange: one that the window does not see end is a long one.
+        static_assert(kRange + kChunk < 64, "window");
         const int begin = down * a.range;
         if (begin >= n_sorted) return;
         auto entry = [&](int i) { return i < 0 || i >= n_sorted ? Sorted{i < 0 ? -2 : -3, 0} : sorted_at(i); };
-        const Sorted lo = entry(begin - 1 + lane), hi = entry(begin + 63 + lane);
-        const int pos[2] = {lo.position, hi.position};
-        const int before_lo = __shfl_up(lo.token, 1), before_hi = __shfl_up(hi.token, 1);
-        const uint64_t head_lo = __ballot(lane > 0 && lo.token != before_lo);
-        const uint64_t head_hi = __ballot(hi.token != (lane > 0 ? before_hi : __builtin_amdgcn_readlane(lo.token, 63)));
-        const uint64_t here = head_lo & ((2ull << a.range) - 2);
+        const Sorted e = entry(begin - 1 + lane);
+        const int before = __shfl_up(e.token, 1);
+        const uint64_t heads = __ballot(lane > 0 && e.token != before);
+        const uint64_t here = heads & ((2ull << a.range) - 2);
         if (here == 0) return;
         const int from = __ffsll((unsigned long long)here) - 1, last = 63 - __clzll((long long)here);
-        const uint64_t after = head_lo & ~((2ull << last) - 1);
-        int to = after ? __ffsll((unsigned long long)after) - 1 : head_hi ? 64 + __ffsll((unsigned long long)head_hi) - 1 : 128;
+        const uint64_t after = heads & ~((2ull << last) - 1);
+        int to = after ? __ffsll((unsigned long long)after) - 1 : 64;
         if (to - last > kChunk) to = last;      // a long row: its parts are summed elsewhere
-        auto ends = [&](int w) { return w + 1 == to || (w + 1 < 64 && head_lo >> (w + 1) & 1); };
+        auto ends = [&](int w) { return w + 1 == to || heads >> (w + 1) & 1; };
         auto row = [&](int w) {
-            const int token = __builtin_amdgcn_readlane(w < 64 ? lo.token : hi.token, w & 63);
+            const int token = __builtin_amdgcn_readlane(e.token, w);
             return a.grad + (uint64_t)(token * a.ld_grad) * kSizeOf<GT>;
         };
         using Old = std::conditional_t<ACC, Piece<GT, V, P>, Nothing>;
         stream<DT, V, P, Old>(
-            a, pos, from, to, c, ends,
+            a, e.position, from, to, c, ends,
             [&](int w, Old &old) {
                 if constexpr (ACC) old.load(row(w), c);
             },
@@ -619,8 +618,8 @@ extern "C" qm_status embedding_grad(const void *tokens, int32_t token_bits, int6
     a.dy = addr(dy), a.grad = addr(grad), a.ld_dy = ld_dy, a.ld_grad = ld_grad;
     a.vocab = (int)vocab, a.cols = (int)cols;
     a.slabs = (int)((cols + span - 1) / span), a.part_ld = (int)sp.part_ld;
-    // positions of a range: 16, or fewer as long as there are less than 4096 units
-    a.range = 16;
+    // positions of a range: fewer as long as there are less than 4096 units
+    a.range = kRange;
     while (a.range > 1 && n_tokens * a.slabs / a.range < 4096) a.range /= 2;
     a.chunks = (int)sp.chunks, a.ranges = (int)((n_tokens + a.range - 1) / a.range);
     a.fills = accumulate ? 0 : (int)((vocab + kFill - 1) / kFill);
