@@ -27,7 +27,9 @@ VOCAB, WIDTH, HIDDEN, LAYERS, BATCH = 512, 256, 512, 2, 1024
 
 class Embedding(torch.autograd.Function):
     """Rows of the table; their gradients are added to the table's buffer, in
-    an order that the tokens determine."""
+    an order that the tokens determine.  The buffer is the one that the table
+    has when the rows are taken.  Autograd itself is told of no gradient: hooks
+    on the table and torch.autograd.grad see none."""
 
     @staticmethod
     def forward(ctx, table, tokens):
