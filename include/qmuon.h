@@ -638,8 +638,9 @@ QM_API qm_status adamw_read_state(const void *host_plan, const void *dev_plan,
  * Coding: scale - 127 = e, the smallest integer with max|x| <= 448 * 2^e over
  * the group, between -95 and 119; data = E4M3(x * 2^-e), rounded to nearest
  * even, at most 448.  A value is off by at most 1/16 of itself, or by 2^-10 *
- * 2^e where it is below 2^-6 * 2^e, and exact in fp32 and bf16.  A group that
- * holds an infinity or a NaN decodes to NaN as a whole.  Rows share a scale,
+ * 2^e where it is below 2^-6 * 2^e, and exact in fp32 and bf16; magnitudes past
+ * 448 * 2^119 = 2.98e38 become that.  A group that holds an infinity or a NaN
+ * decodes to NaN as a whole.  Rows share a scale,
  * not columns: an activation's outliers keep to their columns, and a weight
  * gradient contracts over the rows. */
 typedef struct {
@@ -656,6 +657,7 @@ QM_API qm_status act_pack(const void *x, int32_t dtype, int64_t ld,
                           const qm_act8 *kept, qm_stream_t stream);
 
 /* out = the values kept stands for, rounded to nearest even into its dtype.
+ * f16 numbers of magnitude 63488 and more are kept as 65536, an infinity in f16.
  * Errors: as act_pack. */
 QM_API qm_status act_read(const qm_act8 *kept, void *out, int32_t dtype,
                           int64_t ld, qm_stream_t stream);
@@ -663,7 +665,7 @@ QM_API qm_status act_read(const qm_act8 *kept, void *out, int32_t dtype,
 /* Gradient of a linear layer's weight (n x k) over rows tokens:
  *   out[i][j] (= or +=) sum over t of dy[t][i] * x[t][j]
  * dy: rows x n, bf16 or f16.  x: rows x k of the same type, or null with
- * `kept` in its place (its values, in f16 rounded to f16).  Products exact,
+ * `kept` in its place (its values, in f16 rounded as act_read does).  Products exact,
  * sums in fp32 in an order that the sizes determine; the result is rounded
  * once.  out: any dtype, ld_out < 2^21.  rows = 0: zeros, or nothing to add.
  *   ws: >= weight_grad_workspace_bytes(rows, n, k) bytes (0: none needed),
@@ -682,7 +684,7 @@ QM_API qm_status weight_grad(const void *dy, int32_t dtype, int64_t ld_dy,
  * rounded once.  QM_ACT_SILU: act(g) = g / (1 + exp(-g)); QM_ACT_GELU:
  * act(g) = g / 2 * (1 + tanh(sqrt(2 / pi) * (g + 0.044715 g^3))).
  *   gate8, up8: both null, or what receives gate and up in 8 bits (as
- *   act_pack codes them) for the backward pass.
+ *   act_pack codes them) for the backward pass, which reads those alone.
  * gate, up and h: rows x cols, one dtype.  Errors: as act_pack. */
 typedef enum { QM_ACT_SILU = 0, QM_ACT_GELU = 1 } qm_act;
 QM_API qm_status gated_act_forward(const void *gate, int64_t ld_gate,
@@ -703,10 +705,10 @@ QM_API qm_status gated_act_backward(const qm_act8 *gate8, const qm_act8 *up8,
                                     int64_t ld_h, qm_stream_t stream);
 
 /* out[i] = scale * table[tokens[i]], rounded once; a token outside [0, vocab)
- * (padding) gives a row of zeros.  tokens: contiguous int32 or int64
- * (token_bits); fewer than 2^30 tokens and values.  Errors: QM_E_ARG, QM_E_ALIGN, QM_E_DTYPE,
- * QM_E_SHAPE, QM_E_UNSUPPORTED (more than 2^34 pieces of 4 or 8 columns),
- * QM_E_HIP. */
+ * (padding) gives a row of zeros, whatever the scale.  tokens: contiguous int32
+ * or int64 (token_bits); fewer than 2^30 tokens and values.  Errors: QM_E_ARG,
+ * QM_E_ALIGN, QM_E_DTYPE, QM_E_SHAPE, QM_E_UNSUPPORTED (2^34 pieces of 4 or 8
+ * columns, or more), QM_E_HIP. */
 QM_API qm_status embedding_lookup(const void *tokens, int32_t token_bits,
                                   int64_t n_tokens, const void *table,
                                   int32_t table_dtype, int64_t ld_table,
@@ -720,7 +722,9 @@ QM_API qm_status embedding_lookup(const void *tokens, int32_t token_bits,
  * part in it.
  *   ws: >= embedding_grad_workspace_bytes(n_tokens, vocab, cols) bytes,
  *   16-byte aligned.
- * Errors: as embedding_lookup, and QM_E_WORKSPACE. */
+ * Errors: as embedding_lookup, and QM_E_WORKSPACE; QM_E_UNSUPPORTED: a launch of
+ * 2^31 threads or more, which 2^27 tokens of up to 1024 columns and a vocabulary
+ * of 2^27 stay below. */
 QM_API size_t embedding_grad_workspace_bytes(int64_t n_tokens, int64_t vocab,
                                              int64_t cols);
 QM_API qm_status embedding_grad(const void *tokens, int32_t token_bits,

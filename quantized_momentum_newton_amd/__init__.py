@@ -879,8 +879,9 @@ def act_pack(x, ckpt=None, stream=None):
 
 
 def act_read(ckpt, out=None, dtype=torch.bfloat16, stream=None):
-    """The values an ActCheckpoint stands for (exact in fp32 and bf16), in
-    `out` or a new tensor of `dtype`."""
+    """The values an ActCheckpoint stands for (exact in fp32 and bf16; f16
+    numbers from 63488 on read as infinities in f16), in `out` or a new tensor of
+    `dtype`."""
     if not isinstance(ckpt, ActCheckpoint):
         raise TypeError("ckpt must be an ActCheckpoint")
     if out is None:
@@ -927,8 +928,8 @@ def weight_grad(dy, x, out, accumulate=False, ws=None, stream=None):
 
 def gated_act_forward(gate, up, gate_ckpt=None, up_ckpt=None, out=None, act="silu", keep=True, stream=None):
     """act(gate) * up (act: "silu" or "gelu", the tanh form) and, with keep,
-    gate and up in 8 bits for the backward pass: (h, gate_ckpt, up_ckpt), given
-    or new; the checkpoints are None without keep.  gate and up: rows x cols
+    gate and up in 8 bits for the backward pass, which reads those alone: (h,
+    gate_ckpt, up_ckpt), given or new; the checkpoints are None without keep.  gate and up: rows x cols
     with unit column stride, e.g. the two halves of one product."""
     pg, dt, ldg = _matrix(gate, "gate")
     shape, device = tuple(gate.shape), gate.device
