@@ -16,10 +16,11 @@
 // backward reads 2 bytes of g and u an element instead of 4.
 //
 // HBM bounds all of them (8192 x 14336 bf16, a large copy reaches 6.5 TB/s): pack
-// 56.2 us, 6.3 TB/s; read 57.6 us, 6.2; forward 158.5 us, 6.0; backward with h
-// 204 us, 5.8.  A layer's 8192 x 4096 runs at 5.4 to 5.6 TB/s, with a start and an
-// end of a few us each; rows at odd addresses (3001 x 6145 f16) at 4.2, each
-// access of a wave then touching one more line than it covers.
+// 56.5 us, 6.3 TB/s; read 57.8 us, 6.2; forward 158 us, 6.0 (gelu 160); backward
+// 160 us, 6.0 (163), with h 204 us, 5.8 (207).  A layer's 8192 x 4096 runs at 5.4
+// to 5.6 TB/s, with a start and an end of a few us each; rows at odd addresses
+// (3001 x 6145 f16) at 4.2, each access of a wave then touching one more line than
+// it covers; fp32 (4096 x 4096) forward 46 us, 5.9 TB/s, backward with h 63, 4.8.
 #include <algorithm>
 #include <type_traits>
 
@@ -82,8 +83,9 @@ template <int DT, bool LINES, bool WIDE> __global__ __launch_bounds__(kWaves * 6
 enum { kSilu = QM_ACT_SILU, kGelu = QM_ACT_GELU };
 
 // 1 / (1 + exp(-z)).  16-bit results: the hardware's exponential and
-// reciprocal, each within an ulp of fp32 (2^-23; a bf16 half step is 2^-9, an
-// f16 one 2^-12).
+// reciprocal, each within an ulp of fp32.  The exponential's argument is rounded,
+// which is worth |z| 2^-23 of its result and the larger part: at most 2^-16 before
+// s is 0 (a bf16 half step is 2^-8, an f16 one 2^-11).
 template <bool FAST> __device__ __forceinline__ float sigmoid(float z) {
     if constexpr (FAST) return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * z));
     else return 1.0f / (1.0f + expf(-z));
@@ -199,10 +201,16 @@ qm_status patch_grid(int64_t rows, int64_t cols, int &patches, int &across) {
     patches = (int)(across * ((rows + kGroupRows - 1) / kGroupRows));
     return QM_OK;
 }
-// Workgroups a CU, of those that fit, for the stream's sake (us, 8192 x 14336
-// bf16): pack 57.8 with all (6), 56.2 with 4; read 61.1 (8), 57.6 (3); forward
-// 159.4 (3), 158.5 (2), at 4096 columns 50.6, 48.8; backward 211.3 (4), 204.0
-// (2).  Less what the wide kernels use themselves.
+// Workgroups a CU, of those that fit, for the stream's sake, chosen on wide 16-bit
+// matrices (us, 8192 x 14336 bf16): pack 56.6 with 4, 66.7 with 3, 56.8 with all
+// (6); read 57.8 with 3, 60.6 with all (8); forward 158.1 with 2, 159.4 with 3, at
+// 4096 columns 49.1 and 50.7; backward 203.1 with 2, 211.2 with 4.  Other types and
+// shapes take the same: gelu on 8192 x 4096 f16 forward 51.6 with 2, 49.8 with 4,
+// 3001 x 6145 f16 36.1 and 34.1, backward within 2 %; 4096 x 4096 fp32 within 2 %
+// whatever the number.  What the wide kernels use themselves is taken off; the
+// narrow ones, which use none, hold as much (pack 5 a CU, forward 2): 65536 x 256
+// bf16 forward 30.0, with 4 26.8, backward 33.6 and 30.8, fp32 56.6 and 60.4;
+// 65536 x 500 f16 forward 117, with 8 85.
 constexpr unsigned kPackShare = wgs_per_cu(4) - (8u << 10), kReadShare = wgs_per_cu(3);
 constexpr unsigned kForwardShare = wgs_per_cu(2) - (16u << 10), kBackwardShare = wgs_per_cu(2);
 

@@ -8,15 +8,16 @@
 // of its tokens in that order.  Three launches:
 //
 //   sort   Each workgroup owns a range of the vocabulary (at most 1024
-//          values) and reads every token twice, which 256 workgroups do from
-//          their caches as fast as one does.  What lies below its range tells
+//          values) and looks at every token twice, which 256 workgroups do from
+//          their caches as fast as one does (up to 32768 tokens are read once
+//          and kept in registers).  What lies below its range tells
 //          it where its own part of the order starts, so no workgroup waits
 //          for another.  Counts are per wave and value: a wave owns a
 //          contiguous part of the tokens, so (value, wave, position) is the
 //          order, and the place of equal values among a wave's 64 comes from
-//          one ballot per bit of the value.
-//   sum    A wave takes the rows that start in a range of 16 positions of the
-//          order (per 1024 columns) and runs through their tokens, several rows
+//          one ballot per bit of the value, or per value where those are fewer.
+//   sum    A wave takes the rows that start in a range of up to 16 positions of
+//          the order (per 1024 columns) and runs through their tokens, several rows
 //          of dy in flight whichever row of the table they go to.  Rows of more
 //          than 32 tokens are cut where multiples of 32 positions lie: a cut
 //          part is summed by one wave into the workspace.  A gradient that is
@@ -24,11 +25,14 @@
 //          touched in rows that have tokens.
 //   join   The parts of a long row are added, in order, by one workgroup.
 //
-// 50257 x 2048 fp32 written whole from 32768 skewed tokens: sort 13 us, sum 105
-// (412 MB written, 134 read: 84 at the rate of a large copy), join 8; the sort is
-// bound by its instructions (256 workgroups look at every token), the sum by the
-// latency of start, order and rows in turn.  All zeros: 79 us, torch's fill 61.
-// Added to 32000 x 4096 bf16 from 16384 tokens: 10, 51 and 8 us.
+// 50257 x 2048 fp32 written whole from 32768 skewed tokens: sort 20 us, sum 104 to
+// 121 (412 MB written, 134 read: 84 at the rate of a large copy), join 9; the sort
+// is bound by its instructions (256 workgroups look at every token; 131072 tokens
+// of 64 columns 74 us, 32768 25, one value only 316 and 91: one workgroup then
+// places all), the sum by the latency of start, order and rows in turn.  No tokens:
+// 79 us, torch's fill 61.  Added to 32000 x 4096 bf16 from 16384 tokens: 13, 54 and
+// 9 us.  The lookup of 32768 such rows takes 60 us, 47 at the rate of a large copy
+// by the bytes that it moves.
 #include <algorithm>
 #include <type_traits>
 

@@ -21,14 +21,15 @@
 // round of the GPU are split over t; their parts go to the workspace and are added
 // in order by a second kernel.
 //
-// What bounds it: 14336 x 4096 over 8192 rows of kept input, 759 us (1267
-// TFLOP/s) written and 795 (1210) added to 235 MB; a bf16 product of 8192 cubed
-// by the library reaches 1220.  The same call on zeros takes 587 us: the rest is
-// the clock, which falls to 1.7 GHz under the load of real operands.  There the
-// matrix units are busy 60 % of the cycles, with LDS reads and writes dealt out
-// between the products (all of a slice's reads ahead of its products: 735 us on
-// zeros).  LDS has no bank conflicts and is active in a quarter of the cycles.
-// Products that leave a CU one 128 tile (1024 x 4096 over 8192 rows, 84 to 92 us) are
+// What bounds it: 14336 x 4096 over 8192 rows of kept input, 769 us (1251
+// TFLOP/s) written and 791 (1216) added to 235 MB; a bf16 product of 8192 cubed
+// by the library reaches 1385 over 100 launches, 1190 to 1270 over 20.  The same
+// call on zeros takes 586 us: the rest is the clock, which falls to 1.7 GHz under
+// the load of real operands.  There the matrix units are busy 66 % of the cycles,
+// with LDS reads and writes dealt out between the products (all of a slice's reads
+// ahead of its products: 735 us on zeros).  LDS has no bank conflicts and is
+// active in 36 % of the cycles.
+// Products that leave a CU one 128 tile (1024 x 4096 over 8192 rows, 81 to 89 us) are
 // bound by that tile's one wave a SIMD, which issues one thing at a time; where
 // there is more to issue than products and their reads, it has two (launch_kind).
 #include <math.h>
@@ -571,8 +572,10 @@ Cut cut_for(int b, int splits, int64_t rows, int64_t n, int64_t k) {
 
 // Expected microseconds of a cut, from measured steps: a 256 tile's step takes
 // 1.7 (kept input 1.55) with one workgroup a CU; a 128 tile's 0.6 alone on its
-// CU, 1.0 with a second one.  3 + 3 for the launch and what a tile starts and
-// ends with; parts are written and read at 5 TB/s, by a launch that costs 4.
+// CU, 1.0 with a second one, all on aligned panels.  3 + 3 for the launch and what
+// a tile starts and ends with; parts are written and read at 5 TB/s, by a launch
+// that costs 4.  Panels at odd addresses take up to 1.4 times as long in tiles of
+// 128 and 1.2 times in tiles of 256, which is not in the figure.
 double cost(const Cut &c, int steps, bool kept) {
     const double full = c.b == 256 ? (kept ? 1.55 : 1.7) : 1.0;
     const int slots = c.b == 256 ? kCus : 2 * kCus, parts = c.rest * c.splits;
@@ -583,13 +586,17 @@ double cost(const Cut &c, int steps, bool kept) {
     return us;
 }
 
-// The cut that should take least.  Measured, cut by cut (us; tile / parts):
-// 2048 x 1008 over 5001 rows 128/1 47, 128/2 39, 128/4 40, 256/6 47; 1024 x 4096
-// over 8192 128/1 84, 128/2 88, 256/4 87; 6144 x 2048 over 8192 128/1 217,
-// 256/1 234, from kept input 216 and 195; 1024 x 2048 over 65536 256/8 255,
-// 128/4 305; 256 x 256 over 16384 128/8 24, 128/24 18, 128/64 23; 1000 x 1000
-// over 300 128/1 9, 128/2 13.  Sides below 256 take tiles of 128: rows at any
-// address are read in tiles that both sides hold.
+// The cut that should take least.  Measured, cut by cut, and in brackets expected
+// (us added to fp32; tile / parts): 2048 x 1008 over 5001 rows 128/1 48 (53), 128/2
+// 40 (41), 128/4 43 (43), 256/6 47 (54); 1024 x 4096 over 8192 128/1 88 (83), 128/2
+// 87 (87), 256/4 88 (91), from kept input 84, 90 and 84; 1024 x 2048 over 65536
+// 256/8 250 (254), 128/4 306 (279); 256 x 256 over 16384 128/8 24 (30), 128/24 17
+// (19), 128/64 24 (19); 1000 x 1000 over 300 128/1 9 (9), 128/2 14 (15).  At odd
+// addresses 2047 x 1001 over 5001 128/2 51 (41), 128/4 51 (43), 256/8 51 (54).
+// Where it takes the slower one: 6144 x 2048 over 8192 128/1 231 (211), 256/1 204
+// (224), from kept input the right one, 237 (211) and 191 (204); at odd addresses
+// 4097 x 4351 over 3000 128/2 171 (124), 256/6 145 (124).  Sides below 256 take
+// tiles of 128: rows at any address are read in tiles that both sides hold.
 Cut choose_cut(int64_t rows, int64_t n, int64_t k, bool kept) {
     const int steps = (int)((rows + kStep - 1) / kStep);
     Cut best{};
