@@ -640,9 +640,10 @@ QM_API qm_status adamw_read_state(const void *host_plan, const void *dev_plan,
  * even, at most 448.  A value is off by at most 1/16 of itself, or by 2^-10 *
  * 2^e where it is below 2^-6 * 2^e, and exact in fp32 and bf16; magnitudes past
  * 448 * 2^119 = 2.98e38 become that.  A group that holds an infinity or a NaN
- * decodes to NaN as a whole.  Rows share a scale,
- * not columns: an activation's outliers keep to their columns, and a weight
- * gradient contracts over the rows. */
+ * decodes to NaN as a whole.  Scale bytes are 32 to 246; what others stand for
+ * is not defined, but that 0 beside zero bytes (cleared buffers) is 0.  Rows
+ * share a scale, not columns: an activation's outliers keep to their columns,
+ * and a weight gradient contracts over the rows. */
 typedef struct {
     uint8_t *data;       /* [rows * ld], 16-byte aligned                     */
     uint8_t *scale;      /* [ceil(rows / 32) * ld], 16-byte aligned          */
