@@ -315,9 +315,10 @@ template <int DT, int V, int P> struct Piece {
 };
 
 // Sums dy rows along the order: entries `from` .. `to` - 1 of a window of 64
-// whose positions lanes hold, several rows in flight whatever they belong to.  ends(w): whether a row of the table
-// ends with entry w; then old.load has its gradient under way with the entry's
-// own loads and leave(w, acc, old) takes the sum.
+// whose positions lanes hold, several rows in flight whatever they belong to.
+// ends(w): whether a row of the table ends with entry w; then old.load has its
+// gradient under way with the entry's own loads and leave(w, acc, old) takes the
+// sum.
 template <int DT, int V, int P, typename Old, typename Ends, typename Fetch, typename Leave>
 __device__ __forceinline__ void stream(const SumArgs &a, int pos, int from, int to, const Columns<V, P> &c, Ends ends,
                                        Fetch fetch, Leave leave) {
